@@ -81,7 +81,8 @@ typedef enum {
                               (an internal check, not expected; device status) */
 } spec_status_t;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype_t;
+/* SPEC_F16: the KV cache calls only (logits are fp32 or bf16). */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype_t;
 
 /* Largest supported draft length k of a chain call, and the largest tree
  * (N nodes, L path length) of a tree call. */
@@ -418,6 +419,166 @@ int spec_test_timeout_chain(const spec_chain_params *params, long long wait_cycl
                             void *workspace, size_t workspace_bytes, spec_stream_t stream);
 int spec_test_timeout_greedy(const spec_greedy_params *params, long long wait_cycles,
                              void *workspace, size_t workspace_bytes, spec_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit paged KV cache a verify step runs on: blocks taken and given
+ * back, the tree's ancestor masks, the quantising store, attention, and the
+ * relocation of accepted rows.  None of these calls uses a workspace or
+ * records a status; each says below how a request with bad lengths or block
+ * ids shows.
+ *
+ * A window is the run of tokens a step puts behind a request's committed
+ * prefix: seq_lens[b] is the prefix length (the cursor before the window is
+ * written), and token i of the window sits at logical position
+ * seq_lens[b] + i.  Arrays are padded to W tokens per request;
+ * window_lens [B] (NULL: every request has W) gives the real count w_b in
+ * [0, W].  Padded rows are neither read nor written.
+ * ---------------------------------------------------------------------- */
+
+/* Largest W of a call. */
+#define SPEC_MAX_WINDOW 65536
+
+/* Blocks for the windows of a step, block tables and slot maps.
+ *   block_tables [B, max_blocks] and blocks_held [B], updated in place: the
+ *     first blocks_held[b] entries of a row are the request's blocks.
+ *   free_blocks [num_blocks] with free_count [1]: a stack of free block ids,
+ *     free_blocks[free_count - 1] on top; free_count is updated in place,
+ *     free_blocks is not written.
+ * Request b needs max(0, ceil((seq_lens[b] + w_b) / tokens_per_block) -
+ * blocks_held[b]) more blocks.  They come off the stack in request order
+ * (request 0's first block is the top), up to the first request that the
+ * stack cannot serve: it and every later request that needs a block get
+ * none.
+ *   granted [B]: w_b, or -1 for a request that got none of the blocks it
+ *     needs or whose entries are out of range (seq_lens < 0, w_b outside
+ *     [0, W], blocks_held outside [0, max_blocks], or more than max_blocks
+ *     blocks in all): its row and count are left as they are.  free_count
+ *     outside [0, num_blocks] grants no block.
+ *   slots [B, W] or NULL: the pool row block * tokens_per_block + offset of
+ *     each window token; -1 where padded, not granted, or in a block whose
+ *     id lies outside [0, num_blocks).  num_blocks * tokens_per_block must
+ *     then be below 2^31. */
+int spec_reserve_blocks(const int32_t *seq_lens, const int32_t *window_lens, int W,
+                        int tokens_per_block, int B, int32_t *block_tables, int max_blocks,
+                        int32_t *blocks_held, const int32_t *free_blocks, int num_blocks,
+                        int32_t *free_count, int32_t *slots, int32_t *granted,
+                        spec_stream_t stream);
+
+/* Gives back the last counts[b] blocks of every request (the counts of
+ * spec_rollback_paged): they go on the free stack, their table entries read
+ * -1 and blocks_held drops.  The order on the stack is the one they came off
+ * in, so releasing what spec_reserve_blocks has just granted restores the
+ * stack.  A request whose count lies outside [0, blocks_held[b]] or whose
+ * blocks_held lies outside [0, max_blocks] gives back nothing; when the
+ * stack cannot hold what is given back (or free_count is out of range) the
+ * call changes nothing. */
+int spec_release_blocks(const int32_t *counts, int B, int32_t *block_tables, int max_blocks,
+                        int32_t *blocks_held, int32_t *free_blocks, int num_blocks,
+                        int32_t *free_count, spec_stream_t stream);
+
+/* Ancestor masks of a tree: bit m % 32 of masks[b, n, m / 32] is set when
+ * node m is node n itself or precedes it on a used path (paths as in
+ * spec_verify_tree; entries after a path's first -1 are ignored).  A node on
+ * no used path has an empty row; a request with a node id >= N on a used
+ * path has only empty rows (spec_verify_tree fails it closed).
+ *   paths [B, P, L], masks [B, N, ceil(N / 32)] int32. */
+int spec_tree_masks(const int32_t *paths, int B, int P, int L, int N, int32_t *masks,
+                    spec_stream_t stream);
+
+/* A paged KV cache in 8 bits (e4m3) with one scale per block of tokens, K or
+ * V, and head.
+ *   pool   [num_blocks, 2, kv_heads, tokens_per_block, head_dim] e4m3 bytes,
+ *          16-byte aligned (index 0 of the second axis: K, 1: V);
+ *   scales [num_blocks, 2, kv_heads] float32: an element is its e4m3 value
+ *          times the scale.  Scales are finite and >= 0; spec_store_kv makes
+ *          powers of two (0 for a block of zeros).
+ *   block_tables [B, max_blocks]: as for spec_relocate_accepted_kv.
+ * tokens_per_block is a multiple of 16 up to 1024, head_dim 64 or 128,
+ * kv_heads at most 1024.  Set size = sizeof(spec_kv_cache). */
+typedef struct spec_kv_cache {
+    size_t size;
+    void *pool;
+    float *scales;
+    const int32_t *block_tables;
+    int num_blocks, max_blocks, tokens_per_block, kv_heads, head_dim;
+} spec_kv_cache;
+
+/* Writes a window's K and V rows into the cache.
+ *   k, v  [B, W, kv_heads, head_dim] of `dtype` (SPEC_BF16 or SPEC_F16),
+ *         element (b, i, h, d) at b * strides[0] + i * strides[1] +
+ *         h * strides[2] + d (strides in elements, multiples of 8, bases
+ *         16-byte aligned), so slices of a fused projection need no copy.
+ * Storing appends: the rows of a block before the first one written stay
+ * live, everything behind the window is dead.  For each block, kind and head
+ * the scale becomes the least power of two s (at least 2^-126) with
+ * |x| <= 448 s for every finite new element x, or the block's old scale if
+ * it has live rows and its scale is larger; where a block with live rows
+ * gets a larger scale, their codes are rounded again, q' = rne(q old / new).
+ * A new element is stored as rne(x / s), rounded to the nearest e4m3 value,
+ * ties to even; an element that is not finite is stored as NaN.
+ * A request with seq_lens < 0, w_b outside [0, W], a window past max_blocks
+ * blocks, or a window block id outside [0, num_blocks) stores nothing.
+ * Blocks holding a window must not be shared between requests. */
+int spec_store_kv(const spec_kv_cache *cache, const void *k, const int64_t *k_strides,
+                  const void *v, const int64_t *v_strides, int dtype, const int32_t *seq_lens,
+                  const int32_t *window_lens, int B, int W, spec_stream_t stream);
+
+/* Attention of each window token over its request's cached prefix and the
+ * window (whose rows spec_store_kv has written).
+ *   q     [B, W, q_heads, head_dim] of `dtype` (SPEC_BF16 or SPEC_F16),
+ *         strided as in spec_store_kv; q_heads is a multiple of kv_heads and
+ *         head h reads KV head h / (q_heads / kv_heads).
+ *   masks [B, W, ceil(W / 32)] int32 or NULL (W <= SPEC_MAX_TREE_NODES):
+ *         window token i sees window token j when bit j % 32 of word j / 32
+ *         of its row is set (spec_tree_masks).  NULL: the chain, j <= i.
+ *         Every prefix position is seen.
+ *   out = sum_t p_t v_t with p = softmax over the seen positions t of
+ *   scale * q . k_t; lse = log sum exp of those scores (natural log).  A
+ *   token that sees nothing gets out = 0 and lse = -inf.  Positions that a
+ *   token does not see have no influence on it, whatever they hold (NaN and
+ *   infinities included).
+ *   out     [B, W, q_heads, head_dim] of `dtype`, dense.
+ *   out_lse [B, W, q_heads] float32 or NULL.
+ * The rows of a request with seq_lens < 0, w_b outside [0, W] (all W rows),
+ * a window past max_blocks blocks, or a block id outside [0, num_blocks)
+ * among those it reads are NaN.  Scores and sums are held in fp32; the
+ * weights p are rounded to fp16 (11 bits) relative to the row's largest
+ * before they meet V.
+ *   scratch: spec_attend_scratch_size(...) bytes, 256-byte aligned, used
+ *   during the call only; it need not be initialised and may hold anything,
+ *   but calls that overlap on the GPU must not share it, and it must not be
+ *   the workspace of a verify call.  Results do not depend on timing: equal
+ *   inputs give equal bits. */
+typedef struct spec_attend_params {
+    size_t size;
+    const void *q;
+    int64_t q_strides[3];
+    int dtype;
+    int B, W, q_heads;
+    const int32_t *seq_lens;
+    const int32_t *window_lens;  /* [B] or NULL */
+    const int32_t *masks;        /* or NULL */
+    float scale;                 /* finite */
+    void *out;
+    float *out_lse;              /* or NULL */
+} spec_attend_params;
+int spec_attend_kv(const spec_kv_cache *cache, const spec_attend_params *params, void *scratch,
+                   size_t scratch_bytes, spec_stream_t stream);
+
+/* Scratch of spec_attend_kv for B requests of W window tokens (0 for invalid
+ * sizes). */
+size_t spec_attend_scratch_size(int B, int W, int q_heads, int kv_heads, int head_dim);
+
+/* spec_relocate_accepted_kv for the 8-bit cache: for j = 1..n the K and V
+ * rows of node accepted_nodes[b][j] move to logical position base + j, with
+ * the same rules for which requests are left untouched.  A block written to
+ * gets, per kind and head, the largest scale among the rows that it
+ * receives, and its own old scale if rows before the first one written stay
+ * live (as in spec_store_kv); codes whose scale grows are rounded again.
+ * Rows past base + n are dead. */
+int spec_relocate_quantised_kv(const spec_kv_cache *cache, const int32_t *base_lens,
+                               const int32_t *accepted_nodes, const int32_t *num_accepted, int B,
+                               int L, spec_stream_t stream);
 
 /* Synchronise `stream`, read the workspace status word into *status_out
  * (SPEC_OK, SPEC_EBADINDEX or SPEC_ETIMEOUT) and clear it.  Returns SPEC_OK, SPEC_EINVAL or

@@ -14,6 +14,14 @@ Calls (same names as the C ABI):
                    "Eagle-2" section)
   rollback_lengths KV cursor rollback (TensorRT-LLM walkthrough,
                    update_requests / rewind_cache)
+
+The paged 8-bit KV cache a step runs on:
+  reserve_blocks / release_blocks  blocks for the windows, block tables and
+                   slot maps, and the blocks given back
+  tree_masks       ancestor masks of a tree's nodes, from its paths
+  store_kv         a window's K and V rows into the cache
+  attend_kv        attention of the window's rows over the cache
+  relocate_quantised_kv  the accepted nodes' rows behind the prefix
 """
 from __future__ import annotations
 
@@ -29,12 +37,13 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspecveri
 
 SPEC_OK, SPEC_EINVAL, SPEC_EBADINDEX, SPEC_ECUDA, SPEC_EWORKSPACE, SPEC_ETIMEOUT = 0, -1, -2, -3, -4, -5
 SPEC_ELIMIT = -6
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
 SPEC_MAX_DRAFT = 64
 SPEC_MAX_BATCH = 8192
 SPEC_MAX_TREE_NODES = 1024
 SPEC_MAX_PATH_LEN = 64
 SPEC_MAX_TOPK = 256
+SPEC_MAX_WINDOW = 65536
 
 # Every entry point the header declares.
 SYMBOLS = ("spec_workspace_size", "spec_workspace_init", "spec_verify_chain",
@@ -43,7 +52,8 @@ SYMBOLS = ("spec_workspace_size", "spec_workspace_init", "spec_verify_chain",
            "spec_relocate_accepted_kv", "spec_verify_chain_philox", "spec_philox_uniforms",
            "spec_verify_chain_ex", "spec_verify_greedy_ex", "spec_rollback_paged",
            "spec_workspace_size_filtered", "spec_test_timeout_chain", "spec_test_timeout_greedy",
-           "spec_verify_tree_sampled")
+           "spec_verify_tree_sampled", "spec_reserve_blocks", "spec_release_blocks", "spec_tree_masks",
+           "spec_store_kv", "spec_attend_kv", "spec_attend_scratch_size", "spec_relocate_quantised_kv")
 SPEC_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 class ChainParams(ctypes.Structure):
@@ -66,6 +76,23 @@ class GreedyParams(ctypes.Structure):
                 ("draft_lens", ctypes.c_void_p), ("B", ctypes.c_int), ("k", ctypes.c_int),
                 ("V", ctypes.c_int), ("out_tokens", ctypes.c_void_p),
                 ("out_num_accepted", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
+
+
+class KvCache(ctypes.Structure):
+    """spec_kv_cache (include/spec_verify.h), field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("pool", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("block_tables", ctypes.c_void_p), ("num_blocks", ctypes.c_int),
+                ("max_blocks", ctypes.c_int), ("tokens_per_block", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class AttendParams(ctypes.Structure):
+    """spec_attend_params (include/spec_verify.h), field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("q", ctypes.c_void_p), ("q_strides", ctypes.c_int64 * 3),
+                ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("W", ctypes.c_int),
+                ("q_heads", ctypes.c_int), ("seq_lens", ctypes.c_void_p),
+                ("window_lens", ctypes.c_void_p), ("masks", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("out", ctypes.c_void_p), ("out_lse", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -101,13 +128,24 @@ def _bind(lib):
     lib.spec_rollback_paged.argtypes = [P, P, P, I, P, I, I, P, P, P, P]
     lib.spec_test_timeout_chain.argtypes = [ctypes.POINTER(ChainParams), ctypes.c_longlong, P, S, P]
     lib.spec_test_timeout_greedy.argtypes = [ctypes.POINTER(GreedyParams), ctypes.c_longlong, P, S, P]
+    lib.spec_reserve_blocks.argtypes = [P, P, I, I, I, P, I, P, P, I, P, P, P, P]
+    lib.spec_release_blocks.argtypes = [P, I, P, I, P, P, I, P, P]
+    lib.spec_tree_masks.argtypes = [P, I, I, I, I, P, P]
+    S3 = ctypes.POINTER(ctypes.c_int64)
+    lib.spec_store_kv.argtypes = [ctypes.POINTER(KvCache), P, S3, P, S3, I, P, P, I, I, P]
+    lib.spec_attend_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(AttendParams), P, S, P]
+    lib.spec_attend_scratch_size.argtypes = [I, I, I, I, I]
+    lib.spec_attend_scratch_size.restype = S
+    lib.spec_relocate_quantised_kv.argtypes = [ctypes.POINTER(KvCache), P, P, P, I, I, P]
     lib.spec_status_string.argtypes = [I]
     lib.spec_status_string.restype = ctypes.c_char_p
     for f in ("spec_workspace_init", "spec_verify_chain", "spec_verify_greedy", "spec_verify_tree",
               "spec_rollback_lengths", "spec_last_error", "spec_verify_chain_noalloc",
               "spec_relocate_accepted_kv", "spec_verify_chain_philox", "spec_philox_uniforms",
               "spec_verify_chain_ex", "spec_verify_greedy_ex", "spec_rollback_paged",
-              "spec_test_timeout_chain", "spec_test_timeout_greedy", "spec_verify_tree_sampled"):
+              "spec_test_timeout_chain", "spec_test_timeout_greedy", "spec_verify_tree_sampled",
+              "spec_reserve_blocks", "spec_release_blocks", "spec_tree_masks", "spec_store_kv",
+              "spec_attend_kv", "spec_relocate_quantised_kv"):
         getattr(lib, f).restype = I
     return lib
 
@@ -500,6 +538,245 @@ def philox_uniforms(seeds, offsets, n: int, *, stream=None):
     if rc != SPEC_OK:
         raise SpecError("spec_philox_uniforms", rc)
     return out
+
+
+# ---------------------------------------------------------------- the paged 8-bit KV cache
+def _on_stream(stream, device):
+    """Handle of `stream` and a context in which what torch allocates belongs
+    to it (outputs and scratch made here are then safe to free and, while a
+    graph is captured, come from that graph's own memory)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "value", stream) or 0)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+
+
+def _distinct(**tensors):
+    """Arrays a call writes must not be the same memory as any other."""
+    seen = {}
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        p = t.data_ptr()
+        if p in seen:
+            raise ValueError(f"{name} and {seen[p]} are the same memory")
+        seen[p] = name
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype=None):
+    """A [B, W, heads, D] tensor whose rows along D are dense and 16-byte
+    aligned, and its first three strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16) or dtype not in (None, t.dtype):
+        raise ValueError(f"{name} must be {dtype or 'bfloat16 or float16'}, got {t.dtype}")
+    if t.dim() != 4 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape) if shape else '[B, W, heads, D]'}, got {tuple(t.shape)}")
+    # the stride of an axis of one element is never used
+    st = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+    if t.stride(3) != 1 or any(s % 8 for s in st[:3]) or t.data_ptr() % 16:
+        raise ValueError(f"{name} must be dense along D with 16-byte aligned rows (strides {tuple(t.stride())})")
+    return t, (ctypes.c_int64 * 3)(*st[:3])
+
+
+def _float_code(dtype) -> int:
+    return SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F16
+
+
+def _cache(kv_pool, kv_scales, block_tables):
+    """The spec_kv_cache of a pool [num_blocks, 2, Hkv, tokens_per_block, D]
+    (float8_e4m3fn or uint8), its scales [num_blocks, 2, Hkv] and the block
+    tables [B, max_blocks]."""
+    if not isinstance(kv_pool, torch.Tensor) or kv_pool.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise ValueError("kv_pool must be a float8_e4m3fn or uint8 tensor")
+    p = _dev(kv_pool, "kv_pool")
+    if p.dim() != 5 or p.shape[1] != 2:
+        raise ValueError("kv_pool must be [num_blocks, 2, Hkv, tokens_per_block, D]")
+    n, _, H, tpb, D = p.shape
+    if D not in (64, 128) or tpb % 16 or not 16 <= tpb <= 1024:
+        raise ValueError("kv_pool: D must be 64 or 128 and tokens_per_block a multiple of 16 up to 1024")
+    s = _dev(kv_scales, "kv_scales", torch.float32, (n, 2, H))
+    bt = _dev(block_tables, "block_tables", torch.int32)
+    if bt.dim() != 2:
+        raise ValueError("block_tables must be [B, max_blocks]")
+    _same_device(p.device, kv_scales=s, block_tables=bt)
+    return KvCache(ctypes.sizeof(KvCache), _ptr(p), _ptr(s), _ptr(bt), n, bt.shape[1], tpb, H, D), bt.shape[0]
+
+
+def _lens(seq_lens, window_lens, B, dev, name="seq_lens"):
+    s = _dev(seq_lens, name, torch.int32, (B,))
+    w = None if window_lens is None else _dev(window_lens, "window_lens", torch.int32, (B,))
+    _same_device(dev, **{name: s, "window_lens": w})
+    return s, w
+
+
+def reserve_blocks(seq_lens, block_tables, blocks_held, free_blocks, free_count, tokens_per_block: int,
+                   window: int, *, window_lens=None, want_slots=True, out_slots=None, out_granted=None,
+                   stream=None):
+    """Blocks for every request's window off the free stack; returns (slots
+    [B, window] or None, granted [B]).
+
+    block_tables [B, max_blocks], blocks_held [B] and free_count [1] are
+    updated in place; free_blocks [num_blocks] is the stack, its top at
+    free_count - 1.  granted is the window length (window_lens, or `window`),
+    -1 for a request left without the blocks it needs; slots are the pool
+    rows of the window's tokens, -1 where there is none."""
+    seq = _dev(seq_lens, "seq_lens", torch.int32)
+    dev, B = seq.device, seq.shape[0]
+    seq, win = _lens(seq, window_lens, B, dev)
+    bt = _dev(block_tables, "block_tables", torch.int32)
+    if bt.dim() != 2 or bt.shape[0] != B:
+        raise ValueError("block_tables must be [B, max_blocks]")
+    held = _dev(blocks_held, "blocks_held", torch.int32, (B,))
+    fb = _dev(free_blocks, "free_blocks", torch.int32)
+    fc = _dev(free_count, "free_count", torch.int32, (1,))
+    sh, on = _on_stream(stream, dev)
+    with _on(dev), on:
+        slots = _out(out_slots, "out_slots", (B, int(window)), torch.int32, dev) \
+            if want_slots or out_slots is not None else None
+        granted = _out(out_granted, "out_granted", (B,), torch.int32, dev)
+        _same_device(dev, block_tables=bt, blocks_held=held, free_blocks=fb, free_count=fc, out_slots=slots,
+                     out_granted=granted)
+        _distinct(seq_lens=seq, window_lens=win, block_tables=bt, blocks_held=held, free_blocks=fb,
+                  free_count=fc, out_slots=slots, out_granted=granted)
+        rc = lib().spec_reserve_blocks(_ptr(seq), _ptr(win), int(window), int(tokens_per_block), B, _ptr(bt),
+                                       bt.shape[1], _ptr(held), _ptr(fb), fb.numel(), _ptr(fc), _ptr(slots),
+                                       _ptr(granted), sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_reserve_blocks", rc)
+    return slots, granted
+
+
+def release_blocks(block_tables, blocks_held, counts, free_blocks, free_count, *, stream=None):
+    """Gives back the last counts[b] blocks of every request (rollback_paged's
+    free counts): block_tables, blocks_held, free_blocks and free_count are
+    updated in place."""
+    bt = _dev(block_tables, "block_tables", torch.int32)
+    if bt.dim() != 2:
+        raise ValueError("block_tables must be [B, max_blocks]")
+    dev, B = bt.device, bt.shape[0]
+    held = _dev(blocks_held, "blocks_held", torch.int32, (B,))
+    n = _dev(counts, "counts", torch.int32, (B,))
+    fb = _dev(free_blocks, "free_blocks", torch.int32)
+    fc = _dev(free_count, "free_count", torch.int32, (1,))
+    _same_device(dev, blocks_held=held, counts=n, free_blocks=fb, free_count=fc)
+    _distinct(block_tables=bt, blocks_held=held, counts=n, free_blocks=fb, free_count=fc)
+    sh, on = _on_stream(stream, dev)
+    with _on(dev), on:
+        rc = lib().spec_release_blocks(_ptr(n), B, _ptr(bt), bt.shape[1], _ptr(held), _ptr(fb), fb.numel(),
+                                       _ptr(fc), sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_release_blocks", rc)
+
+
+def tree_masks(paths, num_nodes: int, *, out=None, stream=None):
+    """[B, num_nodes, ceil(num_nodes / 32)] int32: the bits of each node's
+    ancestors and itself, from the paths [B, P, L] of verify_tree."""
+    p = _dev(paths, "paths", torch.int32)
+    if p.dim() != 3:
+        raise ValueError("paths must be [B, P, L]")
+    B, P, L = p.shape
+    sh, on = _on_stream(stream, p.device)
+    with _on(p.device), on:
+        m = _out(out, "out", (B, int(num_nodes), -(-int(num_nodes) // 32)), torch.int32, p.device)
+        _same_device(p.device, out=m)
+        rc = lib().spec_tree_masks(_ptr(p), B, P, L, int(num_nodes), _ptr(m), sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_tree_masks", rc)
+    return m
+
+
+def store_kv(k, v, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=None, stream=None):
+    """Writes a window's rows k, v [B, W, Hkv, D] (bfloat16 or float16, any
+    16-byte aligned strides) at logical positions seq_lens[b] + i of the
+    paged cache: kv_pool [num_blocks, 2, Hkv, tokens_per_block, D]
+    (float8_e4m3fn or uint8) and kv_scales [num_blocks, 2, Hkv] in place."""
+    cache, B = _cache(kv_pool, kv_scales, block_tables)
+    dev = kv_pool.device
+    k, ks = _rows(k, "k", None)
+    W = k.shape[1]
+    k, ks = _rows(k, "k", (B, W, cache.kv_heads, cache.head_dim))
+    v, vs = _rows(v, "v", k.shape, k.dtype)
+    seq, win = _lens(seq_lens, window_lens, B, dev)
+    _same_device(dev, k=k, v=v)
+    sh, on = _on_stream(stream, dev)
+    with _on(dev), on:
+        rc = lib().spec_store_kv(ctypes.byref(cache), _ptr(k), ks, _ptr(v), vs, _float_code(k.dtype), _ptr(seq),
+                                 _ptr(win), B, W, sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_store_kv", rc)
+
+
+def attend_kv(q, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=None, masks=None,
+              scale: float | None = None, out=None, out_lse=None, want_lse=False, scratch=None, stream=None):
+    """Attention of the window's rows q [B, W, Hq, D] (bfloat16 or float16)
+    over each request's cached prefix and its window; returns (out [B, W, Hq,
+    D], lse [B, W, Hq] float32 or None).
+
+    masks [B, W, ceil(W / 32)] int32 (tree_masks) replace the chain's j <= i
+    inside the window; scale defaults to D ** -0.5.  Rows behind a window's
+    end are left as they are in `out` and `out_lse` (zeros in tensors made
+    here).  scratch: a uint8 tensor of spec_attend_scratch_size bytes; made
+    for the call by default."""
+    cache, B = _cache(kv_pool, kv_scales, block_tables)
+    dev = kv_pool.device
+    q, qs = _rows(q, "q", None)
+    W, Hq, D = q.shape[1:]
+    if q.shape[0] != B or D != cache.head_dim or Hq % cache.kv_heads:
+        raise ValueError(f"q must be [{B}, W, a multiple of {cache.kv_heads}, {cache.head_dim}], got {tuple(q.shape)}")
+    seq, win = _lens(seq_lens, window_lens, B, dev)
+    m = None if masks is None else _dev(masks, "masks", torch.int32, (B, W, -(-W // 32)))
+    need = lib().spec_attend_scratch_size(B, W, Hq, cache.kv_heads, D)
+    if need == 0:
+        raise SpecError("spec_attend_scratch_size", SPEC_EINVAL)
+    sh, on = _on_stream(stream, dev)
+    with _on(dev), on:
+        make = torch.zeros if win is not None else torch.empty
+        o = make((B, W, Hq, D), dtype=q.dtype, device=dev) if out is None else _dev(out, "out", q.dtype, (B, W, Hq, D))
+        lse = None
+        if out_lse is not None:
+            lse = _dev(out_lse, "out_lse", torch.float32, (B, W, Hq))
+        elif want_lse:
+            lse = make((B, W, Hq), dtype=torch.float32, device=dev)
+        buf = torch.empty(need, dtype=torch.uint8, device=dev) if scratch is None else _dev(scratch, "scratch", torch.uint8)
+        _same_device(dev, q=q, masks=m, out=o, out_lse=lse, scratch=buf)
+        _distinct(q=q, kv_pool=kv_pool, masks=m, out=o, out_lse=lse, scratch=buf)
+        prm = AttendParams(ctypes.sizeof(AttendParams), _ptr(q), qs, _float_code(q.dtype), B, W, Hq, _ptr(seq),
+                           _ptr(win), _ptr(m), float(D ** -0.5 if scale is None else scale), _ptr(o), _ptr(lse))
+        rc = lib().spec_attend_kv(ctypes.byref(cache), ctypes.byref(prm), _ptr(buf), buf.numel(), sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_attend_kv", rc)
+    return o, lse
+
+
+def relocate_quantised_kv(kv_pool, kv_scales, block_tables, base_lens, accepted_nodes, num_accepted, *,
+                          stream=None):
+    """relocate_accepted_kv for the 8-bit cache, in place: the accepted nodes'
+    K and V rows move behind each request's prefix, their codes re-rounded
+    where a block's scale changes."""
+    cache, B = _cache(kv_pool, kv_scales, block_tables)
+    dev = kv_pool.device
+    base, _ = _lens(base_lens, None, B, dev, "base_lens")
+    nodes = _dev(accepted_nodes, "accepted_nodes", torch.int32)
+    if nodes.dim() != 2 or nodes.shape[0] != B:
+        raise ValueError("accepted_nodes must be [B, L]")
+    n = _dev(num_accepted, "num_accepted", torch.int32, (B,))
+    _same_device(dev, accepted_nodes=nodes, num_accepted=n)
+    sh, on = _on_stream(stream, dev)
+    with _on(dev), on:
+        rc = lib().spec_relocate_quantised_kv(ctypes.byref(cache), _ptr(base), _ptr(nodes), _ptr(n), B,
+                                              nodes.shape[1], sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_relocate_quantised_kv", rc)
+    return kv_pool
 
 
 def last_error(workspace: Workspace, stream=None) -> int:

@@ -1,0 +1,428 @@
+"""Attention over the paged 8-bit cache: oracle pins on the CPU, the CUDA
+call against the 64-bit oracle on the GPU.
+
+Error bound of one output element, from the steps of the computation (u =
+2^-24 is fp32's half step, eps(T) / 2 the output type's):
+  scores   a dot product of D exact products summed in fp32 in any order is
+           off by at most D u sum|q_d k_d|; the products with the two scales
+           and log2(e) and the subtraction of the maximum add a few u of the
+           score: delta = (D + 8) u spread in all, spread = scale sum|q_d k_d|
+  weights  exp2 within 2^-21, rounded to fp16: 2^-11; weights below fp16's
+           normal range (relative to the row's largest, scaled up by at least
+           2^8) are off by at most 2^-32
+  sums     over n keys in fp32: n u each for numerator and denominator
+so |out - exact| <= (2 delta + 2^-11 + 2^-20 + 2 n u) A + n 2^-32 vmax
+                    + eps(T) / 2 |out| + the type's least step,
+A = sum p |v| / sum p.  lse: delta + 2^-20 + n u + 4 u |lse|.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verification_row_gb300 as sv
+from oracle import kv
+from _kv import cache, random_paths, to_bf16, to_f16
+from test_kv_store import BAD_CACHES, _fake_cache
+
+U = 2.0 ** -24
+
+
+# ------------------------------------------------------------------ oracle pins (CPU)
+def test_oracle_matches_a_dense_softmax():
+    rng = np.random.default_rng(0)
+    H, G, D, tpb, seq, w = 2, 3, 64, 16, 21, 5
+    pool, scales, tables = cache(rng, np.array([seq + w]), H, D, tpb)
+    q = rng.normal(0, 1, (1, w, H * G, D))
+    r = kv.attend(q, pool, scales, tables, [seq])
+    x = torch.from_numpy((kv.decode(pool[tables[0, :2]]) * scales[tables[0, :2]][..., None, None]))
+    k, v = (x[:, i].permute(1, 0, 2, 3).reshape(H, -1, D)[:, :seq + w].repeat_interleave(G, 0) for i in (0, 1))
+    qt = torch.from_numpy(q[0]).transpose(0, 1)
+    see = torch.ones(w, seq + w, dtype=torch.bool).tril(seq)
+    want = torch.nn.functional.scaled_dot_product_attention(qt, k, v, attn_mask=see)
+    assert np.allclose(r["out"][0], want.transpose(0, 1).numpy(), rtol=1e-12, atol=1e-12)
+
+
+def test_oracle_empty_rows_and_chain_masks():
+    rng = np.random.default_rng(1)
+    pool, scales, tables = cache(rng, np.array([4]), 1, 64, 16)
+    q = rng.normal(0, 1, (1, 4, 1, 64))
+    chain = kv.tree_masks(np.arange(4, dtype=np.int32)[None, None], 4)
+    a, b = kv.attend(q, pool, scales, tables, [0]), kv.attend(q, pool, scales, tables, [0], masks=chain)
+    assert np.array_equal(a["out"], b["out"])
+    chain[0, 2] = 0
+    c = kv.attend(q, pool, scales, tables, [0], masks=chain)
+    assert (c["out"][0, 2] == 0).all() and c["lse"][0, 2, 0] == -np.inf and np.array_equal(c["out"][0, 3], a["out"][0, 3])
+
+
+def test_refusals_before_any_launch():
+    lib, f = sv.lib(), 16 * 1024
+    ok = dict(size=ctypes.sizeof(sv.AttendParams), q=f, q_strides=(ctypes.c_int64 * 3)(256, 128, 64), dtype=1, B=2, W=3,
+              q_heads=4, seq_lens=f, window_lens=None, masks=None, scale=0.125, out=f, out_lse=None)
+
+    def call(cache=None, scratch=f, nbytes=1 << 40, **o):
+        a = dict(ok, **o)
+        prm = sv.AttendParams(*[a[n] for n, _ in sv.AttendParams._fields_])
+        return lib.spec_attend_kv(ctypes.byref(cache or _fake_cache()), ctypes.byref(prm), scratch, nbytes, None)
+    for bad in BAD_CACHES:
+        assert call(cache=_fake_cache(**bad)) == sv.SPEC_EINVAL, bad
+    odd = (ctypes.c_int64 * 3)(256, 130, 64)
+    for bad in (dict(size=8), dict(q=None), dict(q=f + 8), dict(q_strides=odd), dict(dtype=0), dict(dtype=3), dict(B=0),
+                dict(B=8193), dict(W=0), dict(W=65537), dict(q_heads=3), dict(q_heads=0), dict(seq_lens=None),
+                dict(out=None), dict(out=f + 4), dict(scale=float("nan")), dict(scale=float("inf")),
+                dict(W=1025, masks=f)):
+        assert call(**bad) == sv.SPEC_EINVAL, bad
+    assert call(scratch=None) == call(scratch=f + 16) == call(nbytes=16) == sv.SPEC_EWORKSPACE
+    s = lib.spec_attend_scratch_size
+    assert s(2, 3, 4, 2, 64) > 0
+    assert s(0, 3, 4, 2, 64) == s(2, 0, 4, 2, 64) == s(2, 3, 3, 2, 64) == s(2, 3, 4, 2, 80) == 0
+    cpu = torch.zeros((1, 1, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        sv.attend_kv(cpu, torch.zeros((1, 2, 2, 16, 64), dtype=torch.uint8), torch.zeros((1, 2, 2)),
+                     torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+# ------------------------------------------------------------------ GPU parity
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def i32(a):
+    return dev(np.asarray(a, np.int32))
+
+
+def make_q(rng, shape, dt, amp=1.0):
+    q = (to_bf16 if dt == "bf16" else to_f16)(rng.normal(0, amp, shape))
+    return q, dev(q).to(torch.bfloat16 if dt == "bf16" else torch.float16)
+
+
+def check(out, lse, r, dt, D, rows, vmax):
+    """rows [B, W]: the rows a call writes."""
+    eps = 2.0 ** -8 if dt == "bf16" else 2.0 ** -11
+    got, want = out.double().cpu().numpy()[rows], r["out"][rows]
+    n, spread, amp = r["keys"][rows][..., None], r["spread"][rows][..., None], r["amp"][rows]
+    delta = (D + 8) * U * spread
+    tol = (2 * delta + 2.0 ** -11 + 2.0 ** -20 + 2 * n * U) * amp + n * 2.0 ** -32 * vmax + eps * np.abs(want) + 2.0 ** -25
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    fine = ~np.isnan(want)
+    bad = np.abs(got - want)[fine] > tol[fine]
+    assert not bad.any(), f"{bad.mean():.2%} of {bad.size} outside, worst {(np.abs(got - want)[fine] / tol[fine]).max():.3f}"
+    if lse is not None:
+        got, want = lse.double().cpu().numpy()[rows], r["lse"][rows]
+        assert np.array_equal(np.isneginf(got), np.isneginf(want)) and np.array_equal(np.isnan(got), np.isnan(want))
+        fine = np.isfinite(want)
+        tol = delta[..., 0] + 2.0 ** -20 + n[..., 0] * U + 4 * U * np.abs(np.where(fine, want, 0))
+        assert (np.abs(got - np.where(fine, want, 0))[fine] <= tol[fine]).all()
+
+
+def run_case(rng, seq, win, W, H, G, D, tpb, dt, masks=None, spread=1.0, amp=1.0, scale=None, edit=None):
+    seq, win = np.asarray(seq), np.asarray(win)
+    B = len(seq)
+    pool, scales, tables = cache(rng, seq + win, H, D, tpb, spread=spread)
+    if edit:
+        edit(pool, scales, tables)
+    q, dq = make_q(rng, (B, W, H * G, D), dt, amp)
+    r = kv.attend(q, pool, scales, tables, seq, win, masks, scale)
+    out = torch.full(dq.shape, 7.0, dtype=dq.dtype, device="cuda")
+    lse = torch.full(dq.shape[:3], 7.0, device="cuda")
+    sv.attend_kv(dq, dev(pool), dev(scales), i32(tables), i32(seq), window_lens=i32(win),
+                 masks=None if masks is None else i32(masks), scale=scale, out=out, out_lse=lse)
+    rows = np.arange(W)[None] < win[:, None]
+    live = [b for b in range(B) if win[b]]
+    x = kv.decode(pool)[:, 1] * scales[:, 1][..., None, None]
+    check(out, lse, r, dt, D, rows, np.nanmax(np.abs(np.where(np.isnan(x), 0, x))) if live else 0)
+    assert (out[dev(~rows)] == 7).all() and (lse[dev(~rows)] == 7).all()  # padded rows stay
+    return out, lse
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("G,tpb,seq", [(1, 16, [0]), (4, 16, [1]), (8, 16, [15, 16, 17]), (4, 32, [999]),
+                                       (16, 48, [63, 0, 130]), (5, 64, [127, 128, 129, 500]), (24, 16, [300, 31])])
+def test_single_token(D, dt, G, tpb, seq):
+    rng = np.random.default_rng(G * 100 + len(seq))
+    run_case(rng, seq, [1] * len(seq), 1, 2, G, D, tpb, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("W,H,G,D,tpb,dt,hi", [(2, 1, 1, 64, 16, "bf16", 40), (4, 2, 4, 128, 32, "bf16", 700),
+                                               (8, 2, 4, 128, 32, "f16", 300), (8, 1, 8, 64, 16, "bf16", 600),
+                                               (17, 2, 4, 128, 64, "bf16", 260), (33, 1, 8, 64, 128, "f16", 400),
+                                               (65, 2, 5, 128, 48, "bf16", 200), (130, 1, 3, 64, 16, "f16", 333)])
+def test_chain_windows(W, H, G, D, tpb, dt, hi):
+    rng = np.random.default_rng(W)
+    B = 5
+    seq = rng.integers(0, hi + 1, B)
+    win = rng.integers(0, W + 1, B)
+    seq[0], win[0], win[1] = 0, W, W
+    win[2] = 0
+    run_case(rng, seq, win, W, H, G, D, tpb, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("W,L,H,G,D,tpb,dt", [(8, 4, 1, 1, 64, 16, "bf16"), (12, 5, 2, 1, 128, 16, "f16"),
+                                              (60, 4, 2, 4, 128, 64, "bf16"), (64, 9, 1, 2, 64, 32, "f16"),
+                                              (100, 12, 2, 3, 128, 16, "bf16"), (300, 20, 1, 1, 64, 48, "f16")])
+def test_tree_windows(W, L, H, G, D, tpb, dt):
+    rng = np.random.default_rng(W + L)
+    seq = np.array([0, 37, 200])
+    paths = np.stack([random_paths(rng, W, W, L) for _ in seq])
+    paths[1, -W // 3:] = -1  # some nodes on no path: at an empty prefix their rows see nothing
+    paths[0, -W // 2:] = -1
+    masks = kv.tree_masks(paths, W)
+    run_case(rng, seq, [W, W, W - 1], W, H, G, D, tpb, dt, masks=masks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(2, 3), (8, 12)])
+def test_empty_rows(G, W):
+    rng = np.random.default_rng(9)
+    masks = np.zeros((2, W, 1), np.int32)
+    masks[:, 1] = 0b10
+    out, lse = run_case(rng, [0, 20], [W, W], W, 2, G, 64, 16, "bf16", masks=masks)
+    assert (out[0, 0] == 0).all() and torch.isneginf(lse[0, 0]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 2), (4, 4), (4, 40), (8, 40)])
+@pytest.mark.parametrize("kind", [0, 1])
+def test_nan_in_unseen_places(G, W, kind):
+    # NaN codes in a window row reach the tokens that see it and no others;
+    # rows past the end hold arbitrary bytes already
+    rng = np.random.default_rng(W + kind)
+    seq, H, D, tpb = [19, 0, 300], 2, 128, 16
+
+    def edit(pool, scales, tables):
+        for b, s in enumerate(seq):
+            t = s + W - 1
+            pool[tables[b, t // tpb], kind, 0, t % tpb, 5] = 0x7f
+            pool[tables[b, t // tpb], kind, 1, t % tpb, :] = 0xff
+    run_case(rng, seq, [W] * 3, W, H, G, D, tpb, "bf16", edit=edit)
+    masks = np.zeros((3, W, -(-W // 32)), np.int32)
+    masks[:, :, 0] = 1  # everybody sees token 0; token 1 of the window sees the NaN row
+    masks[:, 1, (W - 1) // 32] |= np.int32(np.uint32(1 << ((W - 1) % 32)).view(np.int32))
+    run_case(rng, seq, [W] * 3, W, H, G, D, tpb, "bf16", masks=masks, edit=edit)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
+def test_nan_in_the_prefix_reaches_every_row(G, W):
+    rng = np.random.default_rng(3)
+
+    def edit(pool, scales, tables):
+        pool[tables[0, 2], 1, 0, 7, 9] = 0x7f
+        pool[tables[1, 1], 0, 1, 3, 9] = 0xff
+    out, _ = run_case(rng, [70, 70], [W, W], W, 2, G, 64, 16, "f16", edit=edit)
+    assert torch.isnan(out[0, 0, 0, 9]) and torch.isnan(out[1, 0, G]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
+def test_bad_requests_read_nan_and_leave_the_others(G, W):
+    rng = np.random.default_rng(4)
+    seq, win = [100, 50, -1, 40, 3, 90], [W, W, W, W + 1, -1, W]
+    B, H, D, tpb = 6, 2, 64, 16
+    pool, scales, tables = cache(rng, np.full(B, 100 + W), H, D, tpb)
+    tables[1, 2] = len(pool)     # a block that does not exist
+    tables[5, (90 + W - 1) // tpb] = -1  # an unmapped block in the window
+    q, dq = make_q(rng, (B, W, H * G, D), "bf16")
+    out, lse = sv.attend_kv(dq, dev(pool), dev(scales), i32(tables), i32(seq), window_lens=i32(win), want_lse=True)
+    r = kv.attend(q, pool, scales, tables, seq, win)
+    assert all(torch.isnan(out[b]).all() and torch.isnan(lse[b]).all() for b in (1, 2, 3, 4, 5))
+    rows = np.zeros((B, W), bool)
+    rows[0] = True
+    check(out, lse, r, "bf16", D, rows, np.nanmax(np.abs(kv.decode(pool[:, 1]))) * scales[:, 1].max())
+    # a window past the table's end
+    o2, _ = sv.attend_kv(dq, dev(pool), dev(scales), i32(tables[:, :3]), i32([48 - W] + [60] * 5))
+    assert torch.isfinite(o2[0].float()).all() and torch.isnan(o2[1]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(2, 1), (4, 4), (4, 40)])
+def test_scales_and_levels(G, W):
+    rng = np.random.default_rng(6)
+    # blocks of very different scales, steep and flat scores, a negative scale, zero blocks
+    run_case(rng, [200, 333], [W, W], W, 2, G, 128, 16, "bf16", spread=6.0, amp=0.05)
+    run_case(rng, [200, 333], [W, W], W, 2, G, 64, 16, "f16", amp=30.0)
+    run_case(rng, [200, 333], [W, W], W, 2, G, 64, 32, "bf16", scale=-0.3)
+    run_case(rng, [200, 333], [W, W], W, 2, G, 64, 32, "bf16", scale=0.0)
+
+    def zero(pool, scales, tables):
+        pool[tables[0, 1]], scales[tables[0, 1]] = 0, 0
+        scales[tables[1]] *= np.float32(0.7)  # not a power of two
+    run_case(rng, [200, 333], [W, W], W, 2, G, 64, 16, "bf16", edit=zero)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(2, 1), (4, 16)])
+def test_many_light_keys_beside_a_heavy_one(G, W):
+    # one position holds about half of the mass, 20000 alike ones the rest:
+    # weights far below the largest still count
+    rng = np.random.default_rng(7)
+    H, D, tpb, T = 1, 64, 64, 20000 // 64 * 64
+
+    def edit(pool, scales, tables):
+        pool[tables[0]] = 0
+        pool[tables[0], 1] = kv.encode(rng.uniform(0.5, 1.5, pool[tables[0], 1].shape))
+        pool[tables[0, 0], 0, 0, 0] = kv.encode(1.0)
+        pool[tables[0, 0], 1, 0, 0] = kv.encode(-1.0)
+        scales[:] = 1
+    seq = T - W
+    pool, scales, tables = cache(rng, np.array([T]), H, D, tpb, extra_cols=0)
+    edit(pool, scales, tables)
+    q = to_bf16(np.full((1, W, G, D), np.log(2e4) / D))
+    r = kv.attend(q, pool, scales, tables, [seq], scale=1.0)
+    out, lse = sv.attend_kv(dev(q).to(torch.bfloat16), dev(pool), dev(scales), i32(tables), i32([seq]), scale=1.0,
+                            want_lse=True)
+    check(out, lse, r, "bf16", D, np.ones((1, W), bool), 1.5)
+
+
+@pytest.mark.gpu
+def test_strided_queries_and_defaults():
+    rng = np.random.default_rng(8)
+    B, W, H, G, D, tpb = 3, 4, 2, 2, 64, 16
+    seq = [40, 7, 90]
+    pool, scales, tables = cache(rng, np.array(seq) + W, H, D, tpb)
+    q, dq = make_q(rng, (B, W, H * G + 2 * H, D), "bf16")
+    r = kv.attend(q[:, :, :H * G], pool, scales, tables, seq)
+    a = [dev(pool).view(torch.float8_e4m3fn), dev(scales), i32(tables), i32(seq)]
+    for x in (dq[:, :, :H * G], dq[:, :, :H * G].transpose(1, 2).contiguous().transpose(1, 2)):
+        out, lse = sv.attend_kv(x, *a)
+        assert lse is None
+        check(out, None, r, "bf16", D, np.ones((B, W), bool), 100)
+    with pytest.raises(ValueError):
+        sv.attend_kv(dq[:, :, :H * G, ::2], *a)
+    with pytest.raises(ValueError):
+        sv.attend_kv(dq[:, :, :3], *a)
+    with pytest.raises(ValueError):
+        sv.attend_kv(dq[:2, :, :H * G], *a)
+    with pytest.raises(ValueError):
+        sv.attend_kv(dq[:, :, :H * G].contiguous(), *a, out=torch.empty((B, W, H * G, D), device="cuda"))
+    with pytest.raises(ValueError):
+        sv.attend_kv(dq[:, :, :H * G], *a, masks=torch.zeros((B, W), dtype=torch.int32, device="cuda"))
+    with pytest.raises(sv.SpecError):
+        sv.attend_kv(dq[:, :, :H * G], *a, scratch=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_streams_graphs_and_repeats():
+    # two captured graphs replayed on two streams at once, eager calls between
+    # them, and the same bits every time
+    rng = np.random.default_rng(10)
+    B, H, D, tpb = 6, 2, 128, 16
+    runs = []
+    for W, G in ((1, 4), (20, 8)):
+        seq = rng.integers(500, 1500, B)
+        pool, scales, tables = cache(rng, seq + W, H, D, tpb)
+        _, dq = make_q(rng, (B, W, H * G, D), "bf16")
+        args = [dq, dev(pool), dev(scales), i32(tables), i32(seq)]
+        want, want_lse = sv.attend_kv(*args, want_lse=True)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            sv.attend_kv(*args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got, got_lse = sv.attend_kv(*args, want_lse=True)
+        runs.append((args, want, want_lse, g, got, got_lse, side))
+    for _ in range(5):
+        for args, want, want_lse, g, got, got_lse, side in runs:
+            with torch.cuda.stream(side):
+                g.replay()
+            eager, _ = sv.attend_kv(*args, stream=runs[0][6])
+            other, _ = sv.attend_kv(*args, stream=side.cuda_stream)
+            torch.cuda.synchronize()
+            assert torch.equal(eager, want) and torch.equal(other, want)
+    for args, want, want_lse, g, got, got_lse, side in runs:
+        assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    # a pool of over 4 GB; the request's blocks lie at its two ends
+    H, D, tpb, W = 8, 128, 128, 4
+    n = (1 << 32) // (2 * H * tpb * D) + 200
+    rng = np.random.default_rng(11)
+    small, scales, tables = cache(rng, np.array([500 + W]), H, D, tpb, spare=0, extra_cols=0)
+    pool = torch.zeros((n, 2, H, tpb, D), dtype=torch.uint8, device="cuda")
+    at = np.array([0, n - 1, n - 2, n - 150])[:len(small)]
+    pool[torch.from_numpy(at).cuda()] = dev(small)
+    big_scales = torch.ones((n, 2, H), device="cuda")
+    big_scales[torch.from_numpy(at).cuda()] = dev(scales)
+    q, dq = make_q(rng, (1, W, H * 4, D), "bf16")
+    r = kv.attend(q, small, scales, tables, [500])
+    out, lse = sv.attend_kv(dq, pool, big_scales, i32(at[tables]), i32([500]), want_lse=True)
+    check(out, lse, r, "bf16", D, np.ones((1, W), bool), 500)
+    k, dk = make_q(rng, (1, W, H, D), "bf16")
+    sv.store_kv(dk, dk, pool, big_scales, i32(at[tables]), i32([500]))
+    want, want_s = kv.store(k, k, small, scales, tables, [500])
+    assert np.array_equal(pool[torch.from_numpy(at).cuda()].cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+def test_a_step_of_tree_decoding():
+    """The calls as a step makes them: blocks, rows, attention, verify,
+    relocation, rollback, blocks back; the next step's attention then reads
+    exactly the accepted tokens."""
+    import oracle
+    import workloads
+    rng = np.random.default_rng(12)
+    w = workloads.make("tree_b16_n60_l4_v151936_bf16", seed=3, B=4, V=4096)
+    B, N, L = w["B"], w["N"], w["L"]
+    H, G, D, tpb = 2, 4, 64, 16
+    seq = np.array([30, 0, 47, 100], np.int32)
+    pool0, scales0, _ = cache(rng, seq, H, D, tpb, spare=40)
+    n = len(pool0)
+    held = -(-seq // tpb)
+    order = rng.permutation(n)
+    tables = np.full((B, 12), -1, np.int32)
+    at = 0
+    for b in range(B):
+        tables[b, :held[b]] = order[at:at + held[b]]
+        at += held[b]
+    scales0[:] = np.exp2(rng.integers(-6, -3, scales0.shape))
+    pool0 &= 0x77  # no NaN codes
+    free = np.full(n, -1, np.int32)
+    free[:n - at] = order[at:]
+    d = dict(seq=i32(seq), tables=i32(tables), held=i32(held), free=i32(free), count=i32([n - at]))
+    pool, scales = dev(pool0), dev(scales0.astype(np.float32))
+    k, dk = make_q(rng, (B, N, H, D), "bf16")
+    v, dv = make_q(rng, (B, N, H, D), "bf16")
+    q, dq = make_q(rng, (B, N, H * G, D), "bf16")
+    # the step
+    slots, granted = sv.reserve_blocks(d["seq"], d["tables"], d["held"], d["free"], d["count"], tpb, N)
+    masks = sv.tree_masks(i32(w["paths"]), N)
+    sv.store_kv(dk, dv, pool, scales, d["tables"], d["seq"])
+    out, lse = sv.attend_kv(dq, pool, scales, d["tables"], d["seq"], masks=masks, want_lse=True)
+    logits = dev(w["target"].view(np.int16)).view(torch.bfloat16)
+    tok, acc, best, nodes = sv.verify_tree(logits, i32(w["tree_tokens"]), i32(w["paths"]))
+    sv.relocate_quantised_kv(pool, scales, d["tables"], d["seq"], nodes, acc)
+    new, _, spare = sv.rollback_paged(d["seq"], acc, N - 1, tpb, blocks_held=d["held"])
+    sv.release_blocks(d["tables"], d["held"], spare, d["free"], d["count"])
+    # the oracle's step
+    slots_o, granted_o, t_o, h_o, c_o = kv.reserve(seq, None, tables, held, free, n - at, tpb, N)
+    assert np.array_equal(slots.cpu().numpy(), slots_o) and (granted == N).all()
+    p_o, s_o = kv.store(k, v, pool0, scales0, t_o, seq)
+    m_o = kv.tree_masks(w["paths"].astype(np.int32), N)
+    r = kv.attend(q, p_o, s_o, t_o, seq, masks=m_o)
+    check(out, lse, r, "bf16", D, np.ones((B, N), bool), 100)
+    o = oracle.verify(w)
+    assert np.array_equal(nodes.cpu().numpy(), o["accepted_nodes"]) and (o["num_accepted"] > 0).any()
+    p_o, s_o = kv.relocate(p_o, s_o, t_o, seq, o["accepted_nodes"], o["num_accepted"])
+    assert np.array_equal(pool.cpu().numpy(), p_o) and np.array_equal(scales.cpu().numpy(), s_o)
+    len_o = seq + o["num_accepted"] + 1
+    give = np.maximum(0, h_o - -(-len_o // tpb))
+    t_o, h_o, f_o, c_o = kv.release(t_o, h_o, give, free, c_o)
+    assert np.array_equal(new.cpu().numpy(), len_o)
+    for got, want in ((d["tables"], t_o), (d["held"], h_o), (d["free"], f_o), (d["count"], [c_o])):
+        assert np.array_equal(got.cpu().numpy(), want)
+    # the next step: one more token behind the accepted rows
+    _, dq = make_q(rng, (B, 1, H * G, D), "bf16")
+    sv.reserve_blocks(new, d["tables"], d["held"], d["free"], d["count"], tpb, 1)
+    sv.store_kv(dk[:, :1], dv[:, :1], pool, scales, d["tables"], new)
+    out, lse = sv.attend_kv(dq, pool, scales, d["tables"], new, want_lse=True)
+    r = kv.attend(dq.double().cpu().numpy(), pool.cpu().numpy(), scales.cpu().numpy(), d["tables"].cpu().numpy(), len_o)
+    check(out, lse, r, "bf16", D, np.ones((B, 1), bool), 100)
