@@ -1,4 +1,5 @@
-// Arguments of the attention kernels over the 8-bit paged cache (internal).
+// Arguments and work division of the attention kernels over the 8-bit paged
+// cache (internal).
 #pragma once
 
 #include "kvcache.cuh"
@@ -17,13 +18,176 @@ struct AttendArgs {
   float scale_log2; // scale * log2(e)
   char* out;
   float* lse;
+  int mtiles;       // row tiles of a full window
+  int* desc;        // scratch: per CTA, where a unit begins that other CTAs end
+  float* part;      // scratch: two partial results per CTA
 };
 
-// A request's lengths; false when they are out of range.
-__device__ __forceinline__ bool attend_lens(const AttendArgs& a, int b, long* seq, int* w) {
-  *seq = a.seq[b];
-  *w = a.win ? a.win[b] : a.W;
-  return *seq >= 0 && *w >= 0 && *w <= a.W && *seq + *w <= (long)a.c.max_blocks * a.c.tpb;
+// Rows of one request and KV head are numbered r = i * G + g (window token i,
+// query head g of the group) and cut into tiles of ROWS; a "unit" is one such
+// tile of one (request, KV head).  Its keys are cut into tiles of KEYS.  The
+// key tiles of all units, in unit order, form one line that is cut into equal
+// shares, one per CTA, so a ragged batch keeps every SM equally busy and a
+// long prefix spreads over the whole GPU.  A unit whose tiles fall to several
+// CTAs is joined afterwards from the (max, sum, weighted V) of each.
+struct Unit {
+  int b, h, mt;
+  long seq;
+  int w;        // window length; -1: the request's lengths are out of range
+  int tiles;    // key tiles of the unit
+};
+
+template <int ROWS, int KEYS>
+struct Division {
+  static __device__ __forceinline__ void lens(const AttendArgs& a, int b, long* seq, int* w) {
+    *seq = a.seq[b];
+    *w = a.win ? a.win[b] : a.W;
+    if (*seq < 0 || *w < 0 || *w > a.W || *seq + *w > (long)a.c.max_blocks * a.c.tpb) *w = -1;
+  }
+  // Keys that some row of tile mt sees, at most (0: the tile has no rows).
+  static __device__ __forceinline__ long seen(const AttendArgs& a, long seq, int w, int mt) {
+    const long r0 = (long)mt * ROWS, rows = (long)w * a.G;
+    if (r0 >= rows) return 0;
+    if (a.masks) return seq + w;
+    const long last = r0 + ROWS < rows ? r0 + ROWS : rows;
+    return seq + (last - 1) / a.G + 1;
+  }
+  static __device__ __forceinline__ int tiles(const AttendArgs& a, long seq, int w, int mt) {
+    if (w < 0) return (long)mt * ROWS < (long)a.W * a.G ? 1 : 0;  // its rows are written all the same
+    return (int)((seen(a, seq, w, mt) + KEYS - 1) / KEYS);
+  }
+  static __device__ __forceinline__ long head_tiles(const AttendArgs& a, long seq, int w) {
+    long n = 0;
+    for (int mt = 0; mt < a.mtiles; ++mt) n += tiles(a, seq, w, mt);
+    return n;
+  }
+  // Moves u to the next unit that has tiles, if any.
+  static __device__ __forceinline__ bool next(const AttendArgs& a, Unit& u) {
+    for (;;) {
+      if (++u.mt == a.mtiles) {
+        u.mt = 0;
+        if (++u.h == a.c.H) {
+          u.h = 0;
+          if (++u.b == a.B) return false;
+          lens(a, u.b, &u.seq, &u.w);
+        }
+      }
+      u.tiles = tiles(a, u.seq, u.w, u.mt);
+      if (u.tiles > 0) return true;
+    }
+  }
+};
+
+// Share of CTA i of n over a line of `total` tiles, and the owner of a tile.
+__device__ __forceinline__ long share_begin(long total, int i, int n) { return total * i / n; }
+__device__ __forceinline__ int share_owner(long total, long tile, int n) {
+  return (int)(((tile + 1) * n - 1) / total);
 }
+
+// What a CTA of THREADS threads knows of the division: its share [t0, t1) of
+// the line, the unit that t0 falls into and the tile there.  False: nothing
+// to do.  sPre: THREADS + 1 words.  `least`: tiles below which a share is not
+// worth a CTA.
+template <int ROWS, int KEYS, int THREADS>
+__device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long* sPre, Unit& u,
+                                       long* t0, long* t1, long* unit0, long* total_out,
+                                       int* ctas_out) {
+  using Div = Division<ROWS, KEYS>;
+  __shared__ long long sWarp[THREADS / 32];
+  __shared__ int sFind[3];
+  __shared__ long long sUnit0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + THREADS - 1) / THREADS;
+  long long mine = 0;
+  for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+    long seq;
+    int w;
+    Div::lens(a, b, &seq, &w);
+    mine += Div::head_tiles(a, seq, w) * a.c.H;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(~0u, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) sWarp[warp] = incl;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) incl += sWarp[i];
+  sPre[tid] = incl - mine;
+  if (tid == THREADS - 1) sPre[THREADS] = incl;
+  __syncthreads();
+  const long total = sPre[THREADS];
+  const long most = total / least > 1 ? total / least : 1;
+  const int ctas = most < (long)gridDim.x ? (int)most : (int)gridDim.x;
+  if (total == 0 || (int)blockIdx.x >= ctas) return false;
+  *total_out = total;
+  *ctas_out = ctas;
+  *t0 = share_begin(total, blockIdx.x, ctas);
+  *t1 = share_begin(total, blockIdx.x + 1, ctas);
+  if (sPre[tid] <= *t0 && *t0 < sPre[tid + 1]) {  // one thread: its requests hold t0
+    long at = sPre[tid];
+    for (int b = tid * per;; ++b) {
+      long seq;
+      int w;
+      Div::lens(a, b, &seq, &w);
+      const long head = Div::head_tiles(a, seq, w);
+      if (*t0 < at + head * a.c.H) {
+        const int h = (int)((*t0 - at) / head);
+        at += h * head;
+        int mt = 0;
+        for (;; ++mt) {
+          const int n = Div::tiles(a, seq, w, mt);
+          if (*t0 < at + n) break;
+          at += n;
+        }
+        sFind[0] = b;
+        sFind[1] = h;
+        sFind[2] = mt;
+        sUnit0 = at;
+        break;
+      }
+      at += head * a.c.H;
+    }
+  }
+  __syncthreads();
+  u.b = sFind[0];
+  u.h = sFind[1];
+  u.mt = sFind[2];
+  *unit0 = sUnit0;
+  Div::lens(a, u.b, &u.seq, &u.w);
+  u.tiles = Div::tiles(a, u.seq, u.w, u.mt);
+  return true;
+}
+
+constexpr float kPBits = 8.f;    // weights are 2^(t - m + 8) ...
+constexpr float kLazy = 7.f;     // ... with m at most 7 below the row's largest t: below 2^15 in fp16
+
+// Partial result slots: floats of one (ROWS x D weighted V, then max and sum).
+template <int ROWS>
+__host__ __device__ constexpr size_t part_floats(int D) { return (size_t)ROWS * (D + 2); }
+
+// desc words per CTA: {request, head, row tile, last CTA of the unit}; -1: none.
+constexpr int kDescWords = 4;
+
+__device__ __forceinline__ uint32_t pack_out(float x, float y, __nv_bfloat16*) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_out(float x, float y, __half*) {
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// lse of a row from its maximum (log2 units) and sum (times 2^kPBits).
+__device__ __forceinline__ float row_lse(float M, float L) {
+  return L == 0.f ? -INFINITY : (M + log2f(L) - kPBits) * 0.69314718055994531f;
+}
+
+constexpr int kSms = 152;
+
+// attend_rows.cu: few rows per KV head.
+size_t attend_rows_scratch(int D);
+cudaError_t launch_attend_rows(AttendArgs& a, int dtype, void* scratch, cudaStream_t st);
 
 }  // namespace sv
