@@ -25,6 +25,7 @@ The paged 8-bit KV cache a step runs on:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -541,81 +542,97 @@ def philox_uniforms(seeds, offsets, n: int, *, stream=None):
 
 
 # ---------------------------------------------------------------- the paged 8-bit KV cache
-def _on_stream(stream, device):
-    """Handle of `stream` and a context in which what torch allocates belongs
-    to it (outputs and scratch made here are then safe to free and, while a
-    graph is captured, come from that graph's own memory)."""
+# These calls are a few microseconds of GPU work each, so their checks are kept
+# short: one combined test per tensor, spelled out only when it fails.
+_I32, _F32 = torch.int32, torch.float32
+_NOTHING = contextlib.nullcontext()
+
+
+def _on_stream(stream, dev):
+    """Handle of `stream` and a context that makes it and its device current
+    if they are not (so what torch allocates inside belongs to the stream and,
+    while a graph is captured, to that graph)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif not isinstance(stream, torch.cuda.Stream):
+        ctx = _NOTHING if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return torch._C._cuda_getCurrentRawStream(dev.index), ctx
+    if not isinstance(stream, torch.cuda.Stream):
         handle = int(getattr(stream, "value", stream) or 0)
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+def _at(t, name, dev, dtype, shape) -> int:
+    """Address of a dense tensor of this type and shape on this device."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or t.shape != shape
+            or not t.is_contiguous()):
+        _dev(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+    return t.data_ptr()
 
 
-def _distinct(**tensors):
-    """Arrays a call writes must not be the same memory as any other."""
-    seen = {}
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        p = t.data_ptr()
-        if p in seen:
-            raise ValueError(f"{name} and {seen[p]} are the same memory")
-        seen[p] = name
-
-
-def _rows(t: torch.Tensor, name: str, shape, dtype=None):
-    """A [B, W, heads, D] tensor whose rows along D are dense and 16-byte
-    aligned, and its first three strides."""
+def _cuda(t, name, dims) -> torch.device:
+    """Device of the CUDA tensor that sets where a call runs."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in (torch.bfloat16, torch.float16) or dtype not in (None, t.dtype):
-        raise ValueError(f"{name} must be {dtype or 'bfloat16 or float16'}, got {t.dtype}")
-    if t.dim() != 4 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must have shape {tuple(shape) if shape else '[B, W, heads, D]'}, got {tuple(t.shape)}")
+    if t.dim() != len(dims):
+        raise ValueError(f"{name} must be [{', '.join(dims)}]")
+    return t.device
+
+
+def _apart(*addresses):
+    """An array that a call writes must not be another of its arrays."""
+    real = [p for p in addresses if p]
+    if len(set(real)) != len(real):
+        raise ValueError("two of the call's arrays are the same memory")
+
+
+def _rows(t, name, dev, shape, dtype):
+    """Address and first three strides of a [B, W, heads, D] tensor whose rows
+    along D are dense and 16-byte aligned."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dtype is not dtype or (dtype is not torch.bfloat16 and dtype is not torch.float16):
+        raise ValueError(f"{name} must be bfloat16 or float16, all of one type, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    b, w, h, d = t.stride()
     # the stride of an axis of one element is never used
-    st = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
-    if t.stride(3) != 1 or any(s % 8 for s in st[:3]) or t.data_ptr() % 16:
+    if shape[0] == 1:
+        b = 0
+    if shape[1] == 1:
+        w = 0
+    if shape[2] == 1:
+        h = 0
+    p = t.data_ptr()
+    if d != 1 or (b | w | h) % 8 or p % 16:
         raise ValueError(f"{name} must be dense along D with 16-byte aligned rows (strides {tuple(t.stride())})")
-    return t, (ctypes.c_int64 * 3)(*st[:3])
+    return p, _Strides(b, w, h)
 
 
-def _float_code(dtype) -> int:
-    return SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F16
+_Strides = ctypes.c_int64 * 3
 
 
 def _cache(kv_pool, kv_scales, block_tables):
     """The spec_kv_cache of a pool [num_blocks, 2, Hkv, tokens_per_block, D]
     (float8_e4m3fn or uint8), its scales [num_blocks, 2, Hkv] and the block
-    tables [B, max_blocks]."""
-    if not isinstance(kv_pool, torch.Tensor) or kv_pool.dtype not in (torch.uint8, torch.float8_e4m3fn):
-        raise ValueError("kv_pool must be a float8_e4m3fn or uint8 tensor")
-    p = _dev(kv_pool, "kv_pool")
-    if p.dim() != 5 or p.shape[1] != 2:
-        raise ValueError("kv_pool must be [num_blocks, 2, Hkv, tokens_per_block, D]")
-    n, _, H, tpb, D = p.shape
+    tables [B, max_blocks]; also B and the device."""
+    dev = _cuda(kv_pool, "kv_pool", ("num_blocks", "2", "Hkv", "tokens_per_block", "D"))
+    n, two, H, tpb, D = kv_pool.shape
+    if kv_pool.dtype is not torch.uint8 and kv_pool.dtype is not torch.float8_e4m3fn:
+        raise ValueError(f"kv_pool must be float8_e4m3fn or uint8, got {kv_pool.dtype}")
+    if two != 2 or not kv_pool.is_contiguous():
+        raise ValueError("kv_pool must be a contiguous [num_blocks, 2, Hkv, tokens_per_block, D]")
     if D not in (64, 128) or tpb % 16 or not 16 <= tpb <= 1024:
         raise ValueError("kv_pool: D must be 64 or 128 and tokens_per_block a multiple of 16 up to 1024")
-    s = _dev(kv_scales, "kv_scales", torch.float32, (n, 2, H))
-    bt = _dev(block_tables, "block_tables", torch.int32)
-    if bt.dim() != 2:
-        raise ValueError("block_tables must be [B, max_blocks]")
-    _same_device(p.device, kv_scales=s, block_tables=bt)
-    return KvCache(ctypes.sizeof(KvCache), _ptr(p), _ptr(s), _ptr(bt), n, bt.shape[1], tpb, H, D), bt.shape[0]
+    _cuda(block_tables, "block_tables", ("B", "max_blocks"))
+    B, cols = block_tables.shape
+    return KvCache(_CACHE_BYTES, kv_pool.data_ptr(), _at(kv_scales, "kv_scales", dev, _F32, (n, 2, H)),
+                   _at(block_tables, "block_tables", dev, _I32, (B, cols)), n, cols, tpb, H, D), B, dev
 
 
-def _lens(seq_lens, window_lens, B, dev, name="seq_lens"):
-    s = _dev(seq_lens, name, torch.int32, (B,))
-    w = None if window_lens is None else _dev(window_lens, "window_lens", torch.int32, (B,))
-    _same_device(dev, **{name: s, "window_lens": w})
-    return s, w
+_CACHE_BYTES, _ATTEND_BYTES = ctypes.sizeof(KvCache), ctypes.sizeof(AttendParams)
 
 
 def reserve_blocks(seq_lens, block_tables, blocks_held, free_blocks, free_count, tokens_per_block: int,
@@ -629,27 +646,28 @@ def reserve_blocks(seq_lens, block_tables, blocks_held, free_blocks, free_count,
     free_count - 1.  granted is the window length (window_lens, or `window`),
     -1 for a request left without the blocks it needs; slots are the pool
     rows of the window's tokens, -1 where there is none."""
-    seq = _dev(seq_lens, "seq_lens", torch.int32)
-    dev, B = seq.device, seq.shape[0]
-    seq, win = _lens(seq, window_lens, B, dev)
-    bt = _dev(block_tables, "block_tables", torch.int32)
-    if bt.dim() != 2 or bt.shape[0] != B:
-        raise ValueError("block_tables must be [B, max_blocks]")
-    held = _dev(blocks_held, "blocks_held", torch.int32, (B,))
-    fb = _dev(free_blocks, "free_blocks", torch.int32)
-    fc = _dev(free_count, "free_count", torch.int32, (1,))
-    sh, on = _on_stream(stream, dev)
-    with _on(dev), on:
-        slots = _out(out_slots, "out_slots", (B, int(window)), torch.int32, dev) \
-            if want_slots or out_slots is not None else None
-        granted = _out(out_granted, "out_granted", (B,), torch.int32, dev)
-        _same_device(dev, block_tables=bt, blocks_held=held, free_blocks=fb, free_count=fc, out_slots=slots,
-                     out_granted=granted)
-        _distinct(seq_lens=seq, window_lens=win, block_tables=bt, blocks_held=held, free_blocks=fb,
-                  free_count=fc, out_slots=slots, out_granted=granted)
-        rc = lib().spec_reserve_blocks(_ptr(seq), _ptr(win), int(window), int(tokens_per_block), B, _ptr(bt),
-                                       bt.shape[1], _ptr(held), _ptr(fb), fb.numel(), _ptr(fc), _ptr(slots),
-                                       _ptr(granted), sh)
+    dev = _cuda(block_tables, "block_tables", ("B", "max_blocks"))
+    B, cols = block_tables.shape
+    W = int(window)
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        slots, granted = out_slots, out_granted
+        if slots is None and want_slots:
+            slots = torch.empty((B, W), dtype=_I32, device=dev)
+        if granted is None:
+            granted = torch.empty((B,), dtype=_I32, device=dev)
+        _cuda(free_blocks, "free_blocks", ("num_blocks",))
+        n = free_blocks.shape[0]
+        a = (_at(seq_lens, "seq_lens", dev, _I32, (B,)),
+             None if window_lens is None else _at(window_lens, "window_lens", dev, _I32, (B,)),
+             _at(block_tables, "block_tables", dev, _I32, (B, cols)),
+             _at(blocks_held, "blocks_held", dev, _I32, (B,)), _at(free_blocks, "free_blocks", dev, _I32, (n,)),
+             _at(free_count, "free_count", dev, _I32, (1,)),
+             None if slots is None else _at(slots, "out_slots", dev, _I32, (B, W)),
+             _at(granted, "out_granted", dev, _I32, (B,)))
+        _apart(*a)
+        rc = lib().spec_reserve_blocks(a[0], a[1], W, int(tokens_per_block), B, a[2], cols, a[3], a[4], n, a[5],
+                                       a[6], a[7], sh)
     if rc != SPEC_OK:
         raise SpecError("spec_reserve_blocks", rc)
     return slots, granted
@@ -659,20 +677,17 @@ def release_blocks(block_tables, blocks_held, counts, free_blocks, free_count, *
     """Gives back the last counts[b] blocks of every request (rollback_paged's
     free counts): block_tables, blocks_held, free_blocks and free_count are
     updated in place."""
-    bt = _dev(block_tables, "block_tables", torch.int32)
-    if bt.dim() != 2:
-        raise ValueError("block_tables must be [B, max_blocks]")
-    dev, B = bt.device, bt.shape[0]
-    held = _dev(blocks_held, "blocks_held", torch.int32, (B,))
-    n = _dev(counts, "counts", torch.int32, (B,))
-    fb = _dev(free_blocks, "free_blocks", torch.int32)
-    fc = _dev(free_count, "free_count", torch.int32, (1,))
-    _same_device(dev, blocks_held=held, counts=n, free_blocks=fb, free_count=fc)
-    _distinct(block_tables=bt, blocks_held=held, counts=n, free_blocks=fb, free_count=fc)
-    sh, on = _on_stream(stream, dev)
-    with _on(dev), on:
-        rc = lib().spec_release_blocks(_ptr(n), B, _ptr(bt), bt.shape[1], _ptr(held), _ptr(fb), fb.numel(),
-                                       _ptr(fc), sh)
+    dev = _cuda(block_tables, "block_tables", ("B", "max_blocks"))
+    B, cols = block_tables.shape
+    _cuda(free_blocks, "free_blocks", ("num_blocks",))
+    n = free_blocks.shape[0]
+    a = (_at(counts, "counts", dev, _I32, (B,)), _at(block_tables, "block_tables", dev, _I32, (B, cols)),
+         _at(blocks_held, "blocks_held", dev, _I32, (B,)), _at(free_blocks, "free_blocks", dev, _I32, (n,)),
+         _at(free_count, "free_count", dev, _I32, (1,)))
+    _apart(*a)
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        rc = lib().spec_release_blocks(a[0], B, a[1], cols, a[2], a[3], n, a[4], sh)
     if rc != SPEC_OK:
         raise SpecError("spec_release_blocks", rc)
 
@@ -680,18 +695,19 @@ def release_blocks(block_tables, blocks_held, counts, free_blocks, free_count, *
 def tree_masks(paths, num_nodes: int, *, out=None, stream=None):
     """[B, num_nodes, ceil(num_nodes / 32)] int32: the bits of each node's
     ancestors and itself, from the paths [B, P, L] of verify_tree."""
-    p = _dev(paths, "paths", torch.int32)
-    if p.dim() != 3:
-        raise ValueError("paths must be [B, P, L]")
-    B, P, L = p.shape
-    sh, on = _on_stream(stream, p.device)
-    with _on(p.device), on:
-        m = _out(out, "out", (B, int(num_nodes), -(-int(num_nodes) // 32)), torch.int32, p.device)
-        _same_device(p.device, out=m)
-        rc = lib().spec_tree_masks(_ptr(p), B, P, L, int(num_nodes), _ptr(m), sh)
+    dev = _cuda(paths, "paths", ("B", "P", "L"))
+    B, P, L = paths.shape
+    N = int(num_nodes)
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        if out is None:
+            out = torch.empty((B, N, -(-N // 32)), dtype=_I32, device=dev)
+        src, dst = _at(paths, "paths", dev, _I32, (B, P, L)), _at(out, "out", dev, _I32, (B, N, -(-N // 32)))
+        _apart(src, dst)
+        rc = lib().spec_tree_masks(src, B, P, L, N, dst, sh)
     if rc != SPEC_OK:
         raise SpecError("spec_tree_masks", rc)
-    return m
+    return out
 
 
 def store_kv(k, v, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=None, stream=None):
@@ -699,18 +715,17 @@ def store_kv(k, v, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=No
     16-byte aligned strides) at logical positions seq_lens[b] + i of the
     paged cache: kv_pool [num_blocks, 2, Hkv, tokens_per_block, D]
     (float8_e4m3fn or uint8) and kv_scales [num_blocks, 2, Hkv] in place."""
-    cache, B = _cache(kv_pool, kv_scales, block_tables)
-    dev = kv_pool.device
-    k, ks = _rows(k, "k", None)
-    W = k.shape[1]
-    k, ks = _rows(k, "k", (B, W, cache.kv_heads, cache.head_dim))
-    v, vs = _rows(v, "v", k.shape, k.dtype)
-    seq, win = _lens(seq_lens, window_lens, B, dev)
-    _same_device(dev, k=k, v=v)
-    sh, on = _on_stream(stream, dev)
-    with _on(dev), on:
-        rc = lib().spec_store_kv(ctypes.byref(cache), _ptr(k), ks, _ptr(v), vs, _float_code(k.dtype), _ptr(seq),
-                                 _ptr(win), B, W, sh)
+    cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
+    _cuda(k, "k", ("B", "W", "Hkv", "D"))
+    shape = (B, k.shape[1], cache.kv_heads, cache.head_dim)
+    kp, ks = _rows(k, "k", dev, shape, k.dtype)
+    vp, vs = _rows(v, "v", dev, shape, k.dtype)
+    seq = _at(seq_lens, "seq_lens", dev, _I32, (B,))
+    win = None if window_lens is None else _at(window_lens, "window_lens", dev, _I32, (B,))
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        rc = lib().spec_store_kv(cache, kp, ks, vp, vs, SPEC_BF16 if k.dtype is torch.bfloat16 else SPEC_F16, seq, win,
+                                 B, shape[1], sh)
     if rc != SPEC_OK:
         raise SpecError("spec_store_kv", rc)
 
@@ -726,35 +741,37 @@ def attend_kv(q, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=None
     end are left as they are in `out` and `out_lse` (zeros in tensors made
     here).  scratch: a uint8 tensor of spec_attend_scratch_size bytes; made
     for the call by default."""
-    cache, B = _cache(kv_pool, kv_scales, block_tables)
-    dev = kv_pool.device
-    q, qs = _rows(q, "q", None)
-    W, Hq, D = q.shape[1:]
-    if q.shape[0] != B or D != cache.head_dim or Hq % cache.kv_heads:
-        raise ValueError(f"q must be [{B}, W, a multiple of {cache.kv_heads}, {cache.head_dim}], got {tuple(q.shape)}")
-    seq, win = _lens(seq_lens, window_lens, B, dev)
-    m = None if masks is None else _dev(masks, "masks", torch.int32, (B, W, -(-W // 32)))
+    cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
+    _cuda(q, "q", ("B", "W", "Hq", "D"))
+    W, Hq, D = q.shape[1], q.shape[2], cache.head_dim
+    if Hq % cache.kv_heads:
+        raise ValueError(f"q must have a multiple of {cache.kv_heads} heads, got {Hq}")
+    qp, qs = _rows(q, "q", dev, (B, W, Hq, D), q.dtype)
+    seq = _at(seq_lens, "seq_lens", dev, _I32, (B,))
+    win = None if window_lens is None else _at(window_lens, "window_lens", dev, _I32, (B,))
+    mp = None if masks is None else _at(masks, "masks", dev, _I32, (B, W, -(-W // 32)))
     need = lib().spec_attend_scratch_size(B, W, Hq, cache.kv_heads, D)
     if need == 0:
         raise SpecError("spec_attend_scratch_size", SPEC_EINVAL)
-    sh, on = _on_stream(stream, dev)
-    with _on(dev), on:
-        make = torch.zeros if win is not None else torch.empty
-        o = make((B, W, Hq, D), dtype=q.dtype, device=dev) if out is None else _dev(out, "out", q.dtype, (B, W, Hq, D))
-        lse = None
-        if out_lse is not None:
-            lse = _dev(out_lse, "out_lse", torch.float32, (B, W, Hq))
-        elif want_lse:
-            lse = make((B, W, Hq), dtype=torch.float32, device=dev)
-        buf = torch.empty(need, dtype=torch.uint8, device=dev) if scratch is None else _dev(scratch, "scratch", torch.uint8)
-        _same_device(dev, q=q, masks=m, out=o, out_lse=lse, scratch=buf)
-        _distinct(q=q, kv_pool=kv_pool, masks=m, out=o, out_lse=lse, scratch=buf)
-        prm = AttendParams(ctypes.sizeof(AttendParams), _ptr(q), qs, _float_code(q.dtype), B, W, Hq, _ptr(seq),
-                           _ptr(win), _ptr(m), float(D ** -0.5 if scale is None else scale), _ptr(o), _ptr(lse))
-        rc = lib().spec_attend_kv(ctypes.byref(cache), ctypes.byref(prm), _ptr(buf), buf.numel(), sh)
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        make = torch.empty if win is None else torch.zeros
+        if out is None:
+            out = make((B, W, Hq, D), dtype=q.dtype, device=dev)
+        if out_lse is None and want_lse:
+            out_lse = make((B, W, Hq), dtype=_F32, device=dev)
+        if scratch is None:
+            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        op = _at(out, "out", dev, q.dtype, (B, W, Hq, D))
+        lp = None if out_lse is None else _at(out_lse, "out_lse", dev, _F32, (B, W, Hq))
+        sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
+        _apart(qp, cache.pool, mp, op, lp, sp)
+        prm = AttendParams(_ATTEND_BYTES, qp, qs, SPEC_BF16 if q.dtype is torch.bfloat16 else SPEC_F16, B, W, Hq, seq,
+                           win, mp, D ** -0.5 if scale is None else scale, op, lp)
+        rc = lib().spec_attend_kv(cache, prm, sp, scratch.numel(), sh)
     if rc != SPEC_OK:
         raise SpecError("spec_attend_kv", rc)
-    return o, lse
+    return out, out_lse
 
 
 def relocate_quantised_kv(kv_pool, kv_scales, block_tables, base_lens, accepted_nodes, num_accepted, *,
@@ -762,18 +779,15 @@ def relocate_quantised_kv(kv_pool, kv_scales, block_tables, base_lens, accepted_
     """relocate_accepted_kv for the 8-bit cache, in place: the accepted nodes'
     K and V rows move behind each request's prefix, their codes re-rounded
     where a block's scale changes."""
-    cache, B = _cache(kv_pool, kv_scales, block_tables)
-    dev = kv_pool.device
-    base, _ = _lens(base_lens, None, B, dev, "base_lens")
-    nodes = _dev(accepted_nodes, "accepted_nodes", torch.int32)
-    if nodes.dim() != 2 or nodes.shape[0] != B:
-        raise ValueError("accepted_nodes must be [B, L]")
-    n = _dev(num_accepted, "num_accepted", torch.int32, (B,))
-    _same_device(dev, accepted_nodes=nodes, num_accepted=n)
-    sh, on = _on_stream(stream, dev)
-    with _on(dev), on:
-        rc = lib().spec_relocate_quantised_kv(ctypes.byref(cache), _ptr(base), _ptr(nodes), _ptr(n), B,
-                                              nodes.shape[1], sh)
+    cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
+    _cuda(accepted_nodes, "accepted_nodes", ("B", "L"))
+    L = accepted_nodes.shape[1]
+    base = _at(base_lens, "base_lens", dev, _I32, (B,))
+    nodes = _at(accepted_nodes, "accepted_nodes", dev, _I32, (B, L))
+    n = _at(num_accepted, "num_accepted", dev, _I32, (B,))
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        rc = lib().spec_relocate_quantised_kv(cache, base, nodes, n, B, L, sh)
     if rc != SPEC_OK:
         raise SpecError("spec_relocate_quantised_kv", rc)
     return kv_pool
