@@ -4,6 +4,13 @@
 
 using namespace sv;
 
+namespace {
+
+// Rows per KV head up to which attend_rows.cu is taken.
+bool few_rows(long W, int G) { return W * G <= 32; }
+
+}  // namespace
+
 extern "C" {
 
 size_t spec_attend_scratch_size(int B, int W, int q_heads, int kv_heads, int head_dim) {
@@ -11,7 +18,8 @@ size_t spec_attend_scratch_size(int B, int W, int q_heads, int kv_heads, int hea
       kv_heads > 1024 || q_heads < 1 || q_heads > 16384 || q_heads % kv_heads != 0 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return attend_rows_scratch(head_dim);
+  return few_rows(W, q_heads / kv_heads) ? attend_rows_scratch(head_dim)
+                                         : attend_tiles_scratch(head_dim);
 }
 
 int spec_attend_kv(const spec_kv_cache* cache, const spec_attend_params* p, void* scratch,
@@ -43,8 +51,10 @@ int spec_attend_kv(const spec_kv_cache* cache, const spec_attend_params* p, void
   a.scale_log2 = (float)((double)p->scale * 1.4426950408889634073599246810019);
   a.out = static_cast<char*>(p->out);
   a.lse = p->out_lse;
-  return launch_attend_rows(a, p->dtype, scratch, (cudaStream_t)stream) == cudaSuccess ? SPEC_OK
-                                                                                       : SPEC_ECUDA;
+  const cudaError_t e = few_rows(a.W, a.G)
+                            ? launch_attend_rows(a, p->dtype, scratch, (cudaStream_t)stream)
+                            : launch_attend_tiles(a, p->dtype, scratch, (cudaStream_t)stream);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
 }  // extern "C"

@@ -184,10 +184,83 @@ __device__ __forceinline__ float row_lse(float M, float L) {
   return L == 0.f ? -INFINITY : (M + log2f(L) - kPBits) * 0.69314718055994531f;
 }
 
+// Joins the units that several CTAs worked on: CTA (i, y) serves rows
+// [16 y, 16 y + 16) of the unit that began in CTA i and did not end there.
+// The parts are read in CTA order, so the result does not depend on timing.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 16;
+
+template <class T, int D, int ROWS, int KEYS>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a) {
+  constexpr int NT = D / 8;  // elements per thread, 8 threads per row
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int first = blockIdx.x;
+  const int4 d = *reinterpret_cast<const int4*>(a.desc + first * kDescWords);
+  if (d.x < 0) return;
+  const int b = d.x, h = d.y, last = d.w;
+  const long r0 = (long)d.z * ROWS;
+  long seq;
+  int w;
+  Division<ROWS, KEYS>::lens(a, b, &seq, &w);
+  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 3), part = threadIdx.x & 7;
+  if (r >= (long)(w < 0 ? a.W : w) * a.G - r0) return;
+  float M = -INFINITY, L = 0.f, x[NT] = {};
+#pragma unroll 4
+  for (int i = first; i <= last; ++i) {
+    const float* p = a.part + (2 * (size_t)i + (i == first)) * part_floats<ROWS>(D);
+    const float pm = p[ROWS * D + r], pl = p[ROWS * D + ROWS + r];
+    float4 z[NT / 4];
+#pragma unroll
+    for (int j = 0; j < NT / 4; ++j)
+      z[j] = *reinterpret_cast<const float4*>(p + r * D + part * NT + 4 * j);
+    if (pm == -INFINITY && pl == 0.f) continue;
+    const float now = fmaxf(M, pm);
+    const float fo = M == now ? 1.f : ex2(M - now), fn = pm == now ? 1.f : ex2(pm - now);
+    M = now;
+    L = L * fo + pl * fn;
+#pragma unroll
+    for (int j = 0; j < NT / 4; ++j) {
+      x[4 * j] = x[4 * j] * fo + z[j].x * fn;
+      x[4 * j + 1] = x[4 * j + 1] * fo + z[j].y * fn;
+      x[4 * j + 2] = x[4 * j + 2] * fo + z[j].z * fn;
+      x[4 * j + 3] = x[4 * j + 3] * fo + z[j].w * fn;
+    }
+  }
+  const int i = (int)((r0 + r) / a.G), head = h * a.G + (int)((r0 + r) % a.G);
+  const size_t orow = ((size_t)b * a.W + i) * a.Hq + head;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint32_t y[NT / 2];
+#pragma unroll
+  for (int j = 0; j < NT; j += 2) y[j / 2] = pack_out(x[j] * inv, x[j + 1] * inv, (T*)nullptr);
+  uint4* dst = reinterpret_cast<uint4*>(a.out + 2 * (orow * D + part * NT));
+#pragma unroll
+  for (int j = 0; j < NT / 8; ++j)
+    dst[j] = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+  if (a.lse && part == 0) a.lse[orow] = row_lse(M, L);
+}
+
+template <class T, int D, int ROWS, int KEYS>
+cudaError_t launch_join(const AttendArgs& a, int ctas, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, ROWS / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, ROWS, KEYS>, a);
+}
+
 constexpr int kSms = 152;
 
 // attend_rows.cu: few rows per KV head.
 size_t attend_rows_scratch(int D);
 cudaError_t launch_attend_rows(AttendArgs& a, int dtype, void* scratch, cudaStream_t st);
+// attend_tiles.cu: many rows per KV head.
+size_t attend_tiles_scratch(int D);
+cudaError_t launch_attend_tiles(AttendArgs& a, int dtype, void* scratch, cudaStream_t st);
 
 }  // namespace sv

@@ -472,57 +472,6 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
   }
 }
 
-// Joins a unit that several CTAs worked on: CTA i of this grid serves the
-// unit that began in CTA i and did not end there.
-template <class T, int D>
-__global__ void __launch_bounds__(kRThreads) attend_rows_join(const AttendArgs a) {
-  constexpr int NT = D / 8;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int first = blockIdx.x;
-  const int4 d = *reinterpret_cast<const int4*>(a.desc + first * kDescWords);
-  if (d.x < 0) return;
-  const int b = d.x, h = d.y, r0 = d.z * kRows, last = d.w;
-  long seq;
-  int w;
-  Div::lens(a, b, &seq, &w);
-  const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
-  if (r >= (long)(w < 0 ? a.W : w) * a.G - r0) return;
-  float M = -INFINITY, L = 0.f, x[NT] = {};
-#pragma unroll 4
-  for (int i = first; i <= last; ++i) {
-    const float* p = a.part + (2 * (size_t)i + (i == first)) * part_floats<kRows>(D);
-    const float pm = p[kRows * D + r], pl = p[kRows * D + kRows + r];
-    float4 z[NT / 4];
-#pragma unroll
-    for (int j = 0; j < NT / 4; ++j)
-      z[j] = *reinterpret_cast<const float4*>(p + r * D + part * NT + 4 * j);
-    if (pm == -INFINITY && pl == 0.f) continue;
-    const float now = fmaxf(M, pm);
-    const float fo = M == now ? 1.f : ex2(M - now), fn = pm == now ? 1.f : ex2(pm - now);
-    M = now;
-    L = L * fo + pl * fn;
-#pragma unroll
-    for (int j = 0; j < NT / 4; ++j) {
-      x[4 * j] = x[4 * j] * fo + z[j].x * fn;
-      x[4 * j + 1] = x[4 * j + 1] * fo + z[j].y * fn;
-      x[4 * j + 2] = x[4 * j + 2] * fo + z[j].z * fn;
-      x[4 * j + 3] = x[4 * j + 3] * fo + z[j].w * fn;
-    }
-  }
-  const int i = (r0 + r) / a.G, head = h * a.G + (r0 + r) % a.G;
-  const size_t orow = ((size_t)b * a.W + i) * a.Hq + head;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint32_t y[NT / 2];
-#pragma unroll
-  for (int j = 0; j < NT; j += 2) y[j / 2] = pack_out(x[j] * inv, x[j + 1] * inv, (T*)nullptr);
-  uint4* dst = reinterpret_cast<uint4*>(a.out + 2 * (orow * D + part * NT));
-#pragma unroll
-  for (int j = 0; j < NT / 8; ++j)
-    dst[j] = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-  if (a.lse && part == 0) a.lse[orow] = row_lse(M, L);
-}
-
 }  // namespace
 
 size_t attend_rows_scratch(int D) {
@@ -549,8 +498,7 @@ cudaError_t launch_rows(const AttendArgs& a, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attend_rows_join<T, D>, a);
+  return launch_join<T, D, kRows, kKeys>(a, kCtas, st);
 }
 
 }  // namespace
