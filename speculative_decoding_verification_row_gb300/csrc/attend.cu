@@ -30,7 +30,8 @@ int spec_attend_kv(const spec_kv_cache* cache, const spec_attend_params* p, void
   if (!p || p->size != sizeof(spec_attend_params) || !kv_strides_ok(p->q, p->q_strides) ||
       (p->dtype != SPEC_BF16 && p->dtype != SPEC_F16) || !p->seq_lens || !p->out ||
       reinterpret_cast<uintptr_t>(p->out) % 16 != 0 || !isfinite(p->scale) ||
-      (p->masks && p->W > SPEC_MAX_TREE_NODES))
+      (p->masks && p->W > SPEC_MAX_TREE_NODES) ||
+      (long)a.c.max_blocks * a.c.tpb > kMaxPositions)
     return SPEC_EINVAL;
   const size_t need = spec_attend_scratch_size(p->B, p->W, p->q_heads, a.c.H, a.c.D);
   if (need == 0) return SPEC_EINVAL;
@@ -48,6 +49,7 @@ int spec_attend_kv(const spec_kv_cache* cache, const spec_attend_params* p, void
   a.win = p->window_lens;
   a.masks = p->masks;
   a.words = (p->W + 31) / 32;
+  a.tpb16_div = (unsigned)((1ull << 32) / (a.c.tpb / 16) + ((1ull << 32) % (a.c.tpb / 16) != 0));
   a.scale_log2 = (float)((double)p->scale * 1.4426950408889634073599246810019);
   a.out = static_cast<char*>(p->out);
   a.lse = p->out_lse;

@@ -19,58 +19,60 @@ struct AttendArgs {
   char* out;
   float* lse;
   int mtiles;       // row tiles of a full window
+  unsigned tpb16_div;  // x / (tpb / 16) = umulhi(x, tpb16_div) for x < 2^26, tpb > 16
   int* desc;        // scratch: per CTA, where a unit begins that other CTAs end
   float* part;      // scratch: two partial results per CTA
 };
 
+// Block table column of 16-key group x.  ceil(2^32 / d) * d - 2^32 < d <= 64, so
+// the quotient is exact for x < 2^26, the limit of kMaxPositions.
+__device__ __forceinline__ unsigned col16(const AttendArgs& a, unsigned x) {
+  return a.c.tpb == 16 ? x : __umulhi(x, a.tpb16_div);
+}
+constexpr long kMaxPositions = 1l << 30;
+
 // Rows of one request and KV head are numbered r = i * G + g (window token i,
 // query head g of the group) and cut into tiles of ROWS; a "unit" is one such
 // tile of one (request, KV head).  Its keys are cut into tiles of KEYS.  The
-// key tiles of all units, in unit order, form one line that is cut into equal
-// shares, one per CTA, so a ragged batch keeps every SM equally busy and a
-// long prefix spreads over the whole GPU.  A unit whose tiles fall to several
-// CTAs is joined afterwards from the (max, sum, weighted V) of each.
+// key tiles of all units, ordered by request, row tile and head, form one
+// line that is cut into equal shares, one per CTA, so a ragged batch keeps
+// every SM equally busy and a long prefix spreads over the whole GPU.  A unit
+// whose tiles fall to several CTAs is joined afterwards from the (max, sum,
+// weighted V) of each.
 struct Unit {
   int b, h, mt;
-  long seq;
+  int seq;
   int w;        // window length; -1: the request's lengths are out of range
   int tiles;    // key tiles of the unit
 };
 
 template <int ROWS, int KEYS>
 struct Division {
-  static __device__ __forceinline__ void lens(const AttendArgs& a, int b, long* seq, int* w) {
+  static __device__ __forceinline__ void lens(const AttendArgs& a, int b, int* seq, int* w) {
     *seq = a.seq[b];
     *w = a.win ? a.win[b] : a.W;
-    if (*seq < 0 || *w < 0 || *w > a.W || *seq + *w > (long)a.c.max_blocks * a.c.tpb) *w = -1;
+    if (*seq < 0 || *w < 0 || *w > a.W || (long)*seq + *w > (long)a.c.max_blocks * a.c.tpb) *w = -1;
   }
   // Keys that some row of tile mt sees, at most (0: the tile has no rows).
-  static __device__ __forceinline__ long seen(const AttendArgs& a, long seq, int w, int mt) {
-    const long r0 = (long)mt * ROWS, rows = (long)w * a.G;
+  static __device__ __forceinline__ unsigned seen(const AttendArgs& a, int seq, int w, int mt) {
+    const int r0 = mt * ROWS, rows = w * a.G;  // at most 2^30: 65536 tokens, 16384 heads
     if (r0 >= rows) return 0;
-    if (a.masks) return seq + w;
-    const long last = r0 + ROWS < rows ? r0 + ROWS : rows;
-    return seq + (last - 1) / a.G + 1;
+    if (a.masks) return (unsigned)seq + w;
+    return (unsigned)seq + (unsigned)(min(r0 + ROWS, rows) - 1) / (unsigned)a.G + 1;
   }
-  static __device__ __forceinline__ int tiles(const AttendArgs& a, long seq, int w, int mt) {
-    if (w < 0) return (long)mt * ROWS < (long)a.W * a.G ? 1 : 0;  // its rows are written all the same
+  static __device__ __forceinline__ int tiles(const AttendArgs& a, int seq, int w, int mt) {
+    if (w < 0) return mt * ROWS < a.W * a.G ? 1 : 0;  // its rows are written all the same
     return (int)((seen(a, seq, w, mt) + KEYS - 1) / KEYS);
-  }
-  static __device__ __forceinline__ long head_tiles(const AttendArgs& a, long seq, int w) {
-    long n = 0;
-    for (int mt = 0; mt < a.mtiles; ++mt) n += tiles(a, seq, w, mt);
-    return n;
   }
   // Moves u to the next unit that has tiles, if any.
   static __device__ __forceinline__ bool next(const AttendArgs& a, Unit& u) {
+    if (++u.h < a.c.H) return true;
+    u.h = 0;
     for (;;) {
       if (++u.mt == a.mtiles) {
         u.mt = 0;
-        if (++u.h == a.c.H) {
-          u.h = 0;
-          if (++u.b == a.B) return false;
-          lens(a, u.b, &u.seq, &u.w);
-        }
+        if (++u.b == a.B) return false;
+        lens(a, u.b, &u.seq, &u.w);
       }
       u.tiles = tiles(a, u.seq, u.w, u.mt);
       if (u.tiles > 0) return true;
@@ -85,9 +87,10 @@ __device__ __forceinline__ int share_owner(long total, long tile, int n) {
 }
 
 // What a CTA of THREADS threads knows of the division: its share [t0, t1) of
-// the line, the unit that t0 falls into and the tile there.  False: nothing
-// to do.  sPre: THREADS + 1 words.  `least`: tiles below which a share is not
-// worth a CTA.
+// the line, the unit that t0 falls into and where that unit begins.  False:
+// nothing to do.  sPre: THREADS + 1 words.  `least`: tiles below which a
+// share is not worth a CTA.  Every CTA sums the line anew, (request, row tile)
+// pairs over its threads: no state between launches and none to clear.
 template <int ROWS, int KEYS, int THREADS>
 __device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long* sPre, Unit& u,
                                        long* t0, long* t1, long* unit0, long* total_out,
@@ -97,14 +100,20 @@ __device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long
   __shared__ int sFind[3];
   __shared__ long long sUnit0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.B + THREADS - 1) / THREADS;
+  const long items = (long)a.B * a.mtiles, per = (items + THREADS - 1) / THREADS;
+  const long x0 = min(items, tid * per), x1 = min(items, x0 + per);
+  // calls f(b, mt, tiles) for this thread's pairs until f returns false
+  auto walk = [&](auto f) {
+    int b = (int)(x0 / a.mtiles), mt = (int)(x0 % a.mtiles), seq = 0, w = 0;
+    for (long x = x0; x < x1; ++x) {
+      if (x == x0 || mt == 0) Div::lens(a, b, &seq, &w);
+      if (!f(b, mt, Div::tiles(a, seq, w, mt))) return;
+      if (++mt == a.mtiles) mt = 0, ++b;
+    }
+  };
   long long mine = 0;
-  for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-    long seq;
-    int w;
-    Div::lens(a, b, &seq, &w);
-    mine += Div::head_tiles(a, seq, w) * a.c.H;
-  }
+  walk([&](int, int, int n) { return mine += n, true; });
+  mine *= a.c.H;
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -125,30 +134,17 @@ __device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long
   *ctas_out = ctas;
   *t0 = share_begin(total, blockIdx.x, ctas);
   *t1 = share_begin(total, blockIdx.x + 1, ctas);
-  if (sPre[tid] <= *t0 && *t0 < sPre[tid + 1]) {  // one thread: its requests hold t0
+  if (sPre[tid] <= *t0 && *t0 < sPre[tid + 1]) {  // one thread: its pairs hold t0
     long at = sPre[tid];
-    for (int b = tid * per;; ++b) {
-      long seq;
-      int w;
-      Div::lens(a, b, &seq, &w);
-      const long head = Div::head_tiles(a, seq, w);
-      if (*t0 < at + head * a.c.H) {
-        const int h = (int)((*t0 - at) / head);
-        at += h * head;
-        int mt = 0;
-        for (;; ++mt) {
-          const int n = Div::tiles(a, seq, w, mt);
-          if (*t0 < at + n) break;
-          at += n;
-        }
-        sFind[0] = b;
-        sFind[1] = h;
-        sFind[2] = mt;
-        sUnit0 = at;
-        break;
-      }
-      at += head * a.c.H;
-    }
+    walk([&](int b, int mt, int n) {
+      if (*t0 >= at + (long)n * a.c.H) return at += (long)n * a.c.H, true;
+      const int h = (int)((*t0 - at) / n);
+      sFind[0] = b;
+      sFind[1] = h;
+      sFind[2] = mt;
+      sUnit0 = at + (long)h * n;
+      return false;
+    });
   }
   __syncthreads();
   u.b = sFind[0];
@@ -200,8 +196,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
   if (d.x < 0) return;
   const int b = d.x, h = d.y, last = d.w;
   const long r0 = (long)d.z * ROWS;
-  long seq;
-  int w;
+  int seq, w;
   Division<ROWS, KEYS>::lens(a, b, &seq, &w);
   const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 3), part = threadIdx.x & 7;
   if (r >= (long)(w < 0 ? a.W : w) * a.G - r0) return;

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
       const long keys = Div::seen(a, u.seq, u.w, u.mt);
       const int steps = (int)min((long)tile1 * kRWarps, (keys + kStep - 1) / kStep);
       if (tile1 == u.tiles)  // a window block that no row of this tile reads is checked all the same
-        for (int i = (int)(u.seq / c.tpb) + tid; (long)i * c.tpb < u.seq + u.w; i += kRThreads)
+        for (int i = (int)(u.seq / c.tpb) + tid; (long)i * c.tpb < (long)u.seq + u.w; i += kRThreads)
           if (table[i] < 0 || table[i] >= c.num_blocks) sBad = 1;
 
       // ---- the ring: step st of the unit = keys [16 st, 16 st + 16)

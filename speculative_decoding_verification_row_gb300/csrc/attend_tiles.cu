@@ -3,12 +3,13 @@
 //
 // One CTA per SM, 128 rows x 128 keys a step, on tcgen05 (fp16 operands, fp32
 // accumulators in tensor memory).  Warps by role:
-//   0-3    softmax: thread = row.  Reads S from tensor memory, writes the
-//          weights P back there as fp16, rescales O when the maximum moves by
-//          more than 2^7, and writes the result.  Loads Q at a unit's start.
-//   4      one thread issues the products: S = Q K^T with Q in tensor memory,
+//   0-7    softmax: two threads per row, one for each half of the tile's
+//          keys (and of D).  Reads S from tensor memory, writes the weights P
+//          back there as fp16, rescales O when the maximum moves by more than
+//          2^7, and writes the result.  Loads Q at a unit's start.
+//   8      one thread issues the products: S = Q K^T with Q in tensor memory,
 //          O += P V with P in tensor memory, K and V in shared memory.
-//   5-12   read e4m3 rows of the pages, one tile ahead in registers, and
+//   9-15   read e4m3 rows of the pages, one tile ahead in registers, and
 //          write them as fp16 (exact) in the 128-byte swizzle.
 // With both left operands in tensor memory a step reads 64 KB (D = 128) and
 // writes 64 KB of shared memory, as long as its products take (1024 clocks);
@@ -25,11 +26,11 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
 constexpr int kLeastTiles = 2;
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kConvWarp = 5, kConvWarps = 8;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarp = 9, kConvWarps = 7;
 constexpr int kTThreads = (kConvWarp + kConvWarps) * 32;
 constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kGroups = kKeys / 16;      // scale groups of a tile
-constexpr int kScaleRing = 8;            // tiles whose scales are kept; more than any role runs ahead
+constexpr int kScaleRing = 8;            // tiles whose scales and pages are kept; more than any role runs ahead
 using Div = Division<kRows, kKeys>;
 
 constexpr uint32_t kColQ = 0, kColP = 64, kColS = 128, kColO = 384, kCols = 512;
@@ -43,7 +44,7 @@ struct Tile {
 
 struct Bars {
   unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4];
-  unsigned long long s_full[2], p_full, pv_done, q_full, scales[kScaleRing], end;
+  unsigned long long s_full[2], p_full, pv_done, q_full, scales[kScaleRing], pages[kScaleRing], end;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -66,43 +67,30 @@ __device__ __forceinline__ bool bar_try(unsigned long long* b, uint32_t parity) 
   return ok != 0;
 }
 // Waits for the phase, about two seconds at most; after that *dead is set and
-// no wait of the CTA waits any longer: it ends, and its rows read NaN.
-__device__ __noinline__ void bar_wait_slow(unsigned long long* b, uint32_t parity, volatile int* dead) {
+// no wait of the CTA waits any longer: it ends, and its rows read NaN.  All
+// inline: a call would make the converters wait for their loads in flight.
+__device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity, volatile int* dead) {
+  if (bar_try(b, parity)) return;
   const long long begin = clock64();
   while (!bar_try(b, parity)) {
     if (*dead) return;
-    if (clock64() - begin > 4000000000ll) {
-      *dead = 1;
-      return;
-    }
+    if (clock64() - begin > 4000000000ll) *dead = 1;
   }
 }
-__device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity, volatile int* dead) {
-  if (!bar_try(b, parity)) bar_wait_slow(b, parity, dead);
-}
 
-__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld32(float* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(addr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -128,6 +116,11 @@ __device__ __forceinline__ void mma_commit(unsigned long long* bar) {
                : "memory");
 }
 
+__device__ __forceinline__ bool elect() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+  return ok != 0;
+}
 // Shared memory descriptor, 128-byte swizzle.  K-major (K^T): 8 rows of 128
 // bytes are an atom, atoms 1024 bytes apart along the keys.  MN-major (V):
 // an atom is 64 elements of d by 8 keys, atoms 1024 bytes apart along the
@@ -161,6 +154,36 @@ __device__ __forceinline__ float2 as_float2(uint32_t w, __half*) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The two softmax warps of the same rows.
+__device__ __forceinline__ void pair_sync(int warp) {
+  asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+}
+
+// Bit k: the row of window token i sees window place j + k (all of the prefix,
+// j + k < 0, is seen).
+__device__ __noinline__ unsigned seen_bits(const AttendArgs& a, const Unit& u, int i, long j) {
+  if (!a.masks) {
+    const long upto = min((long)i, (long)u.w - 1) - j;  // last place seen
+    return upto >= 31 ? ~0u : upto < 0 ? 0u : (2u << upto) - 1;
+  }
+  const int32_t* row = a.masks + ((size_t)u.b * a.W + i) * a.words;
+  unsigned bits = j >= 0 ? 0u : j <= -32 ? ~0u : (1u << -j) - 1;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {  // the two words that 32 places can straddle
+    const long word = (j >> 5) + y;
+    if (word < 0 || word * 32 >= u.w) continue;
+    const int left = (int)(u.w - word * 32), shift = (int)(word * 32 - j);
+    const unsigned m = (unsigned)row[word] & (left < 32 ? (1u << left) - 1 : ~0u);
+    bits |= shift >= 32 ? 0u : shift >= 0 ? m << shift : m >> -shift;
+  }
+  return bits;
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const AttendArgs a) {
   using TL = Tile<D>;
@@ -168,7 +191,9 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   extern __shared__ unsigned char smem_raw[];
   __shared__ Bars bars;
   __shared__ long long sPre[kTThreads + 1];
-  __shared__ float sK[kScaleRing][kGroups], sV[kScaleRing][kGroups];
+  __shared__ __align__(16) float sK[kScaleRing][kGroups], sV[kScaleRing][kGroups];
+  __shared__ const uint8_t* sPage[kScaleRing][kGroups];  // K rows of each 16-key group
+  __shared__ float sTop[2][2][kRows];  // what the two threads of a row tell each other
   __shared__ uint32_t sTmem;
   __shared__ int sDead, sNan;
   const KvCache& c = a.c;
@@ -188,7 +213,10 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     bar_init(&bars.p_full, kSoftWarps);
     bar_init(&bars.pv_done, 1);
     bar_init(&bars.q_full, kSoftWarps);
-    for (int i = 0; i < kScaleRing; ++i) bar_init(&bars.scales[i], 1);
+    for (int i = 0; i < kScaleRing; ++i) {
+      bar_init(&bars.scales[i], 1);
+      bar_init(&bars.pages[i], 1);
+    }
     bar_init(&bars.end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sDead = 0;
@@ -213,55 +241,73 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   unsigned char* tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   volatile int* dead = &sDead;
 
-  // Every role walks the same segments; `n` counts tiles over all of them.
-  uint32_t n = 0, seg = 0;
-  for (long at = t0; at < t1; ++seg) {
-    const long stop = min(t1, unit0 + u.tiles);
-    const int tile0 = (int)(at - unit0), tile1 = (int)(stop - unit0);
-    const long keys = u.w < 0 ? 0 : Div::seen(a, u.seq, u.w, u.mt);
+  // The addresses are below 2^18: adding to the descriptor's low bits never carries out of them.
+  const uint64_t k_desc = smem_desc(smem_u32(tiles), 16);
+  const uint64_t v_desc = smem_desc(smem_u32(tiles) + ST * TL::kBytes, kKeys * 128);
 
-    if (warp < kSoftWarps) {
-      const int r0 = u.mt * kRows, r = tid;
+  // Each role walks the same segments (a unit's tiles within the CTA's share);
+  // `n` counts tiles over all of them, `seg` the segments that load a Q.
+  uint32_t n = 0, seg = 0;
+  auto segments = [&](auto role) {
+    for (long at = t0; at < t1;) {
+      const long stop = min(t1, unit0 + u.tiles);
+      role((int)(at - unit0), (int)(stop - unit0), u.w < 0 ? 0u : Div::seen(a, u.seq, u.w, u.mt));
+      at = stop;
+      unit0 += u.tiles;
+      if (u.w >= 0) ++seg;
+      if (at < t1 && !Div::next(a, u)) break;
+    }
+  };
+  if (warp < kSoftWarps) {
+    segments([&](int tile0, int tile1, unsigned) {
+      const int r0 = u.mt * kRows, half = warp >> 2, r = tid & (kRows - 1);
       const int w = u.w < 0 ? a.W : u.w;
       const int rows = (int)min((long)kRows, (long)w * a.G - r0);
       const int i = r < rows ? (r0 + r) / a.G : 0, head = r < rows ? (r0 + r) % a.G : 0;
-      const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      constexpr int HD = D / 2;  // elements of D that this thread serves
       float m = -INFINITY, l = 0.f, vref = 0.f;
       bool bad = u.w < 0;
       if (u.w >= 0) {
         // ---- Q: a power of two per row, rounded to fp16, into tensor memory
         const uint4* qp = reinterpret_cast<const uint4*>(
-            a.q + 2 * (u.b * a.qb + i * a.qt + ((long)u.h * a.G + head) * a.qh));
+            a.q + 2 * (u.b * a.qb + i * a.qt + ((long)u.h * a.G + head) * a.qh + half * HD));
+        uint4 qv[HD / 8];
         float top = 0.f;
-#pragma unroll 4
-        for (int v = 0; v < D / 8; ++v) {
-          const uint4 x = r < rows ? qp[v] : make_uint4(0, 0, 0, 0);
-          const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int v = 0; v < HD / 8; ++v) qv[v] = r < rows ? qp[v] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < HD / 8; ++v) {
+          const uint32_t e[4] = {qv[v].x, qv[v].y, qv[v].z, qv[v].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 f = as_float2(e[k], (T*)nullptr);
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            top = max3(top, fabsf(f.x), fabsf(f.y));
           }
         }
+        pair_sync(warp);  // the partner has read what the last unit left here
+        sTop[0][half][r] = top;
+        pair_sync(warp);
+        top = fmaxf(sTop[0][0][r], sTop[0][1][r]);
+        pair_sync(warp);
         int e2;
         frexpf(top, &e2);
         const int up = top > 0.f && top < INFINITY ? min(15 - e2, 126) : 0;
         const float f = copysignf(ldexpf(1.f, up), a.scale_log2);
         const float qs = fabsf(a.scale_log2) * ldexpf(1.f, -up);  // >= 0: maxima stay maxima
 #pragma unroll
-        for (int v = 0; v < D / 32; ++v) {
+        for (int v = 0; v < HD / 32; ++v) {
           uint32_t h[16];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const uint4 x = r < rows ? qp[v * 4 + y] : make_uint4(0, 0, 0, 0);
-            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t e[4] = {qv[v * 4 + y].x, qv[v * 4 + y].y, qv[v * 4 + y].z, qv[v * 4 + y].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float2 p = as_float2(e[k], (T*)nullptr);
               h[y * 4 + k] = half2_of(p.x * f, p.y * f);
             }
           }
-          tmem_st16(lanes + kColQ + v * 16, h);
+          tmem_st16(lanes + kColQ + half * (HD / 2) + v * 16, h);
         }
         tmem_wait_st();
         fence_before();
@@ -271,59 +317,45 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         for (int tile = tile0; tile < tile1; ++tile, ++n) {
           const int ring = n % kScaleRing;
           bar_wait(&bars.scales[ring], (n / kScaleRing) & 1, dead);
-          const uint32_t s_addr = lanes + kColS + (n & 1) * kKeys;
+          const float4 k4 = reinterpret_cast<const float4*>(sK[ring])[half];
+          const float4 va = reinterpret_cast<const float4*>(sV[ring])[0];
+          const float4 vb = reinterpret_cast<const float4*>(sV[ring])[1];
+          const float vmax = fmaxf(max3(max3(va.x, va.y, va.z), va.w, vb.x), max3(vb.y, vb.z, vb.w));
+          const float4 v4 = half ? vb : va;
+          float kf[4] = {k4.x * qs, k4.y * qs, k4.z * qs, k4.w * qs};
+#pragma unroll
+          for (int y = 0; y < 4; ++y)  // -inf times it stays -inf; NaN (no such block) stays NaN
+            kf[y] = kf[y] < 0x1p-120f ? 0x1p-120f : kf[y];
           bar_wait(&bars.s_full[n & 1], (n >> 1) & 1, dead);
           fence_after();
-          const long k0 = (long)tile * kKeys;
-          const bool edge = k0 + kKeys > u.seq;
-          // the window tokens that this row sees among keys [x, x + 32) of the tile
-          auto seen32 = [&](int x) {
-            const long j = k0 + x - u.seq;  // window place of key x
-            unsigned bits = 0;
-            if (a.masks) {
-              const int32_t* row = a.masks + ((size_t)u.b * a.W + i) * a.words;
-              const int left = u.w;
+          float s[64];
+          tmem_ld32(s, lanes + kColS + (n & 1) * kKeys + half * 64);
+          tmem_ld32(s + 32, lanes + kColS + (n & 1) * kKeys + half * 64 + 32);
+          tmem_wait_ld();
+          const long k0 = (long)tile * kKeys + half * 64 - u.seq;  // window place of s[0]
+          if (k0 + 64 > 0) {
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {  // the two words that the 32 places can straddle
-                const long wd = (j >> 5) + y;
-                if (wd >= 0 && wd * 32 < left) {
-                  unsigned m32 = (unsigned)row[wd];
-                  if (left - wd * 32 < 32) m32 &= (1u << (left - wd * 32)) - 1;
-                  const int sh = (int)(wd * 32 - j);  // place of the word's bit 0
-                  bits |= sh >= 32 ? 0u : sh >= 0 ? m32 << sh : m32 >> -sh;
-                }
-              }
-              if (j < 0) bits |= j <= -32 ? ~0u : (1u << -j) - 1;
-            } else {
-              const long upto = min((long)i, (long)u.w - 1) - j;  // last place seen
-              bits = upto >= 31 ? ~0u : upto < 0 ? 0u : (2u << upto) - 1;
-            }
-            return bits;
-          };
-          // ---- the tile's largest score, V scale
-          float top = -INFINITY, vmax = 0.f;
-#pragma unroll
-          for (int x = 0; x < kKeys; x += 32) {
-            uint32_t s[32];
-            tmem_ld32(s, s_addr + x);
-            tmem_wait_ld();
-            if (edge) {
-              const unsigned bits = seen32(x);
+            for (int x = 0; x < 64; x += 32) {
+              const unsigned bits = seen_bits(a, u, i, k0 + x);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!(bits >> k & 1)) s[k] = 0xff800000u;
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float t = -INFINITY;
-#pragma unroll
-              for (int k = 0; k < 16; ++k) t = fmaxf(t, __uint_as_float(s[y * 16 + k]));
-              const int grp = x / 16 + y;
-              vmax = fmaxf(vmax, sV[ring][grp]);
-              const float kf = qs * sK[ring][grp];
-              if (t > -INFINITY) top = fmaxf(top, t * kf);
+                if (!(bits >> k & 1)) s[x + k] = -INFINITY;
             }
           }
+          float top = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              t0 = max3(t0, s[y * 16 + k], s[y * 16 + k + 1]);
+              t1 = max3(t1, s[y * 16 + k + 2], s[y * 16 + k + 3]);
+            }
+            top = fmaxf(top, fmaxf(t0, t1) * kf[y]);
+          }
+          sTop[n & 1][half][r] = top;
+          pair_sync(warp);
+          top = fmaxf(top, sTop[n & 1][half ^ 1][r]);
           const bool move = top > m + kLazy;
           const bool wide = vmax > vref;
           if (__any_sync(~0u, move || wide)) {
@@ -337,48 +369,45 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               bar_wait(&bars.pv_done, (n - 1) & 1, dead);
               fence_after();
 #pragma unroll 1
-              for (int x = 0; x < D; x += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, lanes + kColO + x);
+              for (int x = half * HD; x < half * HD + HD; x += 16) {
+                uint32_t o[16];
+                tmem_ld16(o, lanes + kColO + x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ar);
-                tmem_st32(lanes + kColO + x, o);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ar);
+                tmem_st16(lanes + kColO + x, o);
               }
             }
           }
-          const float sub = m == -INFINITY ? 0.f : m - kPBits;
-          const float inv_vref = vref > 0.f ? 1.f / vref : 0.f;
-          // P has one buffer: the last tile's product has read it
-          if (n > 0) bar_wait(&bars.pv_done, (n - 1) & 1, dead);
-          fence_after();
+          // The V scale's ratio goes into the exponent, and out of the sum again.
+          // Where it is below 2^-40 it is taken as that: such a block adds at most
+          // 2^-40 of the largest |V|.
+          const float add = m == -INFINITY ? 0.f : kPBits - m;
+          const float inv_vref = vref > 0.f ? 1.f / vref : 1.f;
+          const float vr[4] = {fmaxf(v4.x * inv_vref, 0x1p-40f), fmaxf(v4.y * inv_vref, 0x1p-40f),
+                               fmaxf(v4.z * inv_vref, 0x1p-40f), fmaxf(v4.w * inv_vref, 0x1p-40f)};
 #pragma unroll
-          for (int x = 0; x < kKeys; x += 32) {
-            uint32_t s[32], p[16];
-            tmem_ld32(s, s_addr + x);
-            tmem_wait_ld();
-            if (edge) {
-              const unsigned bits = seen32(x);
+          for (int z = 0; z < 2; ++z) {
+            uint32_t p[16];
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(bits >> k & 1)) s[k] = 0xff800000u;
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int grp = x / 16 + y;
-              const float kf = qs * sK[ring][grp];
-              const float vr = sV[ring][grp] * inv_vref;
+            for (int y = 2 * z; y < 2 * z + 2; ++y) {
+              const float av = add + __log2f(vr[y]);
+              float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
-                const float s0 = __uint_as_float(s[y * 16 + k]), s1 = __uint_as_float(s[y * 16 + k + 1]);
-                // a masked score stays -inf under a scale of zero
-                const float e0 = ex2(s0 == -INFINITY ? s0 : fmaf(s0, kf, -sub));
-                const float e1 = ex2(s1 == -INFINITY ? s1 : fmaf(s1, kf, -sub));
-                l += e0 + e1;
-                p[y * 8 + k / 2] = half2_of(e0 * vr, e1 * vr);
+                const int x = y * 16 + k;
+                float2 e = fma2(make_float2(s[x], s[x + 1]), make_float2(kf[y], kf[y]), make_float2(av, av));
+                e = make_float2(ex2(e.x), ex2(e.y));
+                sum = add2(sum, e);
+                p[(x & 31) / 2] = half2_of(e.x, e.y);
               }
+              l += __fdividef(sum.x + sum.y, vr[y]);
             }
-            tmem_st16(lanes + kColP + x / 2, p);
+            if (z == 0) {  // P has one buffer: the last tile's product has read it
+              if (n > 0) bar_wait(&bars.pv_done, (n - 1) & 1, dead);
+              fence_after();
+            }
+            tmem_st16(lanes + kColP + half * 32 + z * 16, p);
           }
           tmem_wait_st();
           fence_before();
@@ -388,10 +417,14 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         if (tile1 == u.tiles) {  // a window block that these rows do not read is checked all the same
           const int32_t* table = c.tables + (size_t)u.b * c.max_blocks;
           bool miss = false;
-          for (int x = (int)(u.seq / c.tpb) + lane; (long)x * c.tpb < u.seq + u.w; x += 32)
+          for (int x = (int)(u.seq / c.tpb) + lane; (long)x * c.tpb < (long)u.seq + u.w; x += 32)
             miss = miss || table[x] < 0 || table[x] >= c.num_blocks;
           bad = __any_sync(~0u, miss);
         }
+        pair_sync(warp);
+        sTop[0][half][r] = l;
+        pair_sync(warp);
+        l = sTop[0][0][r] + sTop[0][1][r];
         bar_wait(&bars.pv_done, (n - 1) & 1, dead);
         fence_after();
       }
@@ -405,14 +438,14 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       const long j0 = max(0l, (long)tile0 * kKeys - u.seq);
       const long j1 = sNan ? min((long)u.w, (long)tile1 * kKeys - u.seq) : 0;
 #pragma unroll 1
-      for (int x = 0; x < D; x += 32) {
-        uint32_t o[32];
+      for (int x = half * HD; x < half * HD + HD; x += 32) {
+        float o[32];
         if (u.w >= 0) {
           tmem_ld32(o, lanes + kColO + x);
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
         if (r < rows) {
           for (long j = j0; j < j1; ++j) {
@@ -427,7 +460,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               const uint32_t nb = nan_bytes(v[k]);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (nb >> (8 * e + 7) & 1) o[k * 4 + e] = 0x7fc00000u;
+                if (nb >> (8 * e + 7) & 1) o[k * 4 + e] = NAN;
             }
           }
           if (whole) {
@@ -437,21 +470,21 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               uint32_t y[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                y[e] = pack_out(__uint_as_float(o[k * 8 + e * 2]) * f,
-                                __uint_as_float(o[k * 8 + e * 2 + 1]) * f, (T*)nullptr);
+                y[e] = pack_out(o[k * 8 + e * 2] * f,
+                                o[k * 8 + e * 2 + 1] * f, (T*)nullptr);
               dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               *reinterpret_cast<float4*>(part + (size_t)r * D + x + 4 * k) = make_float4(
-                  __uint_as_float(o[4 * k]) * f, __uint_as_float(o[4 * k + 1]) * f,
-                  __uint_as_float(o[4 * k + 2]) * f, __uint_as_float(o[4 * k + 3]) * f);
+                  o[4 * k] * f, o[4 * k + 1] * f,
+                  o[4 * k + 2] * f, o[4 * k + 3] * f);
           }
         }
         __syncwarp();
       }
-      if (r < rows) {
+      if (r < rows && half == 0) {
         if (whole) {
           if (a.lse) a.lse[orow] = row_lse(m, l);
         } else {
@@ -467,20 +500,23 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         d[3] = share_owner(total, unit0 + u.tiles - 1, ctas);
       }
       fence_before();  // O has been read: the next unit's first product may follow its q_full, p_full
-    } else if (warp == kMmaWarp) {
+    });
+  } else {
+    if (warp == kMmaWarp) {
+      segments([&](int tile0, int tile1, unsigned) {
       if (u.w >= 0) {
         bar_wait(&bars.q_full, seg & 1, dead);
         fence_after();
-        const uint32_t base = smem_u32(tiles);
         auto scores = [&](uint32_t t) {
-          const int st = t % ST;
+          const uint32_t st = t % ST;
           bar_wait(&bars.k_full[st], (t / ST) & 1, dead);
           fence_after();
-          if (lane == 0 && !*dead) {
+          if (elect() && !*dead) {
+            const uint32_t d = tmem + kColS + (t & 1) * kKeys;
+            const uint64_t b = k_desc + st * (TL::kBytes >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              mma_ts(tmem + kColS + (t & 1) * kKeys, tmem + kColQ + k * 8,
-                     smem_desc(base + st * TL::kBytes + (k / 4) * (kKeys * 128) + (k % 4) * 32, 16),
+              mma_ts(d, tmem + kColQ + k * 8, b + (k / 4) * (kKeys * 128 >> 4) + (k % 4) * (32 >> 4),
                      instr_desc(kKeys, false), k > 0);
             mma_commit(&bars.k_empty[st]);
             mma_commit(&bars.s_full[t & 1]);
@@ -490,130 +526,162 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         scores(n);
         for (int tile = tile0; tile < tile1; ++tile, ++n) {
           if (tile + 1 < tile1) scores(n + 1);
-          const int st = n % ST;
+          const uint32_t st = n % ST;
           bar_wait(&bars.v_full[st], (n / ST) & 1, dead);
           bar_wait(&bars.p_full, n & 1, dead);
           fence_after();
-          if (lane == 0 && !*dead) {
+          if (elect() && !*dead) {
+            const uint64_t b = v_desc + st * (TL::kBytes >> 4);
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + kColO, tmem + kColP + k * 8,
-                     smem_desc(base + (ST + st) * TL::kBytes + k * 2048, kKeys * 128),
-                     instr_desc(D, true), tile > tile0 || k > 0);
+              mma_ts(tmem + kColO, tmem + kColP + k * 8, b + k * (2048 >> 4), instr_desc(D, true),
+                     tile > tile0 || k > 0);
             mma_commit(&bars.v_empty[st]);
             mma_commit(&bars.pv_done);
           }
           __syncwarp();
         }
       }
+      });
     } else {
+      segments([&](int tile0, int tile1, unsigned keys) {
       if (u.w >= 0) {
-        // Thread t of the converters: chunk t % (D / 16) of rows t / (D / 16) + kPer p.
-        constexpr int CPR = D / 16, kPer = kConvThreads / CPR, NP = kKeys / kPer;
-        const int t = tid - kConvWarp * 32, ch = t % CPR, row = t / CPR;
+        // Thread t of the converters: chunk ch (16 bytes) of rows row + kPer p.
+        // Eight neighbours hold four chunks of two rows, which keeps their
+        // 16-byte stores below off each other's banks.
+        constexpr int CPR = D / 16, kPer = kConvThreads / CPR, NP = (kKeys + kPer - 1) / kPer;
+        static_assert(kConvThreads % CPR == 0 && kPer % 4 == 0 && NP <= 8, "converter layout");
+        const int t = tid - kConvWarp * 32;
+        const int ch = D == 128 ? (t & 3) | (t >> 1 & 4) : t & 3;
+        const int row = D == 128 ? (t >> 2 & 1) | t >> 4 << 1 : t >> 2;
         const int tpb16 = c.tpb / 16;
         const int32_t* table = c.tables + (size_t)u.b * c.max_blocks;
-        const size_t v_off = (size_t)c.H * c.tpb * D;
-        uint4 kr[NP], vr[NP];
-        const uint8_t* src[NP];
-        auto locate = [&](int tile) {  // where this thread's rows of a tile are (null: no such row)
+        const size_t v_off = (size_t)c.H * c.tpb * D;  // from a block's K rows to its V rows
+
+        // ---- one warp keeps the tiles' pages: lane's group and kind
+        int pblk = -1, sblk = -1;  // block ids, loaded a tile before they are looked at
+        float scale = 0.f;
+        auto group_block = [&](int tile) {
+          const unsigned grp = (unsigned)tile * kGroups + (lane & 7);
+          return lane < 16 && tile < tile1 && grp * 16 < keys ? table[col16(a, grp)] : -2;  // -2: no such keys
+        };
+        auto load_scale = [&]() {
+          scale = sblk == -2 || lane >= 8 ? 0.f : NAN;  // a block that does not exist makes the scores NaN
+          if ((unsigned)sblk < (unsigned)c.num_blocks) scale = c.scales[c.scale_at(sblk, lane >> 3, u.h)];
+        };
+        auto post_pages = [&](int tile, uint32_t at) {
+          if (tile >= tile1) return;
+          // Groups without a block read block 0: their scores are masked or NaN.
+          const unsigned grp = (unsigned)tile * kGroups + (lane & 7);
+          const bool ok = (unsigned)pblk < (unsigned)c.num_blocks;
+          const size_t off = ((size_t)(ok ? pblk : 0) * 2 * c.H + u.h) * c.tpb +
+                             (ok ? (grp - col16(a, grp) * tpb16) * 16 : 0);
+          if (lane < 8) sPage[at % kScaleRing][lane] = c.pool + off * D;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bars.pages[at % kScaleRing]);
+        };
+
+        auto load = [&](uint4 (&x)[NP], uint4 (&y)[NP], int tile, uint32_t at) {
+          if (tile >= tile1) return;
+          bar_wait(&bars.pages[at % kScaleRing], (at / kScaleRing) & 1, dead);
+          const uint8_t* const* page = sPage[at % kScaleRing];
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            const long key = (long)tile * kKeys + p * kPer + row;
-            src[p] = nullptr;
-            if (key < keys) {
-              const int grp = (int)(key >> 4), col = grp / tpb16;
-              const int blk = table[col];
-              if (blk >= 0 && blk < c.num_blocks)
-                src[p] = c.pool + c.row(blk, 0, u.h, (grp - col * tpb16) * 16 + (int)(key & 15)) + ch * 16;
+            const int r = p * kPer + row;
+            if (p * kPer + kPer <= kKeys || r < kKeys) {
+              const uint8_t* src = page[r >> 4] + ((r & 15) * D + ch * 16);
+              x[p] = *reinterpret_cast<const uint4*>(src);
+              y[p] = *reinterpret_cast<const uint4*>(src + v_off);
             }
           }
         };
-        auto load = [&](uint4 (&x)[NP], size_t off) {
-#pragma unroll
-          for (int p = 0; p < NP; ++p)
-            x[p] = src[p] ? *reinterpret_cast<const uint4*>(src[p] + off) : make_uint4(0, 0, 0, 0);
-        };
+        // places of the two fp16 vectors of row `row`; row + kPer is kPer % 8 = 4 rows on in the swizzle
+        const int atom = (ch >> 2) * (kKeys * 128) + row * 128, c0 = (ch & 3) * 2;
+        const int o0 = atom + ((c0 ^ (row & 7)) << 4), o1 = atom + (((c0 + 1) ^ (row & 7)) << 4);
         auto put = [&](const uint4 (&x)[NP], unsigned char* tile) {
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            const int key = p * kPer + row;
-            const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-            uint32_t h[8];
+            if (p * kPer + kPer <= kKeys || p * kPer + row < kKeys) {
+              const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+              uint32_t h[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) e4m3x4_to_half(w[k], h[2 * k], h[2 * k + 1]);
-            unsigned char* at16 = tile + (ch >> 2) * (kKeys * 128) + key * 128;
-            const int c0 = (ch & 3) * 2;
-            // half of the threads write their second 16 bytes first: no bank conflicts
-            const int first = D == 128 ? ch >> 2 : 0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int s = k ^ first;
-              *reinterpret_cast<uint4*>(at16 + (((c0 + s) ^ (key & 7)) << 4)) =
-                  s ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+              for (int k = 0; k < 4; ++k) e4m3x4_to_half(w[k], h[2 * k], h[2 * k + 1]);
+              const int flip = p * kPer & 4 ? 64 : 0;
+              *reinterpret_cast<uint4*>(tile + p * kPer * 128 + (o0 ^ flip)) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(tile + p * kPer * 128 + (o1 ^ flip)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         };
-        locate(tile0);
-        load(kr, 0);
-        load(vr, v_off);
-        for (int tile = tile0; tile < tile1; ++tile, ++n) {
-          const int st = n % ST, ring = n % kScaleRing;
-          if (warp == kConvWarp) {  // the tile's scales
-            const int grp = tile * kGroups + (lane & 7), col = grp / tpb16;
-            float s = 0.f;
-            if (lane < 16 && (long)grp * 16 < keys) {
-              const int blk = table[col];
-              // a block that does not exist makes the scores NaN
-              s = blk >= 0 && blk < c.num_blocks ? c.scales[c.scale_at(blk, lane >> 3, u.h)]
-                                                 : lane < 8 ? NAN : 0.f;
-            }
-            if (lane < 8) sK[ring][lane] = s;
-            else if (lane < 16) sV[ring][lane - 8] = s;
+        // Two tiles are on their way in registers while a third is written.
+        auto step = [&](uint4 (&kr)[NP], uint4 (&vr)[NP], int tile) {
+          const uint32_t st = n % ST, ring = n % kScaleRing;
+          if (warp == kConvWarp) {
+            if (lane < 8) sK[ring][lane] = scale;
+            else if (lane < 16) sV[ring][lane - 8] = scale;
             __syncwarp();
             if (lane == 0) bar_arrive(&bars.scales[ring]);
+            load_scale();
+            sblk = group_block(tile + 2);
+            post_pages(tile + 3, n + 3);
+            pblk = group_block(tile + 4);
           }
           bar_wait(&bars.k_empty[st], ((n / ST) & 1) ^ 1, dead);
           put(kr, tiles + st * TL::kBytes);
           if (lane == 0) bar_arrive(&bars.k_full[st]);
-          if ((long)(tile + 1) * kKeys > u.seq) {
-            // NaN in a window row of V: only the rows that see it may get it
+          if ((tile + 1) * kKeys > u.seq) {
+            // Rows behind the keys hold anything; they are zero here.  NaN in a
+            // window row: only the rows that see it may get it (see the result).
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
+              const unsigned key = (unsigned)tile * kKeys + p * kPer + row;
               uint32_t w[4] = {vr[p].x, vr[p].y, vr[p].z, vr[p].w};
-              if ((long)tile * kKeys + p * kPer + row >= u.seq) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t nb = nan_bytes(w[k]);
-                  if (nb) sNan = 1;
-                  w[k] &= ~((nb >> 7) * 255u);
-                }
-                vr[p] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t nb = key >= keys ? 0x80808080u : key >= (unsigned)u.seq ? nan_bytes(w[k]) : 0u;
+                if (nb && key < keys && p * kPer + row < kKeys) sNan = 1;
+                w[k] &= ~((nb >> 7) * 255u);
               }
+              vr[p] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          }
-          if (tile + 1 < tile1) {
-            locate(tile + 1);
-            load(kr, 0);
           }
           bar_wait(&bars.v_empty[st], ((n / ST) & 1) ^ 1, dead);
           put(vr, tiles + (ST + st) * TL::kBytes);
           if (lane == 0) bar_arrive(&bars.v_full[st]);
-          if (tile + 1 < tile1) load(vr, v_off);
+          load(kr, vr, tile + 2, n + 2);
+          ++n;
+        };
+        uint4 ka[NP], va[NP], kb[NP], vb[NP];
+        if (warp == kConvWarp) {
+          int b3[3];
+#pragma unroll
+          for (int x = 0; x < 3; ++x) b3[x] = group_block(tile0 + x);
+          const int b4 = group_block(tile0 + 3);
+#pragma unroll
+          for (int x = 0; x < 3; ++x) {
+            pblk = b3[x];
+            post_pages(tile0 + x, n + x);
+          }
+          pblk = b4;
+          sblk = b3[0];
+          load_scale();
+          sblk = b3[1];
+        }
+        load(ka, va, tile0, n);
+        load(kb, vb, tile0 + 1, n + 1);
+        for (int tile = tile0; tile < tile1; tile += 2) {
+          step(ka, va, tile);
+          if (tile + 1 < tile1) step(kb, vb, tile + 1);
         }
       }
+      });
     }
-    at = stop;
-    unit0 += u.tiles;
-    if (u.w < 0) --seg;  // no Q was loaded for it
-    if (at < t1 && !Div::next(a, u)) break;
   }
 
   // Every product has finished before tensor memory is given back.
   if (warp == kMmaWarp) {
-    if (lane == 0) mma_commit(&bars.end);
+    if (elect()) mma_commit(&bars.end);
     __syncwarp();
     const long long begin = clock64();
     while (!bar_try(&bars.end, 0) && clock64() - begin < 4000000000ll) {
