@@ -35,8 +35,8 @@ constexpr long kMaxPositions = 1l << 30;
 // query head g of the group) and cut into tiles of ROWS; a "unit" is one such
 // tile of one (request, KV head).  Its keys are cut into tiles of KEYS.  The
 // key tiles of all units, ordered by request, row tile and head, form one
-// line that is cut into equal shares, one per CTA, so a ragged batch keeps
-// every SM equally busy and a long prefix spreads over the whole GPU.  A unit
+// line that is cut into equal shares, one per CTA (see Walk), so a ragged
+// batch keeps every SM equally busy and a long prefix spreads over all.  A unit
 // whose tiles fall to several CTAs is joined afterwards from the (max, sum,
 // weighted V) of each.
 struct Unit {
@@ -80,21 +80,54 @@ struct Division {
   }
 };
 
-// Share of CTA i of n over a line of `total` tiles, and the owner of a tile.
+// Share of CTA i of n over a line of `total` cells, and the owner of a cell.
 __device__ __forceinline__ long share_begin(long total, int i, int n) { return total * i / n; }
-__device__ __forceinline__ int share_owner(long total, long tile, int n) {
-  return (int)(((tile + 1) * n - 1) / total);
+__device__ __forceinline__ int share_owner(long total, long cell, int n) {
+  return (int)(((cell + 1) * n - 1) / total);
 }
 
-// What a CTA of THREADS threads knows of the division: its share [t0, t1) of
-// the line, the unit that t0 falls into and where that unit begins.  False:
-// nothing to do.  sPre: THREADS + 1 words.  `least`: tiles below which a
-// share is not worth a CTA.  Every CTA sums the line anew, (request, row tile)
-// pairs over its threads: no state between launches and none to clear.
-template <int ROWS, int KEYS, int THREADS>
-__device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long* sPre, Unit& u,
-                                       long* t0, long* t1, long* unit0, long* total_out,
-                                       int* ctas_out) {
+// A CTA's share of the line.  A unit takes COST cells (for loading its rows
+// and writing its result) and one for each of its key tiles; the tiles of a
+// unit that fall into the share are a segment.
+template <int ROWS, int KEYS, int COST>
+struct Walk {
+  Unit u;
+  long at, end;      // the share's cells not yet walked
+  long unit0;        // first cell of u
+  long total;
+  int ctas;
+  int tile0, tile1;  // the segment
+  // To the next segment; false at the share's end.
+  __device__ __forceinline__ bool next(const AttendArgs& a) {
+    for (;;) {
+      if (at >= end) return false;
+      const long unit1 = unit0 + COST + u.tiles;
+      if (at == unit1) {
+        unit0 = unit1;
+        if (!Division<ROWS, KEYS>::next(a, u)) return false;
+        continue;
+      }
+      const long stop = min(end, unit1);
+      tile0 = (int)max(0l, at - unit0 - COST);
+      tile1 = (int)max(0l, stop - unit0 - COST);
+      at = stop;
+      if (tile1 > tile0) return true;
+    }
+  }
+  __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == u.tiles; }
+  // The CTA that holds the unit's last tile.
+  __device__ __forceinline__ int last_cta() const {
+    return share_owner(total, unit0 + COST + u.tiles - 1, ctas);
+  }
+};
+
+// Sets a CTA of THREADS threads before the first segment of its share.
+// False: nothing to do.  sPre: THREADS + 1 words.  `least`: cells below which
+// a share is not worth a CTA.  Every CTA sums the line anew, (request, row
+// tile) pairs over its threads: no state between launches and none to clear.
+template <int ROWS, int KEYS, int COST, int THREADS>
+__device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long* sPre,
+                                       Walk<ROWS, KEYS, COST>& v) {
   using Div = Division<ROWS, KEYS>;
   __shared__ long long sWarp[THREADS / 32];
   __shared__ int sFind[3];
@@ -102,17 +135,18 @@ __device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long items = (long)a.B * a.mtiles, per = (items + THREADS - 1) / THREADS;
   const long x0 = min(items, tid * per), x1 = min(items, x0 + per);
-  // calls f(b, mt, tiles) for this thread's pairs until f returns false
-  auto walk = [&](auto f) {
+  // calls f(b, mt, cells) for this thread's pairs until f returns false
+  auto pairs = [&](auto f) {
     int b = (int)(x0 / a.mtiles), mt = (int)(x0 % a.mtiles), seq = 0, w = 0;
     for (long x = x0; x < x1; ++x) {
       if (x == x0 || mt == 0) Div::lens(a, b, &seq, &w);
-      if (!f(b, mt, Div::tiles(a, seq, w, mt))) return;
+      const int n = Div::tiles(a, seq, w, mt);
+      if (!f(b, mt, n > 0 ? n + COST : 0)) return;
       if (++mt == a.mtiles) mt = 0, ++b;
     }
   };
   long long mine = 0;
-  walk([&](int, int, int n) { return mine += n, true; });
+  pairs([&](int, int, int n) { return mine += n, true; });
   mine *= a.c.H;
   long long incl = mine;
 #pragma unroll
@@ -130,15 +164,15 @@ __device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long
   const long most = total / least > 1 ? total / least : 1;
   const int ctas = most < (long)gridDim.x ? (int)most : (int)gridDim.x;
   if (total == 0 || (int)blockIdx.x >= ctas) return false;
-  *total_out = total;
-  *ctas_out = ctas;
-  *t0 = share_begin(total, blockIdx.x, ctas);
-  *t1 = share_begin(total, blockIdx.x + 1, ctas);
-  if (sPre[tid] <= *t0 && *t0 < sPre[tid + 1]) {  // one thread: its pairs hold t0
+  v.total = total;
+  v.ctas = ctas;
+  v.at = share_begin(total, blockIdx.x, ctas);
+  v.end = share_begin(total, blockIdx.x + 1, ctas);
+  if (sPre[tid] <= v.at && v.at < sPre[tid + 1]) {  // one thread: its pairs hold the share's first cell
     long at = sPre[tid];
-    walk([&](int b, int mt, int n) {
-      if (*t0 >= at + (long)n * a.c.H) return at += (long)n * a.c.H, true;
-      const int h = (int)((*t0 - at) / n);
+    pairs([&](int b, int mt, int n) {
+      if (v.at >= at + (long)n * a.c.H) return at += (long)n * a.c.H, true;
+      const int h = (int)((v.at - at) / n);
       sFind[0] = b;
       sFind[1] = h;
       sFind[2] = mt;
@@ -147,12 +181,12 @@ __device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long
     });
   }
   __syncthreads();
-  u.b = sFind[0];
-  u.h = sFind[1];
-  u.mt = sFind[2];
-  *unit0 = sUnit0;
-  Div::lens(a, u.b, &u.seq, &u.w);
-  u.tiles = Div::tiles(a, u.seq, u.w, u.mt);
+  v.u.b = sFind[0];
+  v.u.h = sFind[1];
+  v.u.mt = sFind[2];
+  v.unit0 = sUnit0;
+  Div::lens(a, v.u.b, &v.u.seq, &v.u.w);
+  v.u.tiles = Div::tiles(a, v.u.seq, v.u.w, v.u.mt);
   return true;
 }
 

@@ -28,7 +28,8 @@ constexpr int kRWarps = 4;
 constexpr int kRThreads = kRWarps * 32;
 constexpr int kKeys = kStep * kRWarps;    // keys of a tile: one step of every warp
 constexpr int kStages = 4;
-constexpr int kLeastTiles = 4;
+constexpr int kUnitCost = 2;              // cells of a unit besides its tiles
+constexpr int kLeastCells = 6;
 constexpr int kCtas = 3 * kSms;           // resident at 168 registers and 66 KB of shared memory
 using Div = Division<kRows, kKeys>;
 
@@ -116,20 +117,17 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
   const int g = lane >> 2, cc = lane & 3;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Unit u;
-  long t0, t1, unit0, total;
-  int ctas;
+  Walk<kRows, kKeys, kUnitCost> v;
   if (tid < kDescWords) a.desc[blockIdx.x * kDescWords + tid] = -1;
-  if (!divide<kRows, kKeys, kRThreads>(a, kLeastTiles, sPre, u, &t0, &t1, &unit0, &total, &ctas))
-    return;
+  if (!divide<kRows, kKeys, kUnitCost, kRThreads>(a, kLeastCells, sPre, v)) return;
+  const Unit& u = v.u;
   unsigned char* ring = smem + warp * R::kWarp;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   const int tpb16 = c.tpb / kStep;
   const size_t v_off = (size_t)c.H * c.tpb * D;  // from a block's K rows to its V rows
 
-  for (long at = t0; at < t1;) {
-    const long stop = min(t1, unit0 + u.tiles);
-    const int tile0 = (int)(at - unit0), tile1 = (int)(stop - unit0);
+  while (v.next(a)) {
+    const int tile0 = v.tile0, tile1 = v.tile1;
     const int r0 = u.mt * kRows;
     const int w = u.w < 0 ? a.W : u.w;
     const int rows = min((long)kRows, (long)w * a.G - r0);
@@ -433,7 +431,7 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
         }
         x[j] = y.x, x[j + 1] = y.y, x[j + 2] = y.z, x[j + 3] = y.w;
       }
-      const bool whole = tile0 == 0 && tile1 == u.tiles;
+      const bool whole = v.whole();
       if (r < rows) {
         if (whole) {
           const int i = (r0 + r) / a.G, head = u.h * a.G + (r0 + r) % a.G;
@@ -462,13 +460,10 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
         d[0] = u.b;
         d[1] = u.h;
         d[2] = u.mt;
-        d[3] = share_owner(total, unit0 + u.tiles - 1, ctas);
+        d[3] = v.last_cta();
       }
     }
     __syncthreads();
-    at = stop;
-    unit0 += u.tiles;
-    if (at < t1 && !Div::next(a, u)) break;
   }
 }
 

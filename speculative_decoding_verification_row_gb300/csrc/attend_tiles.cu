@@ -25,14 +25,14 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
-constexpr int kLeastTiles = 2;
+constexpr int kUnitCost = 1;             // cells of a unit besides its tiles
+constexpr int kLeastCells = 3;
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarp = 9, kConvWarps = 7;
 constexpr int kTThreads = (kConvWarp + kConvWarps) * 32;
 constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kGroups = kKeys / 16;      // scale groups of a tile
-constexpr int kScaleRing = 8;            // tiles whose scales and pages are kept; more than any role runs ahead
-using Div = Division<kRows, kKeys>;
-
+constexpr int kRing = 8;                 // tiles whose pages and scales are kept
+constexpr int kAhead = 4;                // tiles that they are looked up ahead of the products
 constexpr uint32_t kColQ = 0, kColP = 64, kColS = 128, kColO = 384, kCols = 512;
 
 template <int D>
@@ -44,7 +44,7 @@ struct Tile {
 
 struct Bars {
   unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4];
-  unsigned long long s_full[2], p_full, pv_done, q_full, scales[kScaleRing], pages[kScaleRing], end;
+  unsigned long long s_full[2], p_full, pv_done, q_full, pages[kRing], end;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -191,9 +191,10 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   extern __shared__ unsigned char smem_raw[];
   __shared__ Bars bars;
   __shared__ long long sPre[kTThreads + 1];
-  __shared__ __align__(16) float sK[kScaleRing][kGroups], sV[kScaleRing][kGroups];
-  __shared__ const uint8_t* sPage[kScaleRing][kGroups];  // K rows of each 16-key group
-  __shared__ float sTop[2][2][kRows];  // what the two threads of a row tell each other
+  __shared__ __align__(16) float sK[kRing][kGroups], sV[kRing][kGroups];
+  __shared__ const uint8_t* sPage[kRing][kGroups];  // K rows of each 16-key group
+  __shared__ int sKeys[kRing], sPrefix[kRing], sFirst[kRing];  // see the lookup
+  __shared__ float sTop[2][2][kRows], sAux[2][2][kRows];  // what the two threads of a row tell each other
   __shared__ uint32_t sTmem;
   __shared__ int sDead, sNan;
   const KvCache& c = a.c;
@@ -213,20 +214,14 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     bar_init(&bars.p_full, kSoftWarps);
     bar_init(&bars.pv_done, 1);
     bar_init(&bars.q_full, kSoftWarps);
-    for (int i = 0; i < kScaleRing; ++i) {
-      bar_init(&bars.scales[i], 1);
-      bar_init(&bars.pages[i], 1);
-    }
+    for (int i = 0; i < kRing; ++i) bar_init(&bars.pages[i], 1);
     bar_init(&bars.end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sDead = 0;
     sNan = 0;
   }
-  Unit u;
-  long t0, t1, unit0, total;
-  int ctas;
-  if (!divide<kRows, kKeys, kTThreads>(a, kLeastTiles, sPre, u, &t0, &t1, &unit0, &total, &ctas))
-    return;
+  Walk<kRows, kKeys, kUnitCost> v;
+  if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, sPre, v)) return;
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sTmem)),
@@ -240,83 +235,84 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sTmem);
   unsigned char* tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   volatile int* dead = &sDead;
+  using Div = Division<kRows, kKeys>;
 
   // The addresses are below 2^18: adding to the descriptor's low bits never carries out of them.
   const uint64_t k_desc = smem_desc(smem_u32(tiles), 16);
   const uint64_t v_desc = smem_desc(smem_u32(tiles) + ST * TL::kBytes, kKeys * 128);
 
-  // Each role walks the same segments (a unit's tiles within the CTA's share);
-  // `n` counts tiles over all of them, `seg` the segments that load a Q.
-  uint32_t n = 0, seg = 0;
-  auto segments = [&](auto role) {
-    for (long at = t0; at < t1;) {
-      const long stop = min(t1, unit0 + u.tiles);
-      role((int)(at - unit0), (int)(stop - unit0), u.w < 0 ? 0u : Div::seen(a, u.seq, u.w, u.mt));
-      at = stop;
-      unit0 += u.tiles;
-      if (u.w >= 0) ++seg;
-      if (at < t1 && !Div::next(a, u)) break;
-    }
-  };
+  // `n` counts tiles over all segments of the CTA's share.
+  uint32_t n = 0;
   if (warp < kSoftWarps) {
-    segments([&](int tile0, int tile1, unsigned) {
-      const int r0 = u.mt * kRows, half = warp >> 2, r = tid & (kRows - 1);
-      const int w = u.w < 0 ? a.W : u.w;
-      const int rows = (int)min((long)kRows, (long)w * a.G - r0);
-      const int i = r < rows ? (r0 + r) / a.G : 0, head = r < rows ? (r0 + r) % a.G : 0;
-      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      constexpr int HD = D / 2;  // elements of D that this thread serves
+    const int half = warp >> 2, r = tid & (kRows - 1);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    constexpr int HD = D / 2;  // elements of D that this thread serves
+    // this thread's row of the segment's unit, and the scale of its scores
+    int r0 = 0, rows = 0, i = 0, head = 0;
+    float qs = 0.f;
+    auto load_q = [&](const Unit& u) {
+      r0 = u.mt * kRows;
+      rows = min(kRows, (u.w < 0 ? a.W : u.w) * a.G - r0);
+      i = r < rows ? (r0 + r) / a.G : 0;
+      head = r < rows ? (r0 + r) % a.G : 0;
+      if (u.w < 0) return;
+      // ---- Q: a power of two per row, rounded to fp16, into tensor memory
+      const uint4* qp = reinterpret_cast<const uint4*>(
+          a.q + 2 * (u.b * a.qb + i * a.qt + ((long)u.h * a.G + head) * a.qh + half * HD));
+      uint4 qv[HD / 8];
+      float top = 0.f;
+#pragma unroll
+      for (int v = 0; v < HD / 8; ++v) qv[v] = r < rows ? qp[v] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int v = 0; v < HD / 8; ++v) {
+        const uint32_t e[4] = {qv[v].x, qv[v].y, qv[v].z, qv[v].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = as_float2(e[k], (T*)nullptr);
+          top = max3(top, fabsf(f.x), fabsf(f.y));
+        }
+      }
+      sAux[0][half][r] = top;
+      pair_sync(warp);
+      top = fmaxf(top, sAux[0][half ^ 1][r]);
+      int e2;
+      frexpf(top, &e2);
+      const int up = top > 0.f && top < INFINITY ? min(15 - e2, 126) : 0;
+      const float f = copysignf(ldexpf(1.f, up), a.scale_log2);
+      qs = fabsf(a.scale_log2) * ldexpf(1.f, -up);  // >= 0: maxima stay maxima
+#pragma unroll
+      for (int v = 0; v < HD / 32; ++v) {
+        uint32_t h[16];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t e[4] = {qv[v * 4 + y].x, qv[v * 4 + y].y, qv[v * 4 + y].z, qv[v * 4 + y].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 p = as_float2(e[k], (T*)nullptr);
+            h[y * 4 + k] = half2_of(p.x * f, p.y * f);
+          }
+        }
+        tmem_st16(lanes + kColQ + half * (HD / 2) + v * 16, h);
+      }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&bars.q_full);
+    };
+    bool more = v.next(a);
+    if (more) load_q(v.u);
+    while (more) {
+      const Unit u = v.u;
+      const int tile0 = v.tile0, tile1 = v.tile1;
+      const bool whole = v.whole();
+      const int last = tile0 == 0 && !whole ? v.last_cta() : 0;
+      const int my_rows = rows, my_i = i, my_head = head;
       float m = -INFINITY, l = 0.f, vref = 0.f;
       bool bad = u.w < 0;
       if (u.w >= 0) {
-        // ---- Q: a power of two per row, rounded to fp16, into tensor memory
-        const uint4* qp = reinterpret_cast<const uint4*>(
-            a.q + 2 * (u.b * a.qb + i * a.qt + ((long)u.h * a.G + head) * a.qh + half * HD));
-        uint4 qv[HD / 8];
-        float top = 0.f;
-#pragma unroll
-        for (int v = 0; v < HD / 8; ++v) qv[v] = r < rows ? qp[v] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int v = 0; v < HD / 8; ++v) {
-          const uint32_t e[4] = {qv[v].x, qv[v].y, qv[v].z, qv[v].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = as_float2(e[k], (T*)nullptr);
-            top = max3(top, fabsf(f.x), fabsf(f.y));
-          }
-        }
-        pair_sync(warp);  // the partner has read what the last unit left here
-        sTop[0][half][r] = top;
-        pair_sync(warp);
-        top = fmaxf(sTop[0][0][r], sTop[0][1][r]);
-        pair_sync(warp);
-        int e2;
-        frexpf(top, &e2);
-        const int up = top > 0.f && top < INFINITY ? min(15 - e2, 126) : 0;
-        const float f = copysignf(ldexpf(1.f, up), a.scale_log2);
-        const float qs = fabsf(a.scale_log2) * ldexpf(1.f, -up);  // >= 0: maxima stay maxima
-#pragma unroll
-        for (int v = 0; v < HD / 32; ++v) {
-          uint32_t h[16];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t e[4] = {qv[v * 4 + y].x, qv[v * 4 + y].y, qv[v * 4 + y].z, qv[v * 4 + y].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 p = as_float2(e[k], (T*)nullptr);
-              h[y * 4 + k] = half2_of(p.x * f, p.y * f);
-            }
-          }
-          tmem_st16(lanes + kColQ + half * (HD / 2) + v * 16, h);
-        }
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bars.q_full);
-
         for (int tile = tile0; tile < tile1; ++tile, ++n) {
-          const int ring = n % kScaleRing;
-          bar_wait(&bars.scales[ring], (n / kScaleRing) & 1, dead);
+          const int ring = n % kRing;
+          bar_wait(&bars.pages[ring], (n / kRing) & 1, dead);
           const float4 k4 = reinterpret_cast<const float4*>(sK[ring])[half];
           const float4 va = reinterpret_cast<const float4*>(sV[ring])[0];
           const float4 vb = reinterpret_cast<const float4*>(sV[ring])[1];
@@ -421,17 +417,21 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
             miss = miss || table[x] < 0 || table[x] >= c.num_blocks;
           bad = __any_sync(~0u, miss);
         }
+      }
+      // The next unit's Q goes in before this one's result comes out: its
+      // first scores are computed meanwhile (all of this unit's are done).
+      more = v.next(a);
+      if (more) load_q(v.u);
+      if (u.w >= 0) {
+        sAux[1][half][r] = l;
         pair_sync(warp);
-        sTop[0][half][r] = l;
-        pair_sync(warp);
-        l = sTop[0][0][r] + sTop[0][1][r];
+        l += sAux[1][half ^ 1][r];
         bar_wait(&bars.pv_done, (n - 1) & 1, dead);
         fence_after();
       }
       if (bad || *dead) l = NAN;
       // ---- the result, or this CTA's part of it
-      const bool whole = tile0 == 0 && tile1 == u.tiles;
-      const size_t orow = ((size_t)u.b * a.W + i) * a.Hq + (size_t)u.h * a.G + head;
+      const size_t orow = ((size_t)u.b * a.W + my_i) * a.Hq + (size_t)u.h * a.G + my_head;
       float* part = a.part + (2 * (size_t)blockIdx.x + (tile0 == 0)) * part_floats<kRows>(D);
       const float f = whole ? (l == 0.f ? 0.f : vref / l) : vref;
       // the window tokens among this segment's keys, for NaN in V
@@ -447,10 +447,10 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
-        if (r < rows) {
+        if (r < my_rows) {
           for (long j = j0; j < j1; ++j) {
-            const bool see = a.masks ? a.masks[((size_t)u.b * a.W + i) * a.words + (j >> 5)] >> (j & 31) & 1
-                                     : j <= i;
+            const bool see = a.masks ? a.masks[((size_t)u.b * a.W + my_i) * a.words + (j >> 5)] >> (j & 31) & 1
+                                     : j <= my_i;
             const int blk = see ? c.block(u.b, u.seq + j) : -1;
             if (blk < 0) continue;
             const uint32_t* v = reinterpret_cast<const uint32_t*>(
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         }
         __syncwarp();
       }
-      if (r < rows && half == 0) {
+      if (r < my_rows && half == 0) {
         if (whole) {
           if (a.lse) a.lse[orow] = row_lse(m, l);
         } else {
@@ -497,185 +497,194 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         d[0] = u.b;
         d[1] = u.h;
         d[2] = u.mt;
-        d[3] = share_owner(total, unit0 + u.tiles - 1, ctas);
+        d[3] = last;
       }
-      fence_before();  // O has been read: the next unit's first product may follow its q_full, p_full
-    });
-  } else {
-    if (warp == kMmaWarp) {
-      segments([&](int tile0, int tile1, unsigned) {
-      if (u.w >= 0) {
+      fence_before();  // O has been read: the next unit's first product follows this thread's p_full
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- the lookup: block ids, then scales, then the ring, a tile apart each, so
+    // that no use waits for its load.  Lane x (< 16): group x % 8, K or V by x / 8.
+    bool more = v.next(a);
+    int tile = 0, keys = 0;          // the tile whose block ids come next
+    int blk = -2, grp1 = 0, info1[3] = {0, 0, 0}, unit_h = 0;  // stage 1; info1[0] = 0: no tile
+    float scale = 0.f;
+    const uint8_t* page = nullptr;
+    int info2[3] = {0, 0, 0};        // stage 2
+    uint32_t posted = 0;
+    bool ended = false;
+    if (more) {
+      while (more && v.u.w < 0) more = v.next(a);
+      if (more) tile = v.tile0, keys = (int)Div::seen(a, v.u.seq, v.u.w, v.u.mt);
+    }
+    auto lookup = [&](bool post) {
+      if (post && !ended) {
+        const int at = posted % kRing;
+        if (lane < 8) sPage[at][lane] = page, sK[at][lane] = scale;
+        else if (lane < 16) sV[at][lane - 8] = scale;
+        // keys of the tile, those before the window, and whether a segment begins;
+        // no keys: the share has ended
+        if (lane == 16) sKeys[at] = info2[0], sPrefix[at] = info2[1], sFirst[at] = info2[2];
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.pages[at]);
+        ended = info2[0] == 0;
+        ++posted;
+      }
+      // a block that does not exist: block 0 is read, and the scores are NaN
+      const bool ok = (unsigned)blk < (unsigned)c.num_blocks;
+      const int off = ok ? (int)(grp1 - col16(a, grp1) * (c.tpb / 16)) * 16 : 0;
+      page = c.pool + ((((size_t)(ok ? blk : 0) * 2) * c.H + unit_h) * c.tpb + off) * D;
+      scale = blk == -2 || lane >= 8 ? 0.f : NAN;
+      if (ok) scale = c.scales[c.scale_at(blk, lane >> 3 & 1, unit_h)];
+#pragma unroll
+      for (int x = 0; x < 3; ++x) info2[x] = info1[x];
+      info1[0] = 0;
+      blk = -2;
+      if (more) {
+        const int k0 = tile * kKeys;
+        info1[0] = min(kKeys, keys - k0);
+        info1[1] = max(0, min(kKeys, v.u.seq - k0));
+        info1[2] = tile == v.tile0;
+        unit_h = v.u.h;
+        grp1 = tile * kGroups + (lane & 7);
+        if (lane < 16 && grp1 * 16 < keys)
+          blk = c.tables[(size_t)v.u.b * c.max_blocks + col16(a, grp1)];
+        if (++tile == v.tile1) {
+          do more = v.next(a);
+          while (more && v.u.w < 0);
+          if (more) tile = v.tile0, keys = (int)Div::seen(a, v.u.seq, v.u.w, v.u.mt);
+        }
+      }
+    };
+    lookup(false);
+    lookup(false);
+    for (int x = 0; x < kAhead; ++x) lookup(true);
+
+    uint32_t seg = 0;
+    auto scores = [&](uint32_t t) {
+      if (sFirst[t % kRing]) {
         bar_wait(&bars.q_full, seg & 1, dead);
-        fence_after();
-        auto scores = [&](uint32_t t) {
-          const uint32_t st = t % ST;
-          bar_wait(&bars.k_full[st], (t / ST) & 1, dead);
-          fence_after();
-          if (elect() && !*dead) {
-            const uint32_t d = tmem + kColS + (t & 1) * kKeys;
-            const uint64_t b = k_desc + st * (TL::kBytes >> 4);
+        ++seg;
+      }
+      const uint32_t st = t % ST;
+      bar_wait(&bars.k_full[st], (t / ST) & 1, dead);
+      fence_after();
+      if (elect() && !*dead) {
+        const uint32_t d = tmem + kColS + (t & 1) * kKeys;
+        const uint64_t b = k_desc + st * (TL::kBytes >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ts(d, tmem + kColQ + k * 8, b + (k / 4) * (kKeys * 128 >> 4) + (k % 4) * (32 >> 4),
-                     instr_desc(kKeys, false), k > 0);
-            mma_commit(&bars.k_empty[st]);
-            mma_commit(&bars.s_full[t & 1]);
-          }
-          __syncwarp();
-        };
-        scores(n);
-        for (int tile = tile0; tile < tile1; ++tile, ++n) {
-          if (tile + 1 < tile1) scores(n + 1);
-          const uint32_t st = n % ST;
-          bar_wait(&bars.v_full[st], (n / ST) & 1, dead);
-          bar_wait(&bars.p_full, n & 1, dead);
-          fence_after();
-          if (elect() && !*dead) {
-            const uint64_t b = v_desc + st * (TL::kBytes >> 4);
+        for (int k = 0; k < D / 16; ++k)
+          mma_ts(d, tmem + kColQ + k * 8, b + (k / 4) * (kKeys * 128 >> 4) + (k % 4) * (32 >> 4),
+                 instr_desc(kKeys, false), k > 0);
+        mma_commit(&bars.k_empty[st]);
+        mma_commit(&bars.s_full[t & 1]);
+      }
+      __syncwarp();
+    };
+    if (sKeys[0] > 0) scores(0);
+    for (; sKeys[n % kRing] > 0; ++n) {
+      const uint32_t next = (n + 1) % kRing;
+      const bool follows = sKeys[next] > 0, first = sFirst[next] != 0;
+      // within a unit the next scores go before this tile's weighted V; a new
+      // unit's wait for its Q, so they go behind
+      if (follows && !first) scores(n + 1);
+      const uint32_t st = n % ST;
+      bar_wait(&bars.v_full[st], (n / ST) & 1, dead);
+      bar_wait(&bars.p_full, n & 1, dead);
+      fence_after();
+      if (elect() && !*dead) {
+        const bool add = sFirst[n % kRing] == 0;
+        const uint64_t b = v_desc + st * (TL::kBytes >> 4);
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + kColO, tmem + kColP + k * 8, b + k * (2048 >> 4), instr_desc(D, true),
-                     tile > tile0 || k > 0);
-            mma_commit(&bars.v_empty[st]);
-            mma_commit(&bars.pv_done);
-          }
-          __syncwarp();
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(tmem + kColO, tmem + kColP + k * 8, b + k * (2048 >> 4), instr_desc(D, true), add || k > 0);
+        mma_commit(&bars.v_empty[st]);
+        mma_commit(&bars.pv_done);
+      }
+      __syncwarp();
+      lookup(true);
+      if (follows && first) scores(n + 1);
+    }
+  } else {
+    // ---- Thread t of the converters: chunk ch (16 bytes) of rows row + kPer p.
+    // Eight neighbours hold four chunks of two rows, which keeps their
+    // 16-byte stores below off each other's banks.
+    constexpr int CPR = D / 16, kPer = kConvThreads / CPR, NP = (kKeys + kPer - 1) / kPer;
+    static_assert(kConvThreads % CPR == 0 && kPer % 4 == 0 && NP <= 8, "converter layout");
+    const int t = tid - kConvWarp * 32;
+    const int ch = D == 128 ? (t & 3) | (t >> 1 & 4) : t & 3;
+    const int row = D == 128 ? (t >> 2 & 1) | t >> 4 << 1 : t >> 2;
+    const size_t v_off = (size_t)c.H * c.tpb * D;  // from a block's K rows to its V rows
+    // the rows of tile `at`; false behind the last
+    auto load = [&](uint4 (&x)[NP], uint4 (&y)[NP], uint32_t at) {
+      bar_wait(&bars.pages[at % kRing], (at / kRing) & 1, dead);
+      if (sKeys[at % kRing] == 0 || *dead) return false;
+      const uint8_t* const* page = sPage[at % kRing];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int r = p * kPer + row;
+        if (p * kPer + kPer <= kKeys || r < kKeys) {
+          const uint8_t* src = page[r >> 4] + ((r & 15) * D + ch * 16);
+          x[p] = *reinterpret_cast<const uint4*>(src);
+          y[p] = *reinterpret_cast<const uint4*>(src + v_off);
         }
       }
-      });
-    } else {
-      segments([&](int tile0, int tile1, unsigned keys) {
-      if (u.w >= 0) {
-        // Thread t of the converters: chunk ch (16 bytes) of rows row + kPer p.
-        // Eight neighbours hold four chunks of two rows, which keeps their
-        // 16-byte stores below off each other's banks.
-        constexpr int CPR = D / 16, kPer = kConvThreads / CPR, NP = (kKeys + kPer - 1) / kPer;
-        static_assert(kConvThreads % CPR == 0 && kPer % 4 == 0 && NP <= 8, "converter layout");
-        const int t = tid - kConvWarp * 32;
-        const int ch = D == 128 ? (t & 3) | (t >> 1 & 4) : t & 3;
-        const int row = D == 128 ? (t >> 2 & 1) | t >> 4 << 1 : t >> 2;
-        const int tpb16 = c.tpb / 16;
-        const int32_t* table = c.tables + (size_t)u.b * c.max_blocks;
-        const size_t v_off = (size_t)c.H * c.tpb * D;  // from a block's K rows to its V rows
-
-        // ---- one warp keeps the tiles' pages: lane's group and kind
-        int pblk = -1, sblk = -1;  // block ids, loaded a tile before they are looked at
-        float scale = 0.f;
-        auto group_block = [&](int tile) {
-          const unsigned grp = (unsigned)tile * kGroups + (lane & 7);
-          return lane < 16 && tile < tile1 && grp * 16 < keys ? table[col16(a, grp)] : -2;  // -2: no such keys
-        };
-        auto load_scale = [&]() {
-          scale = sblk == -2 || lane >= 8 ? 0.f : NAN;  // a block that does not exist makes the scores NaN
-          if ((unsigned)sblk < (unsigned)c.num_blocks) scale = c.scales[c.scale_at(sblk, lane >> 3, u.h)];
-        };
-        auto post_pages = [&](int tile, uint32_t at) {
-          if (tile >= tile1) return;
-          // Groups without a block read block 0: their scores are masked or NaN.
-          const unsigned grp = (unsigned)tile * kGroups + (lane & 7);
-          const bool ok = (unsigned)pblk < (unsigned)c.num_blocks;
-          const size_t off = ((size_t)(ok ? pblk : 0) * 2 * c.H + u.h) * c.tpb +
-                             (ok ? (grp - col16(a, grp) * tpb16) * 16 : 0);
-          if (lane < 8) sPage[at % kScaleRing][lane] = c.pool + off * D;
-          __syncwarp();
-          if (lane == 0) bar_arrive(&bars.pages[at % kScaleRing]);
-        };
-
-        auto load = [&](uint4 (&x)[NP], uint4 (&y)[NP], int tile, uint32_t at) {
-          if (tile >= tile1) return;
-          bar_wait(&bars.pages[at % kScaleRing], (at / kScaleRing) & 1, dead);
-          const uint8_t* const* page = sPage[at % kScaleRing];
+      return true;
+    };
+    // places of the two fp16 vectors of row `row`; row + kPer is kPer % 8 = 4 rows on in the swizzle
+    const int atom = (ch >> 2) * (kKeys * 128) + row * 128, c0 = (ch & 3) * 2;
+    const int o0 = atom + ((c0 ^ (row & 7)) << 4), o1 = atom + (((c0 + 1) ^ (row & 7)) << 4);
+    auto put = [&](const uint4 (&x)[NP], unsigned char* tile) {
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            const int r = p * kPer + row;
-            if (p * kPer + kPer <= kKeys || r < kKeys) {
-              const uint8_t* src = page[r >> 4] + ((r & 15) * D + ch * 16);
-              x[p] = *reinterpret_cast<const uint4*>(src);
-              y[p] = *reinterpret_cast<const uint4*>(src + v_off);
-            }
-          }
-        };
-        // places of the two fp16 vectors of row `row`; row + kPer is kPer % 8 = 4 rows on in the swizzle
-        const int atom = (ch >> 2) * (kKeys * 128) + row * 128, c0 = (ch & 3) * 2;
-        const int o0 = atom + ((c0 ^ (row & 7)) << 4), o1 = atom + (((c0 + 1) ^ (row & 7)) << 4);
-        auto put = [&](const uint4 (&x)[NP], unsigned char* tile) {
+      for (int p = 0; p < NP; ++p) {
+        if (p * kPer + kPer <= kKeys || p * kPer + row < kKeys) {
+          const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+          uint32_t h[8];
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            if (p * kPer + kPer <= kKeys || p * kPer + row < kKeys) {
-              const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-              uint32_t h[8];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) e4m3x4_to_half(w[k], h[2 * k], h[2 * k + 1]);
-              const int flip = p * kPer & 4 ? 64 : 0;
-              *reinterpret_cast<uint4*>(tile + p * kPer * 128 + (o0 ^ flip)) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(tile + p * kPer * 128 + (o1 ^ flip)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        };
-        // Two tiles are on their way in registers while a third is written.
-        auto step = [&](uint4 (&kr)[NP], uint4 (&vr)[NP], int tile) {
-          const uint32_t st = n % ST, ring = n % kScaleRing;
-          if (warp == kConvWarp) {
-            if (lane < 8) sK[ring][lane] = scale;
-            else if (lane < 16) sV[ring][lane - 8] = scale;
-            __syncwarp();
-            if (lane == 0) bar_arrive(&bars.scales[ring]);
-            load_scale();
-            sblk = group_block(tile + 2);
-            post_pages(tile + 3, n + 3);
-            pblk = group_block(tile + 4);
-          }
-          bar_wait(&bars.k_empty[st], ((n / ST) & 1) ^ 1, dead);
-          put(kr, tiles + st * TL::kBytes);
-          if (lane == 0) bar_arrive(&bars.k_full[st]);
-          if ((tile + 1) * kKeys > u.seq) {
-            // Rows behind the keys hold anything; they are zero here.  NaN in a
-            // window row: only the rows that see it may get it (see the result).
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              const unsigned key = (unsigned)tile * kKeys + p * kPer + row;
-              uint32_t w[4] = {vr[p].x, vr[p].y, vr[p].z, vr[p].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t nb = key >= keys ? 0x80808080u : key >= (unsigned)u.seq ? nan_bytes(w[k]) : 0u;
-                if (nb && key < keys && p * kPer + row < kKeys) sNan = 1;
-                w[k] &= ~((nb >> 7) * 255u);
-              }
-              vr[p] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          bar_wait(&bars.v_empty[st], ((n / ST) & 1) ^ 1, dead);
-          put(vr, tiles + (ST + st) * TL::kBytes);
-          if (lane == 0) bar_arrive(&bars.v_full[st]);
-          load(kr, vr, tile + 2, n + 2);
-          ++n;
-        };
-        uint4 ka[NP], va[NP], kb[NP], vb[NP];
-        if (warp == kConvWarp) {
-          int b3[3];
-#pragma unroll
-          for (int x = 0; x < 3; ++x) b3[x] = group_block(tile0 + x);
-          const int b4 = group_block(tile0 + 3);
-#pragma unroll
-          for (int x = 0; x < 3; ++x) {
-            pblk = b3[x];
-            post_pages(tile0 + x, n + x);
-          }
-          pblk = b4;
-          sblk = b3[0];
-          load_scale();
-          sblk = b3[1];
-        }
-        load(ka, va, tile0, n);
-        load(kb, vb, tile0 + 1, n + 1);
-        for (int tile = tile0; tile < tile1; tile += 2) {
-          step(ka, va, tile);
-          if (tile + 1 < tile1) step(kb, vb, tile + 1);
+          for (int k = 0; k < 4; ++k) e4m3x4_to_half(w[k], h[2 * k], h[2 * k + 1]);
+          const int flip = p * kPer & 4 ? 64 : 0;
+          *reinterpret_cast<uint4*>(tile + p * kPer * 128 + (o0 ^ flip)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(tile + p * kPer * 128 + (o1 ^ flip)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
-      });
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
+    // Writes tile n and starts to load tile n + 2 into the same registers:
+    // two tiles are on their way while a third is written.
+    auto step = [&](uint4 (&kr)[NP], uint4 (&vr)[NP], bool follows) {
+      const uint32_t st = n % ST;
+      bar_wait(&bars.k_empty[st], ((n / ST) & 1) ^ 1, dead);
+      put(kr, tiles + st * TL::kBytes);
+      if (lane == 0) bar_arrive(&bars.k_full[st]);
+      const int keys = sKeys[n % kRing], prefix = sPrefix[n % kRing];
+      if (prefix < kKeys) {
+        // Rows behind the keys hold anything; they are zero here.  NaN in a
+        // window row: only the rows that see it may get it (see the result).
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          const int key = p * kPer + row;
+          uint32_t w[4] = {vr[p].x, vr[p].y, vr[p].z, vr[p].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t nb = key >= keys ? 0x80808080u : key >= prefix ? nan_bytes(w[k]) : 0u;
+            if (nb && key < keys) sNan = 1;
+            w[k] &= ~((nb >> 7) * 255u);
+          }
+          vr[p] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      bar_wait(&bars.v_empty[st], ((n / ST) & 1) ^ 1, dead);
+      put(vr, tiles + (ST + st) * TL::kBytes);
+      if (lane == 0) bar_arrive(&bars.v_full[st]);
+      ++n;
+      return follows && load(kr, vr, n + 1);
+    };
+    uint4 ka[NP], va[NP], kb[NP], vb[NP];
+    bool in_a = load(ka, va, 0), in_b = in_a && load(kb, vb, 1);
+    while (in_a) {
+      in_a = step(ka, va, in_b);
+      if (!in_b) break;
+      in_b = step(kb, vb, in_a);
     }
   }
 
