@@ -25,14 +25,14 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
-constexpr int kUnitCost = 1;             // cells of a unit besides its tiles
-constexpr int kLeastCells = 3;
+constexpr int kUnitCost = 4;             // cells of a unit besides its tiles
+constexpr int kLeastCells = 6;
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarp = 9, kConvWarps = 7;
 constexpr int kTThreads = (kConvWarp + kConvWarps) * 32;
 constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kGroups = kKeys / 16;      // scale groups of a tile
-constexpr int kRing = 8;                 // tiles whose pages and scales are kept
-constexpr int kAhead = 4;                // tiles that they are looked up ahead of the products
+constexpr int kRing = 16;                // tiles whose pages and scales are kept
+constexpr int kAhead = 8;                // fewer than these are known ahead: more are looked up
 constexpr uint32_t kColQ = 0, kColP = 64, kColS = 128, kColO = 384, kCols = 512;
 
 template <int D>
@@ -91,7 +91,7 @@ __device__ __forceinline__ void tmem_ld32(float* r, uint32_t addr) {
       : "r"(addr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16};" ::"r"(addr),
@@ -164,6 +164,11 @@ __device__ __forceinline__ void pair_sync(int warp) {
   asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
 }
 
+// Keys of a unit, from the first, that each of its rows sees.
+__device__ __forceinline__ int seen_by_all(const AttendArgs& a, const Unit& u) {
+  return u.seq + (a.masks ? 0 : u.mt * kRows / a.G + 1);
+}
+
 // Bit k: the row of window token i sees window place j + k (all of the prefix,
 // j + k < 0, is seen).
 __device__ __noinline__ unsigned seen_bits(const AttendArgs& a, const Unit& u, int i, long j) {
@@ -191,7 +196,10 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   extern __shared__ unsigned char smem_raw[];
   __shared__ Bars bars;
   __shared__ long long sPre[kTThreads + 1];
-  __shared__ __align__(16) float sK[kRing][kGroups], sV[kRing][kGroups];
+  // of each 16-key group: K's scale; V's scale over the largest so far in the segment, as log2
+  // and as 1 / x; that largest scale, and the last one over it
+  __shared__ __align__(16) float sK[kRing][kGroups], sLog[kRing][kGroups], sInv[kRing][kGroups];
+  __shared__ float sRef[kRing], sGrow[kRing];
   __shared__ const uint8_t* sPage[kRing][kGroups];  // K rows of each 16-key group
   __shared__ int sKeys[kRing], sPrefix[kRing], sFirst[kRing];  // see the lookup
   __shared__ float sTop[2][2][kRows], sAux[2][2][kRows];  // what the two threads of a row tell each other
@@ -314,11 +322,11 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
           const int ring = n % kRing;
           bar_wait(&bars.pages[ring], (n / kRing) & 1, dead);
           const float4 k4 = reinterpret_cast<const float4*>(sK[ring])[half];
-          const float4 va = reinterpret_cast<const float4*>(sV[ring])[0];
-          const float4 vb = reinterpret_cast<const float4*>(sV[ring])[1];
-          const float vmax = fmaxf(max3(max3(va.x, va.y, va.z), va.w, vb.x), max3(vb.y, vb.z, vb.w));
-          const float4 v4 = half ? vb : va;
+          const float4 log4 = reinterpret_cast<const float4*>(sLog[ring])[half];
+          const float4 inv4 = reinterpret_cast<const float4*>(sInv[ring])[half];
+          const float grow = sGrow[ring];
           float kf[4] = {k4.x * qs, k4.y * qs, k4.z * qs, k4.w * qs};
+          const float lv[4] = {log4.x, log4.y, log4.z, log4.w}, iv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
 #pragma unroll
           for (int y = 0; y < 4; ++y)  // -inf times it stays -inf; NaN (no such block) stays NaN
             kf[y] = kf[y] < 0x1p-120f ? 0x1p-120f : kf[y];
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
           tmem_ld32(s + 32, lanes + kColS + (n & 1) * kKeys + half * 64 + 32);
           tmem_wait_ld();
           const long k0 = (long)tile * kKeys + half * 64 - u.seq;  // window place of s[0]
-          if (k0 + 64 > 0) {
+          if ((tile + 1) * kKeys > seen_by_all(a, u)) {
 #pragma unroll
             for (int x = 0; x < 64; x += 32) {
               const unsigned bits = seen_bits(a, u, i, k0 + x);
@@ -353,15 +361,13 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
           pair_sync(warp);
           top = fmaxf(top, sTop[n & 1][half ^ 1][r]);
           const bool move = top > m + kLazy;
-          const bool wide = vmax > vref;
-          if (__any_sync(~0u, move || wide)) {
+          if (__any_sync(~0u, move || grow != 1.f)) {
             const float now = move ? top : m;
             const float al = move ? ex2(m - now) : 1.f;
-            const float ar = al * (wide ? vref / vmax : 1.f);
             m = now;
             l *= al;
-            if (wide) vref = vmax;
             if (tile > tile0) {
+              const float ar = al * grow;
               bar_wait(&bars.pv_done, (n - 1) & 1, dead);
               fence_after();
 #pragma unroll 1
@@ -375,19 +381,14 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               }
             }
           }
-          // The V scale's ratio goes into the exponent, and out of the sum again.
-          // Where it is below 2^-40 it is taken as that: such a block adds at most
-          // 2^-40 of the largest |V|.
+          // V's scale goes into the exponent, and out of the sum again
           const float add = m == -INFINITY ? 0.f : kPBits - m;
-          const float inv_vref = vref > 0.f ? 1.f / vref : 1.f;
-          const float vr[4] = {fmaxf(v4.x * inv_vref, 0x1p-40f), fmaxf(v4.y * inv_vref, 0x1p-40f),
-                               fmaxf(v4.z * inv_vref, 0x1p-40f), fmaxf(v4.w * inv_vref, 0x1p-40f)};
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             uint32_t p[16];
 #pragma unroll
             for (int y = 2 * z; y < 2 * z + 2; ++y) {
-              const float av = add + __log2f(vr[y]);
+              const float av = add + lv[y];
               float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
                 sum = add2(sum, e);
                 p[(x & 31) / 2] = half2_of(e.x, e.y);
               }
-              l += __fdividef(sum.x + sum.y, vr[y]);
+              l = fmaf(sum.x + sum.y, iv[y], l);
             }
             if (z == 0) {  // P has one buffer: the last tile's product has read it
               if (n > 0) bar_wait(&bars.pv_done, (n - 1) & 1, dead);
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         l += sAux[1][half ^ 1][r];
         bar_wait(&bars.pv_done, (n - 1) & 1, dead);
         fence_after();
+        vref = sRef[(n - 1) % kRing];
       }
       if (bad || *dead) l = NAN;
       // ---- the result, or this CTA's part of it
@@ -502,62 +504,99 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       fence_before();  // O has been read: the next unit's first product follows this thread's p_full
     }
   } else if (warp == kMmaWarp) {
-    // ---- the lookup: block ids, then scales, then the ring, a tile apart each, so
-    // that no use waits for its load.  Lane x (< 16): group x % 8, K or V by x / 8.
+    // ---- the lookup, up to four tiles of a segment at a time: block ids, then
+    // scales, then the ring, a call apart each, so that no use waits for its
+    // load.  Lane x: group x % 8 of the batch's tile x / 8.
     bool more = v.next(a);
-    int tile = 0, keys = 0;          // the tile whose block ids come next
-    int blk = -2, grp1 = 0, info1[3] = {0, 0, 0}, unit_h = 0;  // stage 1; info1[0] = 0: no tile
-    float scale = 0.f;
-    const uint8_t* page = nullptr;
-    int info2[3] = {0, 0, 0};        // stage 2
-    uint32_t posted = 0;
-    bool ended = false;
-    if (more) {
+    auto skip = [&]() {
       while (more && v.u.w < 0) more = v.next(a);
-      if (more) tile = v.tile0, keys = (int)Div::seen(a, v.u.seq, v.u.w, v.u.mt);
-    }
+    };
+    skip();
+    int tile = more ? v.tile0 : 0, keys = more ? (int)Div::seen(a, v.u.seq, v.u.w, v.u.mt) : 0;
+    const int my_tile = lane >> 3;
+    // stage 1: block ids under way
+    int blk = -2, grp1 = 0, unit_h = 0, count1 = 0, keys1 = 0, all1 = 0;
+    bool first1 = false;
+    // stage 2: scales under way
+    const uint8_t* page = nullptr;
+    float k_scale = 0.f, v_scale = 0.f;
+    int count2 = 0, keys2 = 0, all2 = 0;
+    bool first2 = false;
+    uint32_t posted = 0;
+    float ref = 0.f;
+    bool ended = false;
     auto lookup = [&](bool post) {
       if (post && !ended) {
-        const int at = posted % kRing;
-        if (lane < 8) sPage[at][lane] = page, sK[at][lane] = scale;
-        else if (lane < 16) sV[at][lane - 8] = scale;
-        // keys of the tile, those before the window, and whether a segment begins;
+        // V's scales against the segment's largest so far; below 2^-40 of it they
+        // are taken as that (such a block adds at most 2^-40 of the largest |V|)
+        float top = my_tile < count2 ? v_scale : 0.f;
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+        float last = first2 ? 0.f : ref;  // before this lane's tile
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          const float y = __shfl_sync(~0u, top, x * 8);
+          if (x < my_tile) last = fmaxf(last, y);
+        }
+        const float mine = fmaxf(last, top);
+        ref = __shfl_sync(~0u, mine, 31);
+        const float over = mine > 0.f ? __fdividef(1.f, mine) : 0.f;
+        const float vr = mine > 0.f ? fmaxf(v_scale * over, 0x1p-40f) : 1.f;
+        const int at = (posted + my_tile) % kRing, g = lane & 7;
+        if (my_tile < count2) {
+          sPage[at][g] = page;
+          sK[at][g] = k_scale;
+          sLog[at][g] = __log2f(vr);
+          sInv[at][g] = __fdividef(1.f, vr);
+          if (g == 0) sRef[at] = mine, sGrow[at] = mine > last ? last * over : 1.f;
+        }
+        // keys of the tile, those that every row sees, and whether a segment begins;
         // no keys: the share has ended
-        if (lane == 16) sKeys[at] = info2[0], sPrefix[at] = info2[1], sFirst[at] = info2[2];
+        if (g == 0 && my_tile < max(count2, 1)) {
+          sKeys[at] = count2 == 0 ? 0 : min(kKeys, keys2 - my_tile * kKeys);
+          sPrefix[at] = max(0, min(kKeys, all2 - my_tile * kKeys));
+          sFirst[at] = first2 && my_tile == 0;
+        }
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars.pages[at]);
-        ended = info2[0] == 0;
-        ++posted;
+        if (g == 0 && my_tile < max(count2, 1)) bar_arrive(&bars.pages[at]);
+        ended = count2 == 0;
+        posted += max(count2, 1);
       }
       // a block that does not exist: block 0 is read, and the scores are NaN
       const bool ok = (unsigned)blk < (unsigned)c.num_blocks;
       const int off = ok ? (int)(grp1 - col16(a, grp1) * (c.tpb / 16)) * 16 : 0;
       page = c.pool + ((((size_t)(ok ? blk : 0) * 2) * c.H + unit_h) * c.tpb + off) * D;
-      scale = blk == -2 || lane >= 8 ? 0.f : NAN;
-      if (ok) scale = c.scales[c.scale_at(blk, lane >> 3 & 1, unit_h)];
-#pragma unroll
-      for (int x = 0; x < 3; ++x) info2[x] = info1[x];
-      info1[0] = 0;
+      k_scale = blk == -2 ? 0.f : NAN;
+      v_scale = 0.f;
+      if (ok) {
+        const float* sp = c.scales + c.scale_at(blk, 0, unit_h);
+        k_scale = sp[0];
+        v_scale = sp[c.H];
+      }
+      count2 = count1, keys2 = keys1, all2 = all1, first2 = first1;
+      count1 = 0;
       blk = -2;
       if (more) {
         const int k0 = tile * kKeys;
-        info1[0] = min(kKeys, keys - k0);
-        info1[1] = max(0, min(kKeys, v.u.seq - k0));
-        info1[2] = tile == v.tile0;
+        count1 = min(4, v.tile1 - tile);
+        keys1 = keys - k0;
+        all1 = seen_by_all(a, v.u) - k0;
+        first1 = tile == v.tile0;
         unit_h = v.u.h;
-        grp1 = tile * kGroups + (lane & 7);
-        if (lane < 16 && grp1 * 16 < keys)
+        grp1 = tile * kGroups + lane;
+        if (my_tile < count1 && grp1 * 16 < keys)
           blk = c.tables[(size_t)v.u.b * c.max_blocks + col16(a, grp1)];
-        if (++tile == v.tile1) {
-          do more = v.next(a);
-          while (more && v.u.w < 0);
+        tile += count1;
+        if (tile == v.tile1) {
+          more = v.next(a);
+          skip();
           if (more) tile = v.tile0, keys = (int)Div::seen(a, v.u.seq, v.u.w, v.u.mt);
         }
       }
     };
     lookup(false);
     lookup(false);
-    for (int x = 0; x < kAhead; ++x) lookup(true);
+    while (posted < kAhead && !ended) lookup(true);
 
     uint32_t seg = 0;
     auto scores = [&](uint32_t t) {
@@ -587,6 +626,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       // within a unit the next scores go before this tile's weighted V; a new
       // unit's wait for its Q, so they go behind
       if (follows && !first) scores(n + 1);
+      if (posted < n + kAhead && !ended) lookup(true);  // while the weights are computed
       const uint32_t st = n % ST;
       bar_wait(&bars.v_full[st], (n / ST) & 1, dead);
       bar_wait(&bars.p_full, n & 1, dead);
@@ -601,7 +641,6 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         mma_commit(&bars.pv_done);
       }
       __syncwarp();
-      lookup(true);
       if (follows && first) scores(n + 1);
     }
   } else {
@@ -658,8 +697,8 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       if (lane == 0) bar_arrive(&bars.k_full[st]);
       const int keys = sKeys[n % kRing], prefix = sPrefix[n % kRing];
       if (prefix < kKeys) {
-        // Rows behind the keys hold anything; they are zero here.  NaN in a
-        // window row: only the rows that see it may get it (see the result).
+        // Rows behind the keys hold anything; they are zero here.  NaN in a key
+        // that not every row sees: only those that do may get it (see the result).
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const int key = p * kPer + row;
