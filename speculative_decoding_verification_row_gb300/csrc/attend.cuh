@@ -164,7 +164,7 @@ __device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long
   const long most = total / least > 1 ? total / least : 1;
   const int ctas = most < (long)gridDim.x ? (int)most : (int)gridDim.x;
   if (total == 0 || (int)blockIdx.x >= ctas) return false;
-  v.total = total;
+  v.total = total;  // every thread stores the same
   v.ctas = ctas;
   v.at = share_begin(total, blockIdx.x, ctas);
   v.end = share_begin(total, blockIdx.x + 1, ctas);

@@ -117,16 +117,22 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
   const int g = lane >> 2, cc = lane & 3;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Walk<kRows, kKeys, kUnitCost> v;
+  // the walk lies in shared memory: its 20 words are needed between segments only
+  __shared__ Walk<kRows, kKeys, kUnitCost> v;
+  __shared__ int sMore;
   if (tid < kDescWords) a.desc[blockIdx.x * kDescWords + tid] = -1;
   if (!divide<kRows, kKeys, kUnitCost, kRThreads>(a, kLeastCells, sPre, v)) return;
-  const Unit& u = v.u;
+  __syncthreads();  // every thread has stored the walk's beginning
   unsigned char* ring = smem + warp * R::kWarp;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   const int tpb16 = c.tpb / kStep;
   const size_t v_off = (size_t)c.H * c.tpb * D;  // from a block's K rows to its V rows
 
-  while (v.next(a)) {
+  for (;;) {
+    if (tid == 0) sMore = v.next(a);
+    __syncthreads();
+    if (!sMore) break;
+    const Unit u = v.u;
     const int tile0 = v.tile0, tile1 = v.tile1;
     const int r0 = u.mt * kRows;
     const int w = u.w < 0 ? a.W : u.w;
