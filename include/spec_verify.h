@@ -548,7 +548,8 @@ int spec_store_kv(const spec_kv_cache *cache, const void *k, const int64_t *k_st
  *   during the call only; it need not be initialised and may hold anything,
  *   but calls that overlap on the GPU must not share it, and it must not be
  *   the workspace of a verify call.  Results do not depend on timing: equal
- *   inputs give equal bits. */
+ *   inputs give equal bits.
+ * Limits: max_blocks * tokens_per_block and B * W * q_heads at most 2^30. */
 typedef struct spec_attend_params {
     size_t size;
     const void *q;

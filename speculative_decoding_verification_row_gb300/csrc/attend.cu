@@ -31,7 +31,8 @@ int spec_attend_kv(const spec_kv_cache* cache, const spec_attend_params* p, void
       (p->dtype != SPEC_BF16 && p->dtype != SPEC_F16) || !p->seq_lens || !p->out ||
       reinterpret_cast<uintptr_t>(p->out) % 16 != 0 || !isfinite(p->scale) ||
       (p->masks && p->W > SPEC_MAX_TREE_NODES) ||
-      (long)a.c.max_blocks * a.c.tpb > kMaxPositions)
+      (long)a.c.max_blocks * a.c.tpb > kMaxPositions ||
+      (long)p->B * p->W * p->q_heads > kMaxRows)
     return SPEC_EINVAL;
   const size_t need = spec_attend_scratch_size(p->B, p->W, p->q_heads, a.c.H, a.c.D);
   if (need == 0) return SPEC_EINVAL;

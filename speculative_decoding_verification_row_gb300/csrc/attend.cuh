@@ -30,6 +30,8 @@ __device__ __forceinline__ unsigned col16(const AttendArgs& a, unsigned x) {
   return a.c.tpb == 16 ? x : __umulhi(x, a.tpb16_div);
 }
 constexpr long kMaxPositions = 1l << 30;
+// Most rows (tokens times query heads) of a call: its outputs would be 128 GB.
+constexpr long kMaxRows = 1l << 30;
 
 // Rows of one request and KV head are numbered r = i * G + g (window token i,
 // query head g of the group) and cut into tiles of ROWS; a "unit" is one such
@@ -80,11 +82,28 @@ struct Division {
   }
 };
 
-// Share of CTA i of n over a line of `total` cells, and the owner of a cell.
-__device__ __forceinline__ long share_begin(long total, int i, int n) { return total * i / n; }
-__device__ __forceinline__ int share_owner(long total, long cell, int n) {
-  return (int)(((cell + 1) * n - 1) / total);
+// x / n: 32-bit arithmetic where it suffices (a 64-bit division takes hundreds of clocks).
+__device__ __forceinline__ long quotient(long x, long n) {
+  return (x | n) >> 31 ? x / n : (long)((unsigned)x / (unsigned)n);
 }
+// A line of `total` cells in n shares: the first `more` of them hold one cell
+// more than `each`.
+struct Shares {
+  long total, each;
+  int n, more;
+  __device__ __forceinline__ void set(long cells, int shares) {
+    total = cells;
+    n = shares;
+    each = quotient(cells, shares);
+    more = (int)(cells - each * shares);
+  }
+  __device__ __forceinline__ long begin(int i) const { return each * i + min(i, more); }
+  // The share that holds a cell.
+  __device__ __forceinline__ int owner(long cell) const {
+    const long wide = (each + 1) * more;  // cells of the longer shares
+    return cell < wide ? (int)quotient(cell, each + 1) : more + (int)quotient(cell - wide, each);
+  }
+};
 
 // A CTA's share of the line.  A unit takes COST cells (for loading its rows
 // and writing its result) and one for each of its key tiles; the tiles of a
@@ -94,8 +113,7 @@ struct Walk {
   Unit u;
   long at, end;      // the share's cells not yet walked
   long unit0;        // first cell of u
-  long total;
-  int ctas;
+  Shares shares;
   int tile0, tile1;  // the segment
   // To the next segment; false at the share's end.
   __device__ __forceinline__ bool next(const AttendArgs& a) {
@@ -117,36 +135,35 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == u.tiles; }
   // The CTA that holds the unit's last tile.
   __device__ __forceinline__ int last_cta() const {
-    return share_owner(total, unit0 + COST + u.tiles - 1, ctas);
+    return shares.owner(unit0 + COST + u.tiles - 1);
   }
 };
 
 // Sets a CTA of THREADS threads before the first segment of its share.
-// False: nothing to do.  sPre: THREADS + 1 words.  `least`: cells below which
-// a share is not worth a CTA.  Every CTA sums the line anew, (request, row
+// False: nothing to do.  `least`: cells below which a share is not worth a
+// CTA.  Every CTA sums the line anew, (request, row
 // tile) pairs over its threads: no state between launches and none to clear.
 template <int ROWS, int KEYS, int COST, int THREADS>
-__device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long* sPre,
-                                       Walk<ROWS, KEYS, COST>& v) {
+__device__ __forceinline__ bool divide(const AttendArgs& a, int least, Walk<ROWS, KEYS, COST>& v) {
   using Div = Division<ROWS, KEYS>;
   __shared__ long long sWarp[THREADS / 32];
-  __shared__ int sFind[3];
+  __shared__ int sFind[6];
   __shared__ long long sUnit0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long items = (long)a.B * a.mtiles, per = (items + THREADS - 1) / THREADS;
-  const long x0 = min(items, tid * per), x1 = min(items, x0 + per);
-  // calls f(b, mt, cells) for this thread's pairs until f returns false
+  const int items = a.B * a.mtiles;  // fits: see kMaxRows
+  const int per = (unsigned)(items + THREADS - 1) / (unsigned)THREADS;
+  const int x0 = min(items, tid * per), x1 = min(items, x0 + per);
+  // calls f(b, mt, seq, w, tiles) for this thread's pairs until f returns false
   auto pairs = [&](auto f) {
-    int b = (int)(x0 / a.mtiles), mt = (int)(x0 % a.mtiles), seq = 0, w = 0;
-    for (long x = x0; x < x1; ++x) {
+    int b = (unsigned)x0 / (unsigned)a.mtiles, mt = x0 - b * a.mtiles, seq = 0, w = 0;
+    for (int x = x0; x < x1; ++x) {
       if (x == x0 || mt == 0) Div::lens(a, b, &seq, &w);
-      const int n = Div::tiles(a, seq, w, mt);
-      if (!f(b, mt, n > 0 ? n + COST : 0)) return;
+      if (!f(b, mt, seq, w, Div::tiles(a, seq, w, mt))) return;
       if (++mt == a.mtiles) mt = 0, ++b;
     }
   };
   long long mine = 0;
-  pairs([&](int, int, int n) { return mine += n, true; });
+  pairs([&](int, int, int, int, int n) { return mine += n > 0 ? n + COST : 0, true; });
   mine *= a.c.H;
   long long incl = mine;
 #pragma unroll
@@ -156,37 +173,40 @@ __device__ __forceinline__ bool divide(const AttendArgs& a, int least, long long
   }
   if (lane == 31) sWarp[warp] = incl;
   __syncthreads();
-  for (int i = 0; i < warp; ++i) incl += sWarp[i];
-  sPre[tid] = incl - mine;
-  if (tid == THREADS - 1) sPre[THREADS] = incl;
-  __syncthreads();
-  const long total = sPre[THREADS];
-  const long most = total / least > 1 ? total / least : 1;
-  const int ctas = most < (long)gridDim.x ? (int)most : (int)gridDim.x;
+  long long total = 0;
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) {
+    if (i < warp) incl += sWarp[i];
+    total += sWarp[i];
+  }
+  const long most = quotient(total, least);
+  const int ctas = most < 1 ? 1 : most < (long)gridDim.x ? (int)most : (int)gridDim.x;
   if (total == 0 || (int)blockIdx.x >= ctas) return false;
-  v.total = total;  // every thread stores the same
-  v.ctas = ctas;
-  v.at = share_begin(total, blockIdx.x, ctas);
-  v.end = share_begin(total, blockIdx.x + 1, ctas);
-  if (sPre[tid] <= v.at && v.at < sPre[tid + 1]) {  // one thread: its pairs hold the share's first cell
-    long at = sPre[tid];
-    pairs([&](int b, int mt, int n) {
-      if (v.at >= at + (long)n * a.c.H) return at += (long)n * a.c.H, true;
-      const int h = (int)((v.at - at) / n);
+  Shares s;
+  s.set(total, ctas);
+  const long begin = s.begin(blockIdx.x);
+  if (incl - mine <= begin && begin < incl) {  // one thread: its pairs hold the share's first cell
+    long at = incl - mine;
+    pairs([&](int b, int mt, int seq, int w, int n) {
+      const int cells = n > 0 ? n + COST : 0;
+      if (begin >= at + (long)cells * a.c.H) return at += (long)cells * a.c.H, true;
+      const int h = (int)quotient(begin - at, cells);
       sFind[0] = b;
       sFind[1] = h;
       sFind[2] = mt;
-      sUnit0 = at + (long)h * n;
+      sFind[3] = seq;
+      sFind[4] = w;
+      sFind[5] = n;
+      sUnit0 = at + (long)h * cells;
       return false;
     });
   }
   __syncthreads();
-  v.u.b = sFind[0];
-  v.u.h = sFind[1];
-  v.u.mt = sFind[2];
+  v.shares = s;  // every thread stores the same
+  v.at = begin;
+  v.end = s.begin(blockIdx.x + 1);
   v.unit0 = sUnit0;
-  Div::lens(a, v.u.b, &v.u.seq, &v.u.w);
-  v.u.tiles = Div::tiles(a, v.u.seq, v.u.w, v.u.mt);
+  v.u = Unit{sFind[0], sFind[1], sFind[2], sFind[3], sFind[4], sFind[5]};
   return true;
 }
 
@@ -197,8 +217,8 @@ constexpr float kLazy = 7.f;     // ... with m at most 7 below the row's largest
 template <int ROWS>
 __host__ __device__ constexpr size_t part_floats(int D) { return (size_t)ROWS * (D + 2); }
 
-// desc words per CTA: {request, head, row tile, last CTA of the unit}; -1: none.
-constexpr int kDescWords = 4;
+// desc words per CTA: {request, head, row tile, last CTA of the unit, its rows}; -1: none.
+constexpr int kDescWords = 8;
 
 __device__ __forceinline__ uint32_t pack_out(float x, float y, __nv_bfloat16*) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
@@ -216,33 +236,37 @@ __device__ __forceinline__ float row_lse(float M, float L) {
 
 // Joins the units that several CTAs worked on: CTA (i, y) serves rows
 // [16 y, 16 y + 16) of the unit that began in CTA i and did not end there.
-// The parts are read in CTA order, so the result does not depend on timing.
-constexpr int kJoinThreads = 128;
+// Four threads sets take every fourth part, all of a set's loads in flight
+// together, and are joined in turn: in an order that depends on the division
+// alone, so the result does not depend on timing.
 constexpr int kJoinRows = 16;
+constexpr int kJoinSets = 4;
+constexpr int kJoinThreads = kJoinRows * 8 * kJoinSets;
 
 template <class T, int D, int ROWS, int KEYS>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a) {
   constexpr int NT = D / 8;  // elements per thread, 8 threads per row
+  __shared__ float sM[kJoinSets][kJoinRows], sL[kJoinSets][kJoinRows];
+  __shared__ __align__(16) float sX[kJoinSets - 1][kJoinRows * 8][NT + 4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int first = blockIdx.x;
-  const int4 d = *reinterpret_cast<const int4*>(a.desc + first * kDescWords);
+  const int4 d = reinterpret_cast<const int4*>(a.desc)[2 * first];
   if (d.x < 0) return;
-  const int b = d.x, h = d.y, last = d.w;
-  const long r0 = (long)d.z * ROWS;
-  int seq, w;
-  Division<ROWS, KEYS>::lens(a, b, &seq, &w);
-  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 3), part = threadIdx.x & 7;
-  if (r >= (long)(w < 0 ? a.W : w) * a.G - r0) return;
+  const int last = d.w, rows = reinterpret_cast<const int*>(a.desc)[8 * first + 4];
+  const int set = threadIdx.x / (kJoinRows * 8), t = threadIdx.x % (kJoinRows * 8);
+  const int r = blockIdx.y * kJoinRows + (t >> 3), part = t & 7;
+  if (blockIdx.y * kJoinRows >= rows) return;
+  const int from = min(r, rows - 1);  // every thread stays for the barrier
   float M = -INFINITY, L = 0.f, x[NT] = {};
-#pragma unroll 4
-  for (int i = first; i <= last; ++i) {
+#pragma unroll 2
+  for (int i = first + set; i <= last; i += kJoinSets) {
     const float* p = a.part + (2 * (size_t)i + (i == first)) * part_floats<ROWS>(D);
-    const float pm = p[ROWS * D + r], pl = p[ROWS * D + ROWS + r];
+    const float pm = p[ROWS * D + from], pl = p[ROWS * D + ROWS + from];
     float4 z[NT / 4];
 #pragma unroll
     for (int j = 0; j < NT / 4; ++j)
-      z[j] = *reinterpret_cast<const float4*>(p + r * D + part * NT + 4 * j);
+      z[j] = *reinterpret_cast<const float4*>(p + from * D + part * NT + 4 * j);
     if (pm == -INFINITY && pl == 0.f) continue;
     const float now = fmaxf(M, pm);
     const float fo = M == now ? 1.f : ex2(M - now), fn = pm == now ? 1.f : ex2(pm - now);
@@ -256,8 +280,30 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
       x[4 * j + 3] = x[4 * j + 3] * fo + z[j].w * fn;
     }
   }
-  const int i = (int)((r0 + r) / a.G), head = h * a.G + (int)((r0 + r) % a.G);
-  const size_t orow = ((size_t)b * a.W + i) * a.Hq + head;
+  if (part == 0) sM[set][t >> 3] = M, sL[set][t >> 3] = L;
+  if (set > 0) {
+#pragma unroll
+    for (int j = 0; j < NT; j += 4)
+      *reinterpret_cast<float4*>(&sX[set - 1][t][j]) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+  }
+  __syncthreads();
+  if (set > 0 || r >= rows) return;
+  float top = M;
+#pragma unroll
+  for (int k = 1; k < kJoinSets; ++k) top = fmaxf(top, sM[k][t >> 3]);
+#pragma unroll
+  for (int k = 0; k < kJoinSets; ++k) {
+    const float km = sM[k][t >> 3], kl = sL[k][t >> 3];
+    const float f = km == top ? 1.f : km == -INFINITY && kl == 0.f ? 0.f : ex2(km - top);
+    L = k == 0 ? L * f : L + kl * f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x[j] = k == 0 ? x[j] * f : x[j] + sX[k ? k - 1 : 0][t][j] * f;
+  }
+  M = top;
+  const int h = d.y;
+  const long row = (long)d.z * ROWS + r;
+  const int i = (int)(row / a.G), head = h * a.G + (int)(row % a.G);
+  const size_t orow = ((size_t)d.x * a.W + i) * a.Hq + head;
   const float inv = L == 0.f ? 0.f : 1.f / L;
   uint32_t y[NT / 2];
 #pragma unroll
@@ -272,7 +318,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
 template <class T, int D, int ROWS, int KEYS>
 cudaError_t launch_join(const AttendArgs& a, int ctas, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, ROWS / kJoinRows);
+  cfg.gridDim = dim3(ctas, min(ROWS, ceil_div((long)a.W * a.G, 16) * 16) / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
   constexpr int NT = D / 8;   // mma tiles along D
   constexpr int VW = D / 32;  // 32-bit words of V per thread and key
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long sPre[kRThreads + 1];
   __shared__ float sM[kRWarps][kRows], sL[kRWarps][kRows], sV[kRWarps];
   __shared__ int sBad;
   const KvCache& c = a.c;
@@ -121,7 +120,7 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
   __shared__ Walk<kRows, kKeys, kUnitCost> v;
   __shared__ int sMore;
   if (tid < kDescWords) a.desc[blockIdx.x * kDescWords + tid] = -1;
-  if (!divide<kRows, kKeys, kUnitCost, kRThreads>(a, kLeastCells, sPre, v)) return;
+  if (!divide<kRows, kKeys, kUnitCost, kRThreads>(a, kLeastCells, v)) return;
   __syncthreads();  // every thread has stored the walk's beginning
   unsigned char* ring = smem + warp * R::kWarp;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
@@ -467,6 +466,7 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
         d[1] = u.h;
         d[2] = u.mt;
         d[3] = v.last_cta();
+        d[4] = rows;
       }
     }
     __syncthreads();

@@ -195,7 +195,6 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   constexpr int ST = TL::kStages;
   extern __shared__ unsigned char smem_raw[];
   __shared__ Bars bars;
-  __shared__ long long sPre[kTThreads + 1];
   // of each 16-key group: K's scale; V's scale over the largest so far in the segment, as log2
   // and as 1 / x; that largest scale, and the last one over it
   __shared__ __align__(16) float sK[kRing][kGroups], sLog[kRing][kGroups], sInv[kRing][kGroups];
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     sNan = 0;
   }
   Walk<kRows, kKeys, kUnitCost> v;
-  if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, sPre, v)) return;
+  if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, v)) return;
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sTmem)),
@@ -500,6 +499,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         d[1] = u.h;
         d[2] = u.mt;
         d[3] = last;
+        d[4] = my_rows;
       }
       fence_before();  // O has been read: the next unit's first product follows this thread's p_full
     }
