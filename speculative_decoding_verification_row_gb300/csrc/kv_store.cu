@@ -103,11 +103,16 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a)
   };
   uint4 keep[kStoreVecs];
   float amax = 0.f;
+  const int blk = table[col];
 #pragma unroll
   for (int q = 0; q < kStoreVecs; ++q) {
     const int v = threadIdx.x + q * kStoreThreads;
     if (v < nvec) keep[q] = vec(v);
   }
+  // the old scale comes while the rows do
+  const bool mapped = blk >= 0 && blk < c.num_blocks;
+  float* ps = c.scales + c.scale_at(mapped ? blk : 0, kind, h);
+  const float old = first > 0 ? *ps : 0.f;
 #pragma unroll
   for (int q = 0; q < kStoreVecs; ++q)
     if (threadIdx.x + q * kStoreThreads < nvec) amax = amax8<T>(keep[q], amax);
@@ -120,12 +125,9 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a)
   if (sBad) return;
 #pragma unroll
   for (int i = 0; i < kStoreThreads / 32; ++i) amax = fmaxf(amax, sMax[i]);
-  const int blk = table[col];
   float scale = scale_for(amax);
   uint8_t* dst = c.pool + c.row(blk, kind, h, 0);
-  float* ps = c.scales + c.scale_at(blk, kind, h);
   if (first > 0) {
-    const float old = *ps;
     if (old >= scale) {
       scale = old;
     } else {  // the live rows move to the larger scale
@@ -135,7 +137,6 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a)
         *p = rescale_e4m3x16(*p, r);
       }
     }
-    __syncthreads();  // every thread has read the old scale
   }
   if (threadIdx.x == 0) *ps = scale;
   const float inv = scale_ratio(1.f, scale);

@@ -9,7 +9,8 @@
 // to thread r of the cluster (8 CTAs x 1024 threads = 8192), the scan crosses
 // the CTAs through distributed shared memory, and the cluster barrier between
 // the last read and the first write lets the counters be updated in place
-// with no workspace and no second launch.
+// with no workspace and no second launch.  The sums saturate at 2^31 - 1,
+// which no stack reaches: 32-bit shuffles and no 64-bit division.
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
@@ -39,41 +40,53 @@ struct PageArgs {
   int32_t* granted;
 };
 
-// Exclusive prefix of x over the cluster's threads in rank order, and the
-// total.  sWarp: 32 words, sTotal: one word that the other CTAs read.  Ends
-// past a cluster barrier: everything the threads loaded before the call has
-// been read by then.
-__device__ long long cluster_scan(cg::cluster_group& cl, long long x, long long* sWarp,
-                                  long long* sTotal, long long* total) {
+__device__ __forceinline__ unsigned sat_add(unsigned a, unsigned b) {
+  return min(a + b, 0x7fffffffu);  // both at most 2^31 - 1
+}
+
+// Inclusive prefix of x over the cluster's threads in rank order (saturating),
+// and the total.  sWarp: 32 words, sTotal: one word that the other CTAs read.
+// Ends past a cluster barrier: everything the threads loaded before the call
+// has been read by then.
+__device__ unsigned cluster_scan(cg::cluster_group& cl, unsigned x, unsigned* sWarp,
+                                 unsigned* sTotal, unsigned* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = x;
+  unsigned incl = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(~0u, incl, d);
-    if (lane >= d) incl += y;
+    const unsigned y = __shfl_up_sync(~0u, incl, d);
+    if (lane >= d) incl = sat_add(incl, y);
   }
   if (lane == 31) sWarp[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    long long w = lane < (int)(blockDim.x >> 5) ? sWarp[lane] : 0;
+  unsigned before = 0, all = 0;
+  if (blockDim.x > 256 || cl.num_blocks() > 1) {
+    if (warp == 0) {
+      unsigned w = lane < (int)(blockDim.x >> 5) ? sWarp[lane] : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(~0u, w, d);
-      if (lane >= d) w += y;
+      for (int d = 1; d < 32; d <<= 1) {
+        const unsigned y = __shfl_up_sync(~0u, w, d);
+        if (lane >= d) w = sat_add(w, y);
+      }
+      sWarp[lane] = w;
+      if (lane == 31) *sTotal = w;
     }
-    sWarp[lane] = w;
-    if (lane == 31) *sTotal = w;
-  }
-  cl.sync();
-  long long before = 0, all = 0;
-  const int me = cl.block_rank(), n = cl.num_blocks();
-  for (int r = 0; r < n; ++r) {
-    const long long t = *cl.map_shared_rank(sTotal, r);
-    before += r < me ? t : 0;
-    all += t;
+    cl.sync();
+    const int me = cl.block_rank(), n = cl.num_blocks();
+    for (int r = 0; r < n; ++r) {
+      const unsigned t = *cl.map_shared_rank(sTotal, r);
+      if (r < me) before = sat_add(before, t);
+      all = sat_add(all, t);
+    }
+    if (warp) before = sat_add(before, sWarp[warp - 1]);
+  } else {  // few warps of one CTA
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+      if (w < warp) before = sat_add(before, sWarp[w]);
+      all = sat_add(all, sWarp[w]);
+    }
   }
   *total = all;
-  return before + (warp ? sWarp[warp - 1] : 0) + incl - x;
+  return sat_add(before, incl);
 }
 
 // Calls f(r, i, n) for i in [0, n) of every lane's n: each lane serves its
@@ -93,49 +106,49 @@ __device__ __forceinline__ void for_entries(int n, F f) {
 }
 
 __global__ void __launch_bounds__(kPageThreads) reserve_kernel(const PageArgs a) {
-  __shared__ long long sWarp[32];
-  __shared__ long long sTotal[2];
-  __shared__ long long sFirst[kPageThreads];  // stack index of the request's first new block
+  __shared__ unsigned sWarp[32], sTotal, sUsed;
+  __shared__ int sFirst[kPageThreads];  // stack index of the request's first new block
   __shared__ int sSeq[kPageThreads], sHeld[kPageThreads], sGranted[kPageThreads];
   cg::cluster_group cl = cg::this_cluster();
   const int b = cl.block_rank() * blockDim.x + threadIdx.x;
   const int count = *a.free_count;
   int seq = 0, win = 0, held = 0;
-  long long need = 0;
+  unsigned need = 0;
   bool ok = false;
+  if (threadIdx.x == 0) sUsed = 0;
   if (b < a.B) {
     seq = a.seq[b];
     win = a.win ? a.win[b] : a.W;
     held = a.held[b];
     ok = seq >= 0 && win >= 0 && win <= a.W && held >= 0 && held <= a.max_blocks;
     if (ok) {
-      const long long blocks = ((long long)seq + win + a.tpb - 1) / a.tpb;
-      ok = blocks <= a.max_blocks;
-      need = ok && blocks > held ? blocks - held : 0;
+      const unsigned end = (unsigned)seq + win, tpb = a.tpb;
+      const unsigned blocks = end / tpb + (end % tpb != 0);
+      ok = blocks <= (unsigned)a.max_blocks;
+      need = ok && blocks > (unsigned)held ? blocks - held : 0;
     }
   }
-  long long total;
-  const long long first = cluster_scan(cl, need, sWarp, &sTotal[0], &total);
-  const int avail = count < 0 || count > a.num_blocks ? 0 : count;
+  unsigned total;
+  const unsigned upto = cluster_scan(cl, need, sWarp, &sTotal, &total);
+  const unsigned avail = count < 0 || count > a.num_blocks ? 0 : count;
   // Requests are served while the running sum fits, so every served request
   // comes before every refused one that needs a block.
-  if (ok && need > 0 && first + need > avail) ok = false;
+  if (ok && need > 0 && upto > avail) ok = false;
   const int take = ok ? (int)need : 0;
-  sFirst[threadIdx.x] = avail - 1 - first;
+  sFirst[threadIdx.x] = (int)(avail - 1 - (upto - need));
   sSeq[threadIdx.x] = seq;
   sHeld[threadIdx.x] = held;
   sGranted[threadIdx.x] = ok ? win : -1;
-  // what the stack gave: the sum up to the first refused request
-  long long used;
-  __syncthreads();
-  cluster_scan(cl, take, sWarp, &sTotal[1], &used);
+  // what the stack gave: the running sum at the last served request
+  const unsigned used = __reduce_max_sync(~0u, take > 0 ? upto : 0u);
+  if ((threadIdx.x & 31) == 0 && used > 0) atomicMax(cl.map_shared_rank(&sUsed, 0), used);
   if (b < a.B) {
     a.granted[b] = ok ? win : -1;
     if (take > 0) a.held[b] = held + take;
   }
-  if (b == 0 && used > 0) *a.free_count = count - (int)used;
   const int b0 = cl.block_rank() * blockDim.x;
   const int w0 = threadIdx.x & ~31;
+  __syncthreads();
   for_entries(take, [&](int lane, int i) {
     const int r = w0 + lane;
     a.tables[(size_t)(b0 + r) * a.max_blocks + sHeld[r] + i] = a.free_blocks[sFirst[r] - i];
@@ -143,28 +156,27 @@ __global__ void __launch_bounds__(kPageThreads) reserve_kernel(const PageArgs a)
   if (a.slots) {
     // A block that was just taken is read from the stack again rather than
     // from the table, so the slots need not wait for its stores.
-    const int rows = min((int)blockDim.x, a.B - b0);
-    const long long n = rows > 0 ? (long long)rows * a.W : 0;
-    for (long long s = threadIdx.x; s < n; s += blockDim.x) {
-      const int r = (int)(s / a.W), i = (int)(s % a.W);
+    const unsigned rows = max(0, min((int)blockDim.x, a.B - b0)), n = rows * a.W;  // at most 2^26
+    for (unsigned s = threadIdx.x; s < n; s += blockDim.x) {
+      const unsigned r = s / (unsigned)a.W, i = s - r * a.W;
       int slot = -1;
-      if (i < sGranted[r]) {
-        const int t = sSeq[r] + i, col = t / a.tpb;
-        const int blk = col < sHeld[r] ? a.tables[(size_t)(b0 + r) * a.max_blocks + col]
-                                       : a.free_blocks[sFirst[r] - (col - sHeld[r])];
-        if (blk >= 0 && blk < a.num_blocks) slot = blk * a.tpb + t % a.tpb;
+      if ((int)i < sGranted[r]) {
+        const unsigned t = (unsigned)sSeq[r] + i, col = t / (unsigned)a.tpb;
+        const int blk = (int)col < sHeld[r] ? a.tables[(size_t)(b0 + r) * a.max_blocks + col]
+                                            : a.free_blocks[sFirst[r] - (int)(col - sHeld[r])];
+        if (blk >= 0 && blk < a.num_blocks) slot = blk * a.tpb + (int)(t - col * a.tpb);
       }
       a.slots[(size_t)b0 * a.W + s] = slot;
     }
   }
-  cl.sync();  // no CTA leaves while another may still read its total
+  cl.sync();  // every CTA has read the totals and stored what it used
+  if (b == 0 && sUsed > 0) *a.free_count = count - (int)sUsed;
 }
 
 __global__ void __launch_bounds__(kPageThreads) release_kernel(const PageArgs a) {
-  __shared__ long long sWarp[32];
-  __shared__ long long sTotal;
-  __shared__ long long sTop[kPageThreads];  // stack index the request's first block goes to
-  __shared__ int sFrom[kPageThreads];       // table column of that block
+  __shared__ unsigned sWarp[32], sTotal;
+  __shared__ int sTop[kPageThreads];   // stack index the request's first block goes to
+  __shared__ int sFrom[kPageThreads];  // table column of that block
   cg::cluster_group cl = cg::this_cluster();
   const int b = cl.block_rank() * blockDim.x + threadIdx.x;
   const int count = *a.free_count;
@@ -174,13 +186,13 @@ __global__ void __launch_bounds__(kPageThreads) release_kernel(const PageArgs a)
     n = a.counts[b];
     if (held < 0 || held > a.max_blocks || n < 0 || n > held) n = 0;
   }
-  long long total;
-  const long long first = cluster_scan(cl, n, sWarp, &sTotal, &total);
-  const bool fits = count >= 0 && count + total <= a.num_blocks;
+  unsigned total;
+  const unsigned upto = cluster_scan(cl, n, sWarp, &sTotal, &total);
+  const bool fits = count >= 0 && count <= a.num_blocks && total <= (unsigned)(a.num_blocks - count);
+  sTop[threadIdx.x] = (int)(count + total - 1 - (upto - n));
   if (!fits) n = 0;
-  sTop[threadIdx.x] = count + total - 1 - first;
   sFrom[threadIdx.x] = held - n;
-  __syncwarp();
+  __syncthreads();  // also: thread 0 stores the count only when all have read it
   if (n > 0) a.held[b] = held - n;
   const int b0 = cl.block_rank() * blockDim.x;
   const int w0 = threadIdx.x & ~31;
@@ -190,48 +202,96 @@ __global__ void __launch_bounds__(kPageThreads) release_kernel(const PageArgs a)
     a.free_blocks[sTop[r] - i] = *entry;
     *entry = -1;
   });
+  cl.sync();  // no CTA leaves, and the count stays, while another may still read
   if (b == 0 && fits && total > 0) *a.free_count = count + (int)total;
-  cl.sync();
 }
 
-// One CTA builds the mask rows [r0, r0 + kMaskRows) of one request in shared
-// memory: a warp reads a whole path (L <= 64: two nodes per lane) and sets,
-// for every node of the path among its rows, the bits of the nodes up to it.
-constexpr int kMaskRows = 64;
-constexpr int kMaskThreads = 256;
+// One CTA builds the mask rows [r0, r0 + kMaskRows) of one request.  The paths
+// pass through shared memory in batches, a warp to a path (L <= 64: two nodes
+// per lane).  First every node's parent: where a node has one parent on all
+// used paths (a tree), its row is its parent's chain up to the root, walked by
+// one thread.  Paths that give a node several parents are ORed bit by bit.
+// 64 requests of 509 nodes and 301 paths of 17: 39 us for that alone, its
+// loads waited for path by path.
+constexpr int kMaskRows = 128;
+constexpr int kMaskThreads = 512;
+constexpr int kMaskBatch = 4096;  // path entries at a time
 
 __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const int32_t* paths, int P, int L,
                                                                  int N, int32_t* masks) {
-  __shared__ unsigned sBits[kMaskRows * (SPEC_MAX_TREE_NODES / 32)];
-  __shared__ int sBad;
-  const int words = (N + 31) / 32;
+  __shared__ int sPath[kMaskBatch];
+  __shared__ int sParent[SPEC_MAX_TREE_NODES];
+  __shared__ unsigned sBits[kMaskRows * (SPEC_MAX_TREE_NODES / 32 + 1)];
+  __shared__ int sBad, sSeveral;
+  constexpr int kNone = -2;  // on no used path; -1: the root's parent
+  const int words = (N + 31) / 32, pitch = words | 1;
   const int chunks = (N + kMaskRows - 1) / kMaskRows;
   const int b = blockIdx.x / chunks, r0 = blockIdx.x % chunks * kMaskRows;
   const int rows = min(kMaskRows, N - r0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < rows * words; i += kMaskThreads) sBits[i] = 0;
-  if (threadIdx.x == 0) sBad = 0;
-  __syncthreads();
-  for (int p = warp; p < P; p += kMaskThreads / 32) {
-    const int32_t* path = paths + ((size_t)b * P + p) * L;
-    const int n0 = lane < L ? path[lane] : -1;
-    const int n1 = lane + 32 < L ? path[lane + 32] : -1;
-    const unsigned neg0 = __ballot_sync(~0u, n0 < 0), neg1 = __ballot_sync(~0u, n1 < 0);
-    if (__shfl_sync(~0u, n0, 0) != 0) continue;  // an unused path
-    const int len = neg0 ? __ffs(neg0) - 1 : neg1 ? 31 + __ffs(neg1) : 64;
-    if ((lane < len && n0 >= N) || (lane + 32 < len && n1 >= N)) sBad = 1;
-    for (int d = 0; d < len; ++d) {
-      const int row = __shfl_sync(~0u, d < 32 ? n0 : n1, d & 31) - r0;
-      if (row < 0 || row >= rows) continue;
-      unsigned* bits = sBits + row * words;
-      if (lane <= d && n0 < N) atomicOr(bits + (n0 >> 5), 1u << (n0 & 31));
-      if (lane + 32 <= d && n1 < N) atomicOr(bits + (n1 >> 5), 1u << (n1 & 31));
+  for (int i = threadIdx.x; i < rows * pitch; i += kMaskThreads) sBits[i] = 0;
+  for (int i = threadIdx.x; i < N; i += kMaskThreads) sParent[i] = kNone;
+  if (threadIdx.x == 0) sBad = sSeveral = 0;
+  const int per = kMaskBatch / L;  // paths of a batch
+  // calls f(n0, n1, len) for every used path: the lane's nodes lane and lane + 32
+  auto each_path = [&](auto f) {
+    for (int p0 = 0; p0 < P; p0 += per) {
+      const int np = min(per, P - p0);
+      const int32_t* src = paths + ((size_t)b * P + p0) * L;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kMaskBatch / kMaskThreads; ++q) {
+        const int i = threadIdx.x + q * kMaskThreads;
+        if (i < np * L) sPath[i] = src[i];
+      }
+      __syncthreads();
+      for (int p = warp; p < np; p += kMaskThreads / 32) {
+        const int* path = sPath + p * L;
+        if (path[0] != 0) continue;  // an unused path
+        const int n0 = lane < L ? path[lane] : -1, n1 = lane + 32 < L ? path[lane + 32] : -1;
+        const unsigned neg0 = __ballot_sync(~0u, n0 < 0), neg1 = __ballot_sync(~0u, n1 < 0);
+        f(path, n0, n1, neg0 ? __ffs(neg0) - 1 : neg1 ? 31 + __ffs(neg1) : 64);
+      }
     }
+  };
+  each_path([&](const int* path, int n0, int n1, int len) {
+    auto claim = [&](int d, int node) {
+      if (d >= len) return;
+      if (node >= N) {
+        sBad = 1;
+        return;
+      }
+      const int parent = d ? path[d - 1] : -1, had = atomicCAS(&sParent[node], kNone, parent);
+      if (had != kNone && had != parent) sSeveral = 1;
+    };
+    claim(lane, n0);
+    claim(lane + 32, n1);
+  });
+  __syncthreads();
+  if (!sBad && !sSeveral) {
+    for (int i = threadIdx.x; i < rows; i += kMaskThreads) {
+      // A parent is on a path before its node: the chain ends at the root.
+      if (sParent[r0 + i] != kNone)
+        for (int node = r0 + i; node >= 0; node = sParent[node])
+          sBits[i * pitch + (node >> 5)] |= 1u << (node & 31);
+    }
+  } else if (!sBad) {
+    each_path([&](const int* path, int n0, int n1, int len) {
+      for (int d = 0; d < len; ++d) {
+        const int row = path[d] - r0;
+        if (row < 0 || row >= rows) continue;
+        unsigned* bits = sBits + row * pitch;
+        if (lane <= d) atomicOr(bits + (n0 >> 5), 1u << (n0 & 31));
+        if (lane + 32 <= d) atomicOr(bits + (n1 >> 5), 1u << (n1 & 31));
+      }
+    });
   }
   __syncthreads();
   int32_t* dst = masks + ((size_t)b * N + r0) * words;
-  for (int i = threadIdx.x; i < rows * words; i += kMaskThreads)
-    dst[i] = sBad ? 0 : (int32_t)sBits[i];
+  for (int i = threadIdx.x; i < rows * words; i += kMaskThreads) {
+    const int r = (unsigned)i / (unsigned)words;
+    dst[i] = (int32_t)sBits[r * pitch + i - r * words];
+  }
 }
 
 // One cluster that gives every request a thread: a CTA up to 1024 requests,
@@ -239,7 +299,7 @@ __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const int32_t* 
 template <class Kern>
 cudaError_t launch_paged(Kern kernel, const PageArgs& a, long slots, cudaStream_t st) {
   const int ctas = a.B > 4 * kPageThreads ? 8 : a.B > 2 * kPageThreads ? 4 : a.B > kPageThreads ? 2 : 1;
-  const int per = max(ceil_div(a.B, ctas), min(kPageThreads, ceil_div(slots, 8L * ctas)));
+  const int per = max(ceil_div(a.B, ctas), min(kPageThreads, ceil_div(slots, 2L * ctas)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(max(64, (per + 31) / 32 * 32));
