@@ -565,8 +565,8 @@ def _on_stream(stream, dev):
 
 def _at(t, name, dev, dtype, shape) -> int:
     """Address of a dense tensor of this type and shape on this device."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or t.shape != shape
-            or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev.index
+            or t.shape != shape or not t.is_contiguous()):
         _dev(t, name, dtype, shape)
         raise ValueError(f"{name} must be on {dev}, is on {t.device}")
     return t.data_ptr()
@@ -583,15 +583,16 @@ def _cuda(t, name, dims) -> torch.device:
 
 def _apart(*addresses):
     """An array that a call writes must not be another of its arrays."""
-    real = [p for p in addresses if p]
-    if len(set(real)) != len(real):
-        raise ValueError("two of the call's arrays are the same memory")
+    if len(set(addresses)) != len(addresses):
+        real = [p for p in addresses if p]
+        if len(set(real)) != len(real):
+            raise ValueError("two of the call's arrays are the same memory")
 
 
 def _rows(t, name, dev, shape, dtype):
     """Address and first three strides of a [B, W, heads, D] tensor whose rows
     along D are dense and 16-byte aligned."""
-    if not isinstance(t, torch.Tensor) or t.device != dev:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev.index:
         raise ValueError(f"{name} must be a CUDA tensor on {dev}")
     if t.dtype is not dtype or (dtype is not torch.bfloat16 and dtype is not torch.float16):
         raise ValueError(f"{name} must be bfloat16 or float16, all of one type, got {t.dtype}")

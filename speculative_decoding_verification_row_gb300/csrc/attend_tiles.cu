@@ -14,7 +14,7 @@
 // With both left operands in tensor memory a step reads 64 KB (D = 128) and
 // writes 64 KB of shared memory, as long as its products take (1024 clocks);
 // with Q in shared memory it would be 160 KB and shared memory the bound.
-// Tensor memory: Q, P (one buffer), S (two buffers), O: 512 columns, all.
+// Tensor memory: Q, S (two buffers; the weights replace the scores there), O.
 //
 // Scales, weights and lazy rescaling are as in attend_rows.cu.
 #include "attend.cuh"
@@ -33,7 +33,7 @@ constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kGroups = kKeys / 16;      // scale groups of a tile
 constexpr int kRing = 16;                // tiles whose pages and scales are kept
 constexpr int kAhead = 8;                // fewer than these are known ahead: more are looked up
-constexpr uint32_t kColQ = 0, kColP = 64, kColS = 128, kColO = 384, kCols = 512;
+constexpr uint32_t kColQ = 0, kColS = 128, kColO = 384, kCols = 512;
 
 template <int D>
 struct Tile {
@@ -44,7 +44,7 @@ struct Tile {
 
 struct Bars {
   unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4];
-  unsigned long long s_full[2], p_full, pv_done, q_full, pages[kRing], end;
+  unsigned long long s_full[2], p_full[2], pv_done[2], q_full, pages[kRing], end;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -218,8 +218,11 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     }
     bar_init(&bars.s_full[0], 1);
     bar_init(&bars.s_full[1], 1);
-    bar_init(&bars.p_full, kSoftWarps);
-    bar_init(&bars.pv_done, 1);
+    // by a tile's parity: a warp may be a tile ahead of another, or two behind the products
+    bar_init(&bars.p_full[0], kSoftWarps);
+    bar_init(&bars.p_full[1], kSoftWarps);
+    bar_init(&bars.pv_done[0], 1);
+    bar_init(&bars.pv_done[1], 1);
     bar_init(&bars.q_full, kSoftWarps);
     for (int i = 0; i < kRing; ++i) bar_init(&bars.pages[i], 1);
     bar_init(&bars.end, 1);
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
             l *= al;
             if (tile > tile0) {
               const float ar = al * grow;
-              bar_wait(&bars.pv_done, (n - 1) & 1, dead);
+              bar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, dead);
               fence_after();
 #pragma unroll 1
               for (int x = half * HD; x < half * HD + HD; x += 16) {
@@ -399,16 +402,13 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               }
               l = fmaf(sum.x + sum.y, iv[y], l);
             }
-            if (z == 0) {  // P has one buffer: the last tile's product has read it
-              if (n > 0) bar_wait(&bars.pv_done, (n - 1) & 1, dead);
-              fence_after();
-            }
-            tmem_st16(lanes + kColP + half * 32 + z * 16, p);
+            // over this thread's scores, all of which it has read
+            tmem_st16(lanes + kColS + (n & 1) * kKeys + half * 64 + z * 16, p);
           }
           tmem_wait_st();
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(&bars.p_full);
+          if (lane == 0) bar_arrive(&bars.p_full[n & 1]);
         }
         if (tile1 == u.tiles) {  // a window block that these rows do not read is checked all the same
           const int32_t* table = c.tables + (size_t)u.b * c.max_blocks;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         sAux[1][half][r] = l;
         pair_sync(warp);
         l += sAux[1][half ^ 1][r];
-        bar_wait(&bars.pv_done, (n - 1) & 1, dead);
+        bar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, dead);
         fence_after();
         vref = sRef[(n - 1) % kRing];
       }
@@ -623,22 +623,26 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     for (; sKeys[n % kRing] > 0; ++n) {
       const uint32_t next = (n + 1) % kRing;
       const bool follows = sKeys[next] > 0, first = sFirst[next] != 0;
-      // within a unit the next scores go before this tile's weighted V; a new
-      // unit's wait for its Q, so they go behind
+      // The next scores' buffer is free when the product with the weights in it is
+      // done.  Within a unit they go before this tile's weighted V; a new unit's
+      // wait for its Q, so they go behind.
+      if (n > 0) bar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, dead);
       if (follows && !first) scores(n + 1);
       if (posted < n + kAhead && !ended) lookup(true);  // while the weights are computed
       const uint32_t st = n % ST;
       bar_wait(&bars.v_full[st], (n / ST) & 1, dead);
-      bar_wait(&bars.p_full, n & 1, dead);
+      bar_wait(&bars.p_full[n & 1], (n >> 1) & 1, dead);
       fence_after();
       if (elect() && !*dead) {
         const bool add = sFirst[n % kRing] == 0;
+        const uint32_t p = tmem + kColS + (n & 1) * kKeys;  // 32 columns, and 32 from the 64th on
         const uint64_t b = v_desc + st * (TL::kBytes >> 4);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + kColO, tmem + kColP + k * 8, b + k * (2048 >> 4), instr_desc(D, true), add || k > 0);
+          mma_ts(tmem + kColO, p + k / 4 * 64 + k % 4 * 8, b + k * (2048 >> 4), instr_desc(D, true),
+                 add || k > 0);
         mma_commit(&bars.v_empty[st]);
-        mma_commit(&bars.pv_done);
+        mma_commit(&bars.pv_done[n & 1]);
       }
       __syncwarp();
       if (follows && first) scores(n + 1);

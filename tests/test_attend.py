@@ -426,3 +426,20 @@ def test_a_step_of_tree_decoding():
     out, lse = sv.attend_kv(dq, pool, scales, d["tables"], new, want_lse=True)
     r = kv.attend(dq.double().cpu().numpy(), pool.cpu().numpy(), scales.cpu().numpy(), d["tables"].cpu().numpy(), len_o)
     check(out, lse, r, "bf16", D, np.ones((B, 1), bool), 100)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W,D,B,seq", [(4, 40, 64, 2, 9000), (8, 30, 128, 3, 20000), (1, 4, 64, 1, 60000), (4, 4, 128, 40, 3000)])
+def test_long_prefixes(G, W, D, B, seq):
+    # many tiles per CTA: every ring of the kernels wraps several times.  The
+    # oracle's rows are those of one request; the others are its copies.
+    rng = np.random.default_rng(D)
+    H, tpb = 1, 64
+    pool, scales, tables = cache(rng, np.array([seq + W]), H, D, tpb)
+    tables = np.repeat(tables, B, 0)
+    q, dq = make_q(rng, (1, W, H * G, D), "bf16", 0.3)
+    r = kv.attend(q, pool, scales, tables[:1], [seq])
+    for _ in range(3):
+        out, lse = sv.attend_kv(dq.repeat(B, 1, 1, 1), dev(pool), dev(scales), i32(tables), i32([seq] * B), want_lse=True)
+    for b in range(B):
+        check(out[b:b + 1], lse[b:b + 1], r, "bf16", D, np.ones((1, W), bool), np.abs(np.nan_to_num(kv.decode(pool))).max() * scales.max())
