@@ -7,9 +7,12 @@
 //          keys (and of D).  Reads S from tensor memory, writes the weights P
 //          back there as fp16, rescales O when the maximum moves by more than
 //          2^7, and writes the result.  Loads Q at a unit's start.
-//   8      one thread issues the products: S = Q K^T with Q in tensor memory,
-//          O += P V with P in tensor memory, K and V in shared memory.
-//   9-15   read e4m3 rows of the pages, one tile ahead in registers, and
+//   8      one thread issues S = Q K^T, Q in tensor memory, K in shared memory.
+//   9      one thread issues O += P V, P in tensor memory, V in shared memory.
+//          (Issuing takes as long as the product: with one warp for both, its
+//          waits left the tensor cores idle half of the time.)  The warp also
+//          looks up the pages and scales of the tiles to come.
+//   10-15  read e4m3 rows of the pages, two tiles ahead in registers, and
 //          write them as fp16 (exact) in the 128-byte swizzle.
 // With both left operands in tensor memory a step reads 64 KB (D = 128) and
 // writes 64 KB of shared memory, as long as its products take (1024 clocks);
@@ -27,7 +30,7 @@ constexpr int kRows = 128;
 constexpr int kKeys = 128;
 constexpr int kUnitCost = 4;             // cells of a unit besides its tiles
 constexpr int kLeastCells = 6;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarp = 9, kConvWarps = 7;
+constexpr int kSoftWarps = 8, kScoreWarp = 8, kValueWarp = 9, kConvWarp = 10, kConvWarps = 6;
 constexpr int kTThreads = (kConvWarp + kConvWarps) * 32;
 constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kGroups = kKeys / 16;      // scale groups of a tile
@@ -225,14 +228,14 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     bar_init(&bars.pv_done[1], 1);
     bar_init(&bars.q_full, kSoftWarps);
     for (int i = 0; i < kRing; ++i) bar_init(&bars.pages[i], 1);
-    bar_init(&bars.end, 1);
+    bar_init(&bars.end, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sDead = 0;
     sNan = 0;
   }
   Walk<kRows, kKeys, kUnitCost> v;
   if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, v)) return;
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sTmem)),
                  "r"(kCols)
@@ -503,7 +506,33 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       }
       fence_before();  // O has been read: the next unit's first product follows this thread's p_full
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kScoreWarp) {
+    for (uint32_t seg = 0;; ++n) {
+      const int at = n % kRing;
+      bar_wait(&bars.pages[at], (n / kRing) & 1, dead);
+      if (sKeys[at] == 0 || *dead) break;
+      if (sFirst[at]) {
+        bar_wait(&bars.q_full, seg & 1, dead);
+        ++seg;
+      }
+      // the buffer is free when the product with the weights that lay in it is done
+      if (n > 1) bar_wait(&bars.pv_done[n & 1], ((n >> 1) - 1) & 1, dead);
+      const uint32_t st = n % ST;
+      bar_wait(&bars.k_full[st], (n / ST) & 1, dead);
+      fence_after();
+      if (elect() && !*dead) {
+        const uint32_t d = tmem + kColS + (n & 1) * kKeys;
+        const uint64_t b = k_desc + st * (TL::kBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ts(d, tmem + kColQ + k * 8, b + (k / 4) * (kKeys * 128 >> 4) + (k % 4) * (32 >> 4),
+                 instr_desc(kKeys, false), k > 0);
+        mma_commit(&bars.k_empty[st]);
+        mma_commit(&bars.s_full[n & 1]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == kValueWarp) {
     // ---- the lookup, up to four tiles of a segment at a time: block ids, then
     // scales, then the ring, a call apart each, so that no use waits for its
     // load.  Lane x: group x % 8 of the batch's tile x / 8.
@@ -529,26 +558,17 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       if (post && !ended) {
         // V's scales against the segment's largest so far; below 2^-40 of it they
         // are taken as that (such a block adds at most 2^-40 of the largest |V|)
-        float top = my_tile < count2 ? v_scale : 0.f;
-#pragma unroll
-        for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-        float last = first2 ? 0.f : ref;  // before this lane's tile
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
-          const float y = __shfl_sync(~0u, top, x * 8);
-          if (x < my_tile) last = fmaxf(last, y);
-        }
-        const float mine = fmaxf(last, top);
-        ref = __shfl_sync(~0u, mine, 31);
-        const float over = mine > 0.f ? __fdividef(1.f, mine) : 0.f;
-        const float vr = mine > 0.f ? fmaxf(v_scale * over, 0x1p-40f) : 1.f;
+        const float last = first2 ? 0.f : ref;
+        ref = fmaxf(last, __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(v_scale))));
+        const float over = ref > 0.f ? __fdividef(1.f, ref) : 0.f;
+        const float vr = ref > 0.f ? fmaxf(v_scale * over, 0x1p-40f) : 1.f;
         const int at = (posted + my_tile) % kRing, g = lane & 7;
         if (my_tile < count2) {
           sPage[at][g] = page;
           sK[at][g] = k_scale;
           sLog[at][g] = __log2f(vr);
           sInv[at][g] = __fdividef(1.f, vr);
-          if (g == 0) sRef[at] = mine, sGrow[at] = mine > last ? last * over : 1.f;
+          if (g == 0) sRef[at] = ref, sGrow[at] = my_tile == 0 && ref > last ? last * over : 1.f;
         }
         // keys of the tile, those that every row sees, and whether a segment begins;
         // no keys: the share has ended
@@ -598,37 +618,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     lookup(false);
     while (posted < kAhead && !ended) lookup(true);
 
-    uint32_t seg = 0;
-    auto scores = [&](uint32_t t) {
-      if (sFirst[t % kRing]) {
-        bar_wait(&bars.q_full, seg & 1, dead);
-        ++seg;
-      }
-      const uint32_t st = t % ST;
-      bar_wait(&bars.k_full[st], (t / ST) & 1, dead);
-      fence_after();
-      if (elect() && !*dead) {
-        const uint32_t d = tmem + kColS + (t & 1) * kKeys;
-        const uint64_t b = k_desc + st * (TL::kBytes >> 4);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ts(d, tmem + kColQ + k * 8, b + (k / 4) * (kKeys * 128 >> 4) + (k % 4) * (32 >> 4),
-                 instr_desc(kKeys, false), k > 0);
-        mma_commit(&bars.k_empty[st]);
-        mma_commit(&bars.s_full[t & 1]);
-      }
-      __syncwarp();
-    };
-    if (sKeys[0] > 0) scores(0);
-    for (; sKeys[n % kRing] > 0; ++n) {
-      const uint32_t next = (n + 1) % kRing;
-      const bool follows = sKeys[next] > 0, first = sFirst[next] != 0;
-      // The next scores' buffer is free when the product with the weights in it is
-      // done.  Within a unit they go before this tile's weighted V; a new unit's
-      // wait for its Q, so they go behind.
-      if (n > 0) bar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, dead);
-      if (follows && !first) scores(n + 1);
-      if (posted < n + kAhead && !ended) lookup(true);  // while the weights are computed
+    for (; sKeys[n % kRing] > 0 && !*dead; ++n) {
       const uint32_t st = n % ST;
       bar_wait(&bars.v_full[st], (n / ST) & 1, dead);
       bar_wait(&bars.p_full[n & 1], (n >> 1) & 1, dead);
@@ -645,7 +635,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         mma_commit(&bars.pv_done[n & 1]);
       }
       __syncwarp();
-      if (follows && first) scores(n + 1);
+      if (posted < n + kAhead && !ended) lookup(true);  // while the next weights are computed
     }
   } else {
     // ---- Thread t of the converters: chunk ch (16 bytes) of rows row + kPer p.
@@ -732,9 +722,11 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   }
 
   // Every product has finished before tensor memory is given back.
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp || warp == kValueWarp) {
     if (elect()) mma_commit(&bars.end);
     __syncwarp();
+  }
+  if (warp == kScoreWarp) {
     const long long begin = clock64();
     while (!bar_try(&bars.end, 0) && clock64() - begin < 4000000000ll) {
     }
@@ -742,7 +734,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == kMmaWarp)
+  if (warp == kScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
 }
 
