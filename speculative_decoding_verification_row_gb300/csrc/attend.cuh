@@ -83,7 +83,7 @@ struct Division {
 };
 
 // x / n: 32-bit arithmetic where it suffices (a 64-bit division takes hundreds of clocks).
-__device__ __forceinline__ long quotient(long x, long n) {
+static __device__ __noinline__ long quotient(long x, long n) {
   return (x | n) >> 31 ? x / n : (long)((unsigned)x / (unsigned)n);
 }
 // A line of `total` cells in n shares: the first `more` of them hold one cell
@@ -115,14 +115,18 @@ struct Walk {
   long unit0;        // first cell of u
   Shares shares;
   int tile0, tile1;  // the segment
-  // To the next segment; false at the share's end.
-  __device__ __forceinline__ bool next(const AttendArgs& a) {
+  // To the next segment; false at the share's end.  For one thread, on a walk
+  // in shared memory; not inlined: the kernels' code has to stay in the
+  // instruction caches.
+  __device__ __noinline__ bool next(const AttendArgs& a) {
     for (;;) {
       if (at >= end) return false;
       const long unit1 = unit0 + COST + u.tiles;
       if (at == unit1) {
         unit0 = unit1;
-        if (!Division<ROWS, KEYS>::next(a, u)) return false;
+        Unit n = u;
+        if (!Division<ROWS, KEYS>::next(a, n)) return false;
+        u = n;
         continue;
       }
       const long stop = min(end, unit1);

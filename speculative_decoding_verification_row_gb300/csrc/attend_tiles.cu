@@ -163,6 +163,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 // The two softmax warps of the same rows.
+__device__ __forceinline__ void soft_sync() {  // all softmax warps
+  asm volatile("barrier.cta.sync 5, %0;" ::"n"(kSoftWarps * 32) : "memory");
+}
 __device__ __forceinline__ void pair_sync(int warp) {
   asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
 }
@@ -205,6 +208,13 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   __shared__ const uint8_t* sPage[kRing][kGroups];  // K rows of each 16-key group
   __shared__ int sKeys[kRing], sPrefix[kRing], sFirst[kRing];  // see the lookup
   __shared__ float sTop[2][2][kRows], sAux[2][2][kRows];  // what the two threads of a row tell each other
+  // the walk of the softmax warps and that of the lookup; the segment that thread 0 found
+  using Walker = Walk<kRows, kKeys, kUnitCost>;
+  __shared__ Walker sWalk[2];
+  __shared__ struct {
+    Unit u;
+    int tile0, tile1, whole, last, more;
+  } sSeg;
   __shared__ uint32_t sTmem;
   __shared__ int sDead, sNan;
   const KvCache& c = a.c;
@@ -233,8 +243,9 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     sDead = 0;
     sNan = 0;
   }
-  Walk<kRows, kKeys, kUnitCost> v;
-  if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, v)) return;
+  if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, sWalk[0])) return;
+  __syncthreads();  // every thread has stored the walk's beginning
+  if (tid == 0) sWalk[1] = sWalk[0];
   if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sTmem)),
@@ -312,107 +323,13 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       __syncwarp();
       if (lane == 0) bar_arrive(&bars.q_full);
     };
-    bool more = v.next(a);
-    if (more) load_q(v.u);
-    while (more) {
-      const Unit u = v.u;
-      const int tile0 = v.tile0, tile1 = v.tile1;
-      const bool whole = v.whole();
-      const int last = tile0 == 0 && !whole ? v.last_cta() : 0;
-      const int my_rows = rows, my_i = i, my_head = head;
-      float m = -INFINITY, l = 0.f, vref = 0.f;
+    Unit u = {};
+    int tile0 = 0, tile1 = 0, last = 0;
+    bool whole = false, any = false;
+    float m = 0.f, l = 0.f, vref = 0.f;
+    auto finish = [&](int my_rows, int my_i, int my_head) {
       bool bad = u.w < 0;
       if (u.w >= 0) {
-        for (int tile = tile0; tile < tile1; ++tile, ++n) {
-          const int ring = n % kRing;
-          bar_wait(&bars.pages[ring], (n / kRing) & 1, dead);
-          const float4 k4 = reinterpret_cast<const float4*>(sK[ring])[half];
-          const float4 log4 = reinterpret_cast<const float4*>(sLog[ring])[half];
-          const float4 inv4 = reinterpret_cast<const float4*>(sInv[ring])[half];
-          const float grow = sGrow[ring];
-          float kf[4] = {k4.x * qs, k4.y * qs, k4.z * qs, k4.w * qs};
-          const float lv[4] = {log4.x, log4.y, log4.z, log4.w}, iv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y)  // -inf times it stays -inf; NaN (no such block) stays NaN
-            kf[y] = kf[y] < 0x1p-120f ? 0x1p-120f : kf[y];
-          bar_wait(&bars.s_full[n & 1], (n >> 1) & 1, dead);
-          fence_after();
-          float s[64];
-          tmem_ld32(s, lanes + kColS + (n & 1) * kKeys + half * 64);
-          tmem_ld32(s + 32, lanes + kColS + (n & 1) * kKeys + half * 64 + 32);
-          tmem_wait_ld();
-          const long k0 = (long)tile * kKeys + half * 64 - u.seq;  // window place of s[0]
-          if ((tile + 1) * kKeys > seen_by_all(a, u)) {
-#pragma unroll
-            for (int x = 0; x < 64; x += 32) {
-              const unsigned bits = seen_bits(a, u, i, k0 + x);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(bits >> k & 1)) s[x + k] = -INFINITY;
-            }
-          }
-          float top = -INFINITY;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              t0 = max3(t0, s[y * 16 + k], s[y * 16 + k + 1]);
-              t1 = max3(t1, s[y * 16 + k + 2], s[y * 16 + k + 3]);
-            }
-            top = fmaxf(top, fmaxf(t0, t1) * kf[y]);
-          }
-          sTop[n & 1][half][r] = top;
-          pair_sync(warp);
-          top = fmaxf(top, sTop[n & 1][half ^ 1][r]);
-          const bool move = top > m + kLazy;
-          if (__any_sync(~0u, move || grow != 1.f)) {
-            const float now = move ? top : m;
-            const float al = move ? ex2(m - now) : 1.f;
-            m = now;
-            l *= al;
-            if (tile > tile0) {
-              const float ar = al * grow;
-              bar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, dead);
-              fence_after();
-#pragma unroll 1
-              for (int x = half * HD; x < half * HD + HD; x += 16) {
-                uint32_t o[16];
-                tmem_ld16(o, lanes + kColO + x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ar);
-                tmem_st16(lanes + kColO + x, o);
-              }
-            }
-          }
-          // V's scale goes into the exponent, and out of the sum again
-          const float add = m == -INFINITY ? 0.f : kPBits - m;
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            uint32_t p[16];
-#pragma unroll
-            for (int y = 2 * z; y < 2 * z + 2; ++y) {
-              const float av = add + lv[y];
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const int x = y * 16 + k;
-                float2 e = fma2(make_float2(s[x], s[x + 1]), make_float2(kf[y], kf[y]), make_float2(av, av));
-                e = make_float2(ex2(e.x), ex2(e.y));
-                sum = add2(sum, e);
-                p[(x & 31) / 2] = half2_of(e.x, e.y);
-              }
-              l = fmaf(sum.x + sum.y, iv[y], l);
-            }
-            // over this thread's scores, all of which it has read
-            tmem_st16(lanes + kColS + (n & 1) * kKeys + half * 64 + z * 16, p);
-          }
-          tmem_wait_st();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&bars.p_full[n & 1]);
-        }
         if (tile1 == u.tiles) {  // a window block that these rows do not read is checked all the same
           const int32_t* table = c.tables + (size_t)u.b * c.max_blocks;
           bool miss = false;
@@ -420,12 +337,6 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
             miss = miss || table[x] < 0 || table[x] >= c.num_blocks;
           bad = __any_sync(~0u, miss);
         }
-      }
-      // The next unit's Q goes in before this one's result comes out: its
-      // first scores are computed meanwhile (all of this unit's are done).
-      more = v.next(a);
-      if (more) load_q(v.u);
-      if (u.w >= 0) {
         sAux[1][half][r] = l;
         pair_sync(warp);
         l += sAux[1][half ^ 1][r];
@@ -505,6 +416,125 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         d[4] = my_rows;
       }
       fence_before();  // O has been read: the next unit's first product follows this thread's p_full
+    };
+    // Segment by segment; the next one's Q goes in before this one's result
+    // comes out: its first scores are computed meanwhile (all of this one's are
+    // done).
+    auto find_next = [&]() {
+      Walker& v = sWalk[0];
+      sSeg.more = v.next(a);
+      sSeg.u = v.u;
+      sSeg.tile0 = v.tile0;
+      sSeg.tile1 = v.tile1;
+      sSeg.whole = v.whole();
+      sSeg.last = v.tile0 == 0 && !v.whole() && sSeg.more ? v.last_cta() : 0;
+    };
+    if (tid == 0) find_next();
+    for (;;) {
+      soft_sync();
+      const bool more = sSeg.more;
+      const int my_rows = rows, my_i = i, my_head = head;
+      if (more) load_q(sSeg.u);
+      if (any) finish(my_rows, my_i, my_head);
+      if (!more) break;
+      u = sSeg.u;
+      tile0 = sSeg.tile0, tile1 = sSeg.tile1, last = sSeg.last;
+      whole = sSeg.whole;
+      any = true;
+      soft_sync();  // sSeg has been read
+      if (tid == 0) find_next();
+      m = -INFINITY, l = 0.f, vref = 0.f;
+      if (u.w < 0) continue;
+      for (int tile = tile0; tile < tile1; ++tile, ++n) {
+        const int ring = n % kRing;
+        bar_wait(&bars.pages[ring], (n / kRing) & 1, dead);
+        const float4 k4 = reinterpret_cast<const float4*>(sK[ring])[half];
+        const float4 log4 = reinterpret_cast<const float4*>(sLog[ring])[half];
+        const float4 inv4 = reinterpret_cast<const float4*>(sInv[ring])[half];
+        const float grow = sGrow[ring];
+        float kf[4] = {k4.x * qs, k4.y * qs, k4.z * qs, k4.w * qs};
+        const float lv[4] = {log4.x, log4.y, log4.z, log4.w}, iv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y)  // -inf times it stays -inf; NaN (no such block) stays NaN
+          kf[y] = kf[y] < 0x1p-120f ? 0x1p-120f : kf[y];
+        bar_wait(&bars.s_full[n & 1], (n >> 1) & 1, dead);
+        fence_after();
+        float s[64];
+        tmem_ld32(s, lanes + kColS + (n & 1) * kKeys + half * 64);
+        tmem_ld32(s + 32, lanes + kColS + (n & 1) * kKeys + half * 64 + 32);
+        tmem_wait_ld();
+        const long k0 = (long)tile * kKeys + half * 64 - u.seq;  // window place of s[0]
+        if ((tile + 1) * kKeys > seen_by_all(a, u)) {
+#pragma unroll
+          for (int x = 0; x < 64; x += 32) {
+            const unsigned bits = seen_bits(a, u, i, k0 + x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!(bits >> k & 1)) s[x + k] = -INFINITY;
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            t0 = max3(t0, s[y * 16 + k], s[y * 16 + k + 1]);
+            t1 = max3(t1, s[y * 16 + k + 2], s[y * 16 + k + 3]);
+          }
+          top = fmaxf(top, fmaxf(t0, t1) * kf[y]);
+        }
+        sTop[n & 1][half][r] = top;
+        pair_sync(warp);
+        top = fmaxf(top, sTop[n & 1][half ^ 1][r]);
+        const bool move = top > m + kLazy;
+        if (__any_sync(~0u, move || grow != 1.f)) {
+          const float now = move ? top : m;
+          const float al = move ? ex2(m - now) : 1.f;
+          m = now;
+          l *= al;
+          if (tile > tile0) {
+            const float ar = al * grow;
+            bar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, dead);
+            fence_after();
+#pragma unroll 1
+            for (int x = half * HD; x < half * HD + HD; x += 16) {
+              uint32_t o[16];
+              tmem_ld16(o, lanes + kColO + x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ar);
+              tmem_st16(lanes + kColO + x, o);
+            }
+          }
+        }
+        // V's scale goes into the exponent, and out of the sum again
+        const float add = m == -INFINITY ? 0.f : kPBits - m;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          uint32_t p[16];
+#pragma unroll
+          for (int y = 2 * z; y < 2 * z + 2; ++y) {
+            const float av = add + lv[y];
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const int x = y * 16 + k;
+              float2 e = fma2(make_float2(s[x], s[x + 1]), make_float2(kf[y], kf[y]), make_float2(av, av));
+              e = make_float2(ex2(e.x), ex2(e.y));
+              sum = add2(sum, e);
+              p[(x & 31) / 2] = half2_of(e.x, e.y);
+            }
+            l = fmaf(sum.x + sum.y, iv[y], l);
+          }
+          // over this thread's scores, all of which it has read
+          tmem_st16(lanes + kColS + (n & 1) * kKeys + half * 64 + z * 16, p);
+        }
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.p_full[n & 1]);
+      }
     }
   } else if (warp == kScoreWarp) {
     for (uint32_t seg = 0;; ++n) {
@@ -536,12 +566,11 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     // ---- the lookup, up to four tiles of a segment at a time: block ids, then
     // scales, then the ring, a call apart each, so that no use waits for its
     // load.  Lane x: group x % 8 of the batch's tile x / 8.
-    bool more = v.next(a);
-    auto skip = [&]() {
-      while (more && v.u.w < 0) more = v.next(a);
-    };
-    skip();
-    int tile = more ? v.tile0 : 0, keys = more ? (int)Div::seen(a, v.u.seq, v.u.w, v.u.mt) : 0;
+    // the walk's segment: lane 0 walks, all copy
+    Walker& v = sWalk[1];
+    Unit u = {};
+    int tile = 0, tile0 = 0, tile1 = 0, keys = 0;
+    bool more = true;
     const int my_tile = lane >> 3;
     // stage 1: block ids under way
     int blk = -2, grp1 = 0, unit_h = 0, count1 = 0, keys1 = 0, all1 = 0;
@@ -596,29 +625,42 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       count2 = count1, keys2 = keys1, all2 = all1, first2 = first1;
       count1 = 0;
       blk = -2;
+      while (more && tile == tile1) {  // a new segment; those without keys are skipped
+        bool left = false;
+        if (lane == 0) left = v.next(a);
+        more = __shfl_sync(~0u, left, 0);
+        __syncwarp();
+        u = v.u;
+        tile = tile0 = v.tile0;
+        tile1 = more && u.w >= 0 ? v.tile1 : tile0;
+        keys = (int)Div::seen(a, u.seq, u.w, u.mt);
+        __syncwarp();
+      }
       if (more) {
         const int k0 = tile * kKeys;
-        count1 = min(4, v.tile1 - tile);
+        count1 = min(4, tile1 - tile);
         keys1 = keys - k0;
-        all1 = seen_by_all(a, v.u) - k0;
-        first1 = tile == v.tile0;
-        unit_h = v.u.h;
+        all1 = seen_by_all(a, u) - k0;
+        first1 = tile == tile0;
+        unit_h = u.h;
         grp1 = tile * kGroups + lane;
         if (my_tile < count1 && grp1 * 16 < keys)
-          blk = c.tables[(size_t)v.u.b * c.max_blocks + col16(a, grp1)];
+          blk = c.tables[(size_t)u.b * c.max_blocks + col16(a, grp1)];
         tile += count1;
-        if (tile == v.tile1) {
-          more = v.next(a);
-          skip();
-          if (more) tile = v.tile0, keys = (int)Div::seen(a, v.u.seq, v.u.w, v.u.mt);
-        }
       }
     };
-    lookup(false);
-    lookup(false);
-    while (posted < kAhead && !ended) lookup(true);
-
-    for (; sKeys[n % kRing] > 0 && !*dead; ++n) {
+    // One loop, so that the lookup is in the code once: calls -2 and -1 fill its
+    // stages, those up to `ready` the ring, the others go between the products.
+    int calls = -2;
+    bool ready = false;
+    for (;;) {
+      if (!ended && posted < n + kAhead) {
+        lookup(calls >= 0);  // while the next weights are computed
+        ++calls;
+        if (!ready) continue;
+      }
+      ready = true;
+      if (sKeys[n % kRing] == 0 || *dead) break;
       const uint32_t st = n % ST;
       bar_wait(&bars.v_full[st], (n / ST) & 1, dead);
       bar_wait(&bars.p_full[n & 1], (n >> 1) & 1, dead);
@@ -635,7 +677,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         mma_commit(&bars.pv_done[n & 1]);
       }
       __syncwarp();
-      if (posted < n + kAhead && !ended) lookup(true);  // while the next weights are computed
+      ++n;
     }
   } else {
     // ---- Thread t of the converters: chunk ch (16 bytes) of rows row + kPer p.
