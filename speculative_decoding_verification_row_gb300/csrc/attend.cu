@@ -6,8 +6,14 @@ using namespace sv;
 
 namespace {
 
-// Rows per KV head up to which attend_rows.cu is taken.
-bool few_rows(long W, int G) { return W * G <= 32; }
+// Whether attend_rows.cu serves this many rows per KV head; else attend_tiles.cu.
+// The first reads the cache once for every 16 rows, the second once for 128 at
+// a step's fixed cost.  Measured with 64 requests of 4096 cached positions and
+// 8 KV heads: D = 128, rows 109 us for 16 rows and 194 for 20, tiles 172 for
+// both; D = 64, rows 67 us for 16 and 120 for 32, tiles 141 (and 224 against
+// 144 for 64).  With 4 requests of 30000 and D = 128: rows 61 us for 16 and 93
+// for 32, tiles 78.
+bool few_rows(int W, int G, int D) { return (long)W * G <= (D == 64 ? 32 : 16); }
 
 }  // namespace
 
@@ -18,7 +24,7 @@ size_t spec_attend_scratch_size(int B, int W, int q_heads, int kv_heads, int hea
       kv_heads > 1024 || q_heads < 1 || q_heads > 16384 || q_heads % kv_heads != 0 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return few_rows(W, q_heads / kv_heads) ? attend_rows_scratch(head_dim)
+  return few_rows(W, q_heads / kv_heads, head_dim) ? attend_rows_scratch(head_dim)
                                          : attend_tiles_scratch(head_dim);
 }
 
@@ -54,7 +60,7 @@ int spec_attend_kv(const spec_kv_cache* cache, const spec_attend_params* p, void
   a.scale_log2 = (float)((double)p->scale * 1.4426950408889634073599246810019);
   a.out = static_cast<char*>(p->out);
   a.lse = p->out_lse;
-  const cudaError_t e = few_rows(a.W, a.G)
+  const cudaError_t e = few_rows(a.W, a.G, a.c.D)
                             ? launch_attend_rows(a, p->dtype, scratch, (cudaStream_t)stream)
                             : launch_attend_tiles(a, p->dtype, scratch, (cudaStream_t)stream);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;

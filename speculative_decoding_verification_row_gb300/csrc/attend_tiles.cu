@@ -195,6 +195,10 @@ __device__ __noinline__ unsigned seen_bits(const AttendArgs& a, const Unit& u, i
   return bits;
 }
 
+__device__ __forceinline__ void give_back(uint32_t tmem) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const AttendArgs a) {
   using TL = Tile<D>;
@@ -219,9 +223,6 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   __shared__ int sDead, sNan;
   const KvCache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid < kDescWords) a.desc[blockIdx.x * kDescWords + tid] = -1;
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       bar_init(&bars.k_full[i], kConvWarps);
@@ -243,9 +244,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     sDead = 0;
     sNan = 0;
   }
-  if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, sWalk[0])) return;
-  __syncthreads();  // every thread has stored the walk's beginning
-  if (tid == 0) sWalk[1] = sWalk[0];
+  // none of this touches what the kernel before may still write
   if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sTmem)),
@@ -253,6 +252,15 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid < kDescWords) a.desc[blockIdx.x * kDescWords + tid] = -1;
+  if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, sWalk[0])) {
+    if (warp == kScoreWarp) give_back(sTmem);
+    return;
+  }
+  __syncthreads();  // every thread has stored the walk's beginning
+  if (tid == 0) sWalk[1] = sWalk[0];
   fence_before();
   __syncthreads();
   fence_after();
@@ -391,10 +399,11 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(part + (size_t)r * D + x + 4 * k) = make_float4(
-                  o[4 * k] * f, o[4 * k + 1] * f,
-                  o[4 * k + 2] * f, o[4 * k + 3] * f);
+            for (int k = 0; k < 32; k += 8)  // whole sectors: every lane has a row of its own
+              asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(part + (size_t)r * D + x + k),
+                           "f"(o[k] * f), "f"(o[k + 1] * f), "f"(o[k + 2] * f), "f"(o[k + 3] * f), "f"(o[k + 4] * f),
+                           "f"(o[k + 5] * f), "f"(o[k + 6] * f), "f"(o[k + 7] * f)
+                           : "memory");
           }
         }
         __syncwarp();
@@ -776,8 +785,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == kScoreWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  if (warp == kScoreWarp) give_back(tmem);
 }
 
 }  // namespace
