@@ -488,7 +488,7 @@ int spec_tree_masks(const int32_t *paths, int B, int P, int L, int N, int32_t *m
 /* A paged KV cache in 8 bits (e4m3) with one scale per block of tokens, K or
  * V, and head.
  *   pool   [num_blocks, 2, kv_heads, tokens_per_block, head_dim] e4m3 bytes,
- *          16-byte aligned (index 0 of the second axis: K, 1: V);
+ *          32-byte aligned (index 0 of the second axis: K, 1: V);
  *   scales [num_blocks, 2, kv_heads] float32: an element is its e4m3 value
  *          times the scale.  Scales are finite and >= 0; spec_store_kv makes
  *          powers of two (0 for a block of zeros).

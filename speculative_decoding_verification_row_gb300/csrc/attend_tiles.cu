@@ -195,6 +195,11 @@ __device__ __noinline__ unsigned seen_bits(const AttendArgs& a, const Unit& u, i
   return bits;
 }
 
+__device__ __forceinline__ void load32(uint32_t (&x)[8], const void* p) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+               : "l"(p));
+}
 __device__ __forceinline__ void give_back(uint32_t tmem) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
 }
@@ -689,17 +694,17 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       ++n;
     }
   } else {
-    // ---- Thread t of the converters: chunk ch (16 bytes) of rows row + kPer p.
-    // Eight neighbours hold four chunks of two rows, which keeps their
-    // 16-byte stores below off each other's banks.
-    constexpr int CPR = D / 16, kPer = kConvThreads / CPR, NP = (kKeys + kPer - 1) / kPer;
-    static_assert(kConvThreads % CPR == 0 && kPer % 4 == 0 && NP <= 8, "converter layout");
+    // ---- Thread t of the converters: chunk ch (32 bytes) of rows row + kPer p.
+    // Eight neighbours hold two chunks of four rows, one atom's, which keeps
+    // their 16-byte stores below off each other's banks.
+    constexpr int CPR = D / 32, kPer = kConvThreads / CPR, NP = (kKeys + kPer - 1) / kPer;
+    static_assert(kConvThreads % CPR == 0 && kPer % 8 == 0, "converter layout");
     const int t = tid - kConvWarp * 32;
-    const int ch = D == 128 ? (t & 3) | (t >> 1 & 4) : t & 3;
-    const int row = D == 128 ? (t >> 2 & 1) | t >> 4 << 1 : t >> 2;
+    const int ch = D == 128 ? (t & 1) | (t >> 2 & 2) : t & 1;
+    const int row = D == 128 ? (t >> 1 & 3) | t >> 4 << 2 : t >> 1;
     const size_t v_off = (size_t)c.H * c.tpb * D;  // from a block's K rows to its V rows
     // the rows of tile `at`; false behind the last
-    auto load = [&](uint4 (&x)[NP], uint4 (&y)[NP], uint32_t at) {
+    auto load = [&](uint32_t (&x)[NP][8], uint32_t (&y)[NP][8], uint32_t at) {
       bar_wait(&bars.pages[at % kRing], (at / kRing) & 1, dead);
       if (sKeys[at % kRing] == 0 || *dead) return false;
       const uint8_t* const* page = sPage[at % kRing];
@@ -707,27 +712,27 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       for (int p = 0; p < NP; ++p) {
         const int r = p * kPer + row;
         if (p * kPer + kPer <= kKeys || r < kKeys) {
-          const uint8_t* src = page[r >> 4] + ((r & 15) * D + ch * 16);
-          x[p] = *reinterpret_cast<const uint4*>(src);
-          y[p] = *reinterpret_cast<const uint4*>(src + v_off);
+          const uint8_t* src = page[r >> 4] + ((r & 15) * D + ch * 32);
+          load32(x[p], src);
+          load32(y[p], src + v_off);
         }
       }
       return true;
     };
-    // places of the two fp16 vectors of row `row`; row + kPer is kPer % 8 = 4 rows on in the swizzle
-    const int atom = (ch >> 2) * (kKeys * 128) + row * 128, c0 = (ch & 3) * 2;
-    const int o0 = atom + ((c0 ^ (row & 7)) << 4), o1 = atom + (((c0 + 1) ^ (row & 7)) << 4);
-    auto put = [&](const uint4 (&x)[NP], unsigned char* tile) {
+    // places of the four fp16 vectors of row `row` (kPer is a multiple of the swizzle's 8 rows)
+    const int atom = (ch >> 1) * (kKeys * 128) + row * 128, c0 = (ch & 1) * 4;
+    auto put = [&](const uint32_t (&x)[NP][8], unsigned char* tile) {
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         if (p * kPer + kPer <= kKeys || p * kPer + row < kKeys) {
-          const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-          uint32_t h[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) e4m3x4_to_half(w[k], h[2 * k], h[2 * k + 1]);
-          const int flip = p * kPer & 4 ? 64 : 0;
-          *reinterpret_cast<uint4*>(tile + p * kPer * 128 + (o0 ^ flip)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(tile + p * kPer * 128 + (o1 ^ flip)) = make_uint4(h[4], h[5], h[6], h[7]);
+          for (int s = 0; s < 4; ++s) {
+            uint32_t h[4];
+            e4m3x4_to_half(x[p][2 * s], h[0], h[1]);
+            e4m3x4_to_half(x[p][2 * s + 1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(tile + p * kPer * 128 + atom + (((c0 + s) ^ (row & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     };
     // Writes tile n and starts to load tile n + 2 into the same registers:
     // two tiles are on their way while a third is written.
-    auto step = [&](uint4 (&kr)[NP], uint4 (&vr)[NP], bool follows) {
+    auto step = [&](uint32_t (&kr)[NP][8], uint32_t (&vr)[NP][8], bool follows) {
       const uint32_t st = n % ST;
       bar_wait(&bars.k_empty[st], ((n / ST) & 1) ^ 1, dead);
       put(kr, tiles + st * TL::kBytes);
@@ -747,14 +752,12 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const int key = p * kPer + row;
-          uint32_t w[4] = {vr[p].x, vr[p].y, vr[p].z, vr[p].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t nb = key >= keys ? 0x80808080u : key >= prefix ? nan_bytes(w[k]) : 0u;
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t nb = key >= keys ? 0x80808080u : key >= prefix ? nan_bytes(vr[p][k]) : 0u;
             if (nb && key < keys) sNan = 1;
-            w[k] &= ~((nb >> 7) * 255u);
+            vr[p][k] &= ~((nb >> 7) * 255u);
           }
-          vr[p] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       bar_wait(&bars.v_empty[st], ((n / ST) & 1) ^ 1, dead);
@@ -763,7 +766,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       ++n;
       return follows && load(kr, vr, n + 1);
     };
-    uint4 ka[NP], va[NP], kb[NP], vb[NP];
+    uint32_t ka[NP][8], va[NP][8], kb[NP][8], vb[NP][8];
     bool in_a = load(ka, va, 0), in_b = in_a && load(kb, vb, 1);
     while (in_a) {
       in_a = step(ka, va, in_b);

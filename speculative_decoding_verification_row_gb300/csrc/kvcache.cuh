@@ -38,7 +38,7 @@ inline int kv_setup(const spec_kv_cache* s, KvCache* c) {
   if (s->num_blocks < 1 || s->max_blocks < 1 || s->tokens_per_block < 16 ||
       s->tokens_per_block > 1024 || s->tokens_per_block % 16 != 0 || s->kv_heads < 1 ||
       s->kv_heads > 1024 || (s->head_dim != 64 && s->head_dim != 128) ||
-      reinterpret_cast<uintptr_t>(s->pool) % 16 != 0)
+      reinterpret_cast<uintptr_t>(s->pool) % 32 != 0)
     return SPEC_EINVAL;
   *c = KvCache{static_cast<uint8_t*>(s->pool), s->scales, s->block_tables, s->num_blocks,
                s->max_blocks, s->tokens_per_block, s->kv_heads, s->head_dim};
