@@ -239,84 +239,88 @@ __device__ __forceinline__ float row_lse(float M, float L) {
 }
 
 // Joins the units that several CTAs worked on: CTA (i, y) serves rows
-// [16 y, 16 y + 16) of the unit that began in CTA i and did not end there.
-// Four threads sets take every fourth part, all of a set's loads in flight
-// together, and are joined in turn: in an order that depends on the division
-// alone, so the result does not depend on timing.
+// [16 y, 16 y + 16) of the unit that began in CTA i and did not end there.  A
+// warp per row, or 2, 4 or 8 where the unit has few: these take turns at the
+// parts, kJoinBatch parts' loads in flight together, and are joined in the
+// end, in an order that depends on the division alone, so the result does not
+// depend on timing.
 constexpr int kJoinRows = 16;
-constexpr int kJoinSets = 4;
-constexpr int kJoinThreads = kJoinRows * 8 * kJoinSets;
+constexpr int kJoinBatch = 6;
+constexpr int kJoinThreads = kJoinRows * 32;
+
+// A row's partial result: its maximum, sum and the E elements of a lane.
+template <int E>
+struct Part {
+  float m, l, x[E];
+  __device__ __forceinline__ void add(float pm, float pl, const float* px) {
+    if (pm == -INFINITY && pl == 0.f) return;
+    const float now = fmaxf(m, pm);
+    const float fo = m == now ? 1.f : ex2(m - now), fn = pm == now ? 1.f : ex2(pm - now);
+    m = now;
+    l = l * fo + pl * fn;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = x[e] * fo + px[e] * fn;
+  }
+};
 
 template <class T, int D, int ROWS, int KEYS>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a) {
-  constexpr int NT = D / 8;  // elements per thread, 8 threads per row
-  __shared__ float sM[kJoinSets][kJoinRows], sL[kJoinSets][kJoinRows];
-  __shared__ __align__(16) float sX[kJoinSets - 1][kJoinRows * 8][NT + 4];
+__global__ void __launch_bounds__(kJoinThreads, 2) attend_join_kernel(const AttendArgs a) {
+  constexpr int E = D / 32;  // elements of a lane: 2 or 4
+  __shared__ Part<E> sPart[kJoinRows][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int first = blockIdx.x;
   const int4 d = reinterpret_cast<const int4*>(a.desc)[2 * first];
+  const int rows = reinterpret_cast<const int*>(a.desc)[8 * first + 4];
   if (d.x < 0) return;
-  const int last = d.w, rows = reinterpret_cast<const int*>(a.desc)[8 * first + 4];
-  const int set = threadIdx.x / (kJoinRows * 8), t = threadIdx.x % (kJoinRows * 8);
-  const int r = blockIdx.y * kJoinRows + (t >> 3), part = t & 7;
-  if (blockIdx.y * kJoinRows >= rows) return;
-  const int from = min(r, rows - 1);  // every thread stays for the barrier
-  float M = -INFINITY, L = 0.f, x[NT] = {};
-#pragma unroll 2
-  for (int i = first + set; i <= last; i += kJoinSets) {
-    const float* p = a.part + (2 * (size_t)i + (i == first)) * part_floats<ROWS>(D);
-    const float pm = p[ROWS * D + from], pl = p[ROWS * D + ROWS + from];
-    float4 z[NT / 4];
+  const int last = d.w, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int mine = min(rows - (int)blockIdx.y * kJoinRows, kJoinRows);  // this CTA's rows
+  if (mine <= 0) return;
+  const int sets = mine > 8 ? 1 : mine > 4 ? 2 : mine > 2 ? 4 : 8;
+  const int set = warp % sets, r = blockIdx.y * kJoinRows + warp / sets;
+  const bool real = warp / sets < mine;
+  Part<E> sum{-INFINITY, 0.f, {}};
+  if (real) {
+    for (int i = first + set; i <= last; i += sets * kJoinBatch) {
+      float pm[kJoinBatch], pl[kJoinBatch], px[kJoinBatch][E];
 #pragma unroll
-    for (int j = 0; j < NT / 4; ++j)
-      z[j] = *reinterpret_cast<const float4*>(p + from * D + part * NT + 4 * j);
-    if (pm == -INFINITY && pl == 0.f) continue;
-    const float now = fmaxf(M, pm);
-    const float fo = M == now ? 1.f : ex2(M - now), fn = pm == now ? 1.f : ex2(pm - now);
-    M = now;
-    L = L * fo + pl * fn;
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const int at = i + k * sets;
+        const float* p = a.part + (2 * (size_t)at + (at == first)) * part_floats<ROWS>(D);
+        pm[k] = at <= last ? p[ROWS * D + r] : -INFINITY;
+        pl[k] = at <= last ? p[ROWS * D + ROWS + r] : 0.f;
+        if (E == 4) {
+          const float4 z = at <= last ? reinterpret_cast<const float4*>(p + r * D)[lane] : make_float4(0, 0, 0, 0);
+          px[k][0] = z.x, px[k][1] = z.y, px[k][E - 2] = z.z, px[k][E - 1] = z.w;
+        } else {
+          const float2 z = at <= last ? reinterpret_cast<const float2*>(p + r * D)[lane] : make_float2(0, 0);
+          px[k][0] = z.x, px[k][1] = z.y;
+        }
+      }
 #pragma unroll
-    for (int j = 0; j < NT / 4; ++j) {
-      x[4 * j] = x[4 * j] * fo + z[j].x * fn;
-      x[4 * j + 1] = x[4 * j + 1] * fo + z[j].y * fn;
-      x[4 * j + 2] = x[4 * j + 2] * fo + z[j].z * fn;
-      x[4 * j + 3] = x[4 * j + 3] * fo + z[j].w * fn;
+      for (int k = 0; k < kJoinBatch; ++k) sum.add(pm[k], pl[k], px[k]);
     }
   }
-  if (part == 0) sM[set][t >> 3] = M, sL[set][t >> 3] = L;
-  if (set > 0) {
-#pragma unroll
-    for (int j = 0; j < NT; j += 4)
-      *reinterpret_cast<float4*>(&sX[set - 1][t][j]) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+  if (sets > 1) {
+    if (set) sPart[warp][lane] = sum;
+    __syncthreads();
+    if (!set)
+      for (int k = 1; k < sets; ++k) sum.add(sPart[warp + k][lane].m, sPart[warp + k][lane].l, sPart[warp + k][lane].x);
   }
-  __syncthreads();
-  if (set > 0 || r >= rows) return;
-  float top = M;
-#pragma unroll
-  for (int k = 1; k < kJoinSets; ++k) top = fmaxf(top, sM[k][t >> 3]);
-#pragma unroll
-  for (int k = 0; k < kJoinSets; ++k) {
-    const float km = sM[k][t >> 3], kl = sL[k][t >> 3];
-    const float f = km == top ? 1.f : km == -INFINITY && kl == 0.f ? 0.f : ex2(km - top);
-    L = k == 0 ? L * f : L + kl * f;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) x[j] = k == 0 ? x[j] * f : x[j] + sX[k ? k - 1 : 0][t][j] * f;
-  }
-  M = top;
-  const int h = d.y;
+  if (set || !real) return;
   const long row = (long)d.z * ROWS + r;
-  const int i = (int)(row / a.G), head = h * a.G + (int)(row % a.G);
+  const int i = (int)(row / a.G), head = d.y * a.G + (int)(row % a.G);
   const size_t orow = ((size_t)d.x * a.W + i) * a.Hq + head;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint32_t y[NT / 2];
+  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+  uint32_t y[E / 2];
 #pragma unroll
-  for (int j = 0; j < NT; j += 2) y[j / 2] = pack_out(x[j] * inv, x[j + 1] * inv, (T*)nullptr);
-  uint4* dst = reinterpret_cast<uint4*>(a.out + 2 * (orow * D + part * NT));
-#pragma unroll
-  for (int j = 0; j < NT / 8; ++j)
-    dst[j] = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-  if (a.lse && part == 0) a.lse[orow] = row_lse(M, L);
+  for (int e = 0; e < E; e += 2) y[e / 2] = pack_out(sum.x[e] * inv, sum.x[e + 1] * inv, (T*)nullptr);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + 2 * (orow * D + lane * E));
+  if (E == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[E / 2 - 1]);
+  else
+    dst[0] = y[0];
+  if (a.lse && lane == 0) a.lse[orow] = row_lse(sum.m, sum.l);
 }
 
 template <class T, int D, int ROWS, int KEYS>

@@ -29,7 +29,10 @@ constexpr int kRThreads = kRWarps * 32;
 constexpr int kKeys = kStep * kRWarps;    // keys of a tile: one step of every warp
 constexpr int kStages = 4;
 constexpr int kUnitCost = 2;              // cells of a unit besides its tiles
-constexpr int kLeastCells = 6;
+// Cells below which a share is not worth a CTA.  One request, one token, 8 KV
+// heads, 100 / 1000 / 30000 positions: 10.5 / 12.3 / 34.7 us with 3 cells, 9.5
+// / 12.5 / 34.4 with 4, 15.7 / 13.4 / 34.4 with 6, 25.4 / 19.5 / 33.1 with 12.
+constexpr int kLeastCells = 4;
 constexpr int kCtas = 3 * kSms;           // resident at 168 registers and 66 KB of shared memory
 using Div = Division<kRows, kKeys>;
 
@@ -153,10 +156,16 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
       // ---- the ring: step st of the unit = keys [16 st, 16 st + 16)
       int fst = tile0 * kRWarps + warp;               // next step to fetch
       int fcol = fst / tpb16, foff = fst % tpb16;     // its block table column and place there
-      int fblk = fst < steps ? table[fcol] : 0;       // its block, loaded one fetch ahead
+      int fblk = fst < steps ? table[fcol] : 0;       // its block, loaded one fetch ahead ...
       const int dcol = kRWarps / tpb16, doff = kRWarps % tpb16;
       int stage = 0;
-      auto fetch = [&]() {
+      int early[kStages - 1];  // ... but for the first fetches, whose blocks are loaded together
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) {
+        const int st = fst + (i + 1) * kRWarps;
+        early[i] = st < steps ? table[st / tpb16] : 0;
+      }
+      auto fetch = [&](int n) {
         if (fst < steps) {
           const bool ok = fblk >= 0 && fblk < c.num_blocks;
           if (!ok) sBad = 1;
@@ -176,13 +185,16 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
           fcol += dcol;
           foff += doff;
           if (foff >= tpb16) foff -= tpb16, ++fcol;
-          if (fst < steps) fblk = table[fcol];
+          if (n < kStages - 1)
+            fblk = early[n];
+          else if (fst < steps)
+            fblk = table[fcol];
         }
         cp_commit();
         stage = stage + 1 == kStages ? 0 : stage + 1;
       };
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) fetch();
+      for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
       // ---- Q fragments: thread (g, cc) holds elements 16 (cc + 4 x) .. + 15 of rows g and g + 8
       uint32_t qf[U * 4][4];
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
           for (int d = 0; d < 4; ++d) mma16816(o[x * 4 + d], pa, b[0][d], b[1][d]);
         }
         __syncwarp();  // every lane has read the stage that the next fetch may reuse
-        fetch();
+        fetch(kStages);
       }
       cp_wait<0>();
 #pragma unroll

@@ -29,7 +29,7 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
 constexpr int kUnitCost = 4;             // cells of a unit besides its tiles
-constexpr int kLeastCells = 6;
+constexpr int kLeastCells = 4;              // a share below this is not worth a CTA: see attend_rows.cu
 constexpr int kSoftWarps = 8, kScoreWarp = 8, kValueWarp = 9, kConvWarp = 10, kConvWarps = 6;
 constexpr int kTThreads = (kConvWarp + kConvWarps) * 32;
 constexpr int kConvThreads = kConvWarps * 32;
