@@ -16,6 +16,12 @@
 // multiplied by the ratio of their block's V scale to the largest V scale so
 // far, which the sums are held in.  m follows the maximum only when a score
 // exceeds it by more than 7, so that the sums are rarely rescaled.
+//
+// Measured with 32 heads over 8 KV heads of 128 and windows of 4 tokens: 256
+// requests of 8192 positions 689 us, 6.2 TB/s (0.92 of the measured copy rate);
+// 256 of 512 to 8192, 406 us, 5.6 TB/s (0.83).  One token of one request over
+// 1000 positions takes 12.3 us in a graph, both launches: latency (the shares,
+// the table, the rows, the four warps' merge, the join).
 #include "attend.cuh"
 
 namespace sv {

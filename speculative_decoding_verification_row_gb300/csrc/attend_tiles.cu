@@ -20,6 +20,12 @@
 // Tensor memory: Q, S (two buffers; the weights replace the scores there), O.
 //
 // Scales, weights and lazy rescaling are as in attend_rows.cu.
+//
+// Measured with 32 heads over 8 KV heads of 128: 16 trees of 60 tokens over
+// 8192 positions 174 us, 740 TFLOP/s (0.39 of the measured dense rate; 16 of
+// the 256 rows are empty); over 512 to 8192, 108 us.  A tile takes about 2200
+// clocks where its products take 1024: the hops weights -> product -> scores of
+// a row's chain, and the conversion of the pages, which the products wait for.
 #include "attend.cuh"
 
 namespace sv {

@@ -8,8 +8,11 @@
 // fall below the normal range (2^-6 s), and the consumers' products with the
 // scales are exact as well.
 //
-// Both are bound by latency at a step's sizes (a few hundred KB) and by HBM
-// for prompts.
+// Both are bound by latency: table -> rows -> maximum -> codes.  In a graph
+// (operands in L2) the store of 64 requests of 8 tokens, 8 heads of 128 takes
+// 6.0 us, that of 4 prompts of 4001 tokens, 4 heads of 64, 5.4 us (6.2 MB:
+// 1.2 TB/s); the relocation of 16 requests' paths of 4 takes 3.9 us, of 256
+// requests' paths of 17 7.2 us.
 #include "kvcache.cuh"
 
 namespace sv {
