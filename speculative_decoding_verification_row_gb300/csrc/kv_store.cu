@@ -8,10 +8,11 @@
 // fall below the normal range (2^-6 s), and the consumers' products with the
 // scales are exact as well.
 //
-// Both are bound by latency: table -> rows -> maximum -> codes.  In a graph
-// (operands in L2) the store of 64 requests of 8 tokens, 8 heads of 128 takes
-// 6.0 us, that of 4 prompts of 4001 tokens, 4 heads of 64, 5.4 us (6.2 MB:
-// 1.2 TB/s); the relocation of 16 requests' paths of 4 takes 3.9 us, of 256
+// At a step's sizes both are bound by latency: table -> rows -> maximum ->
+// codes.  In a graph (operands in L2) the store of 64 requests of 8 tokens, 8
+// heads of 128 takes 3.8 us, that of 4 prompts of 4001 tokens, 4 heads of 64,
+// 5.4 us; 64 prompts of 4096 tokens with 8 heads of 128, 280 us, 5.75 TB/s (0.85
+// of the measured copy rate).  The relocation of 16 requests' paths of 4 takes 3.9 us, of 256
 // requests' paths of 17 7.2 us.
 #include "kvcache.cuh"
 
@@ -26,6 +27,7 @@ struct StoreArgs {
   const int32_t* seq;
   const int32_t* win;
   int B, W, pages;
+  int split;  // CTAs per block of a request's window
 };
 
 template <class T>
@@ -66,20 +68,23 @@ __device__ __forceinline__ uint2 quant8(uint4 v, float r) {
 }
 
 constexpr int kStoreThreads = 128;
-constexpr int kStoreVecs = 8;  // 16-byte vectors a thread keeps between the two passes
 
-// One CTA = one block of one request's window, one kind, one head: the
-// largest magnitude of the new rows, the scale, the codes.  The rows stay in
-// registers between the passes up to 8192 elements (64 rows of 128); what a
-// larger block holds beyond that is read again (from L2).
-template <class T>
-__global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a) {
+// A unit is one block of one request's window, one kind, one head: the
+// largest magnitude of the new rows, the scale, the codes.  WARPS warps serve
+// it (1, or the CTA's 4) and a CTA takes (kind, head) pairs of one block: one
+// round of them in a small call, all in a large one, so that the window's
+// blocks are checked once.  The rows stay in registers between the passes, VECS 16-byte vectors
+// a lane; what a larger block holds beyond that is read again (from L2).  With
+// the CTA per unit 9 CTAs share an SM (56 registers; 80 and 6 without the
+// bound: 333 us instead of 300 with blocks of 64 tokens).
+template <class T, int WARPS, int VECS>
+__global__ void __launch_bounds__(kStoreThreads, WARPS > 1 ? 9 : 0) store_kernel(const StoreArgs a) {
+  constexpr int kUnits = kStoreThreads / 32 / WARPS, kLanes = 32 * WARPS;
   const KvCache& c = a.c;
+  const int groups = (2 * c.H + kUnits - 1) / kUnits;
   int u = blockIdx.x;
-  const int h = u % c.H;
-  u /= c.H;
-  const int kind = u & 1;
-  u >>= 1;
+  const int group0 = u % a.split;
+  u /= a.split;
   const int page = u % a.pages, b = u / a.pages;
   const long seq = a.seq[b];
   const int w = a.win ? a.win[b] : a.W;
@@ -88,69 +93,76 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(const StoreArgs a)
   const int last = (int)((seq + w - 1) / c.tpb);
   if (col > last || last >= c.max_blocks) return;
   __shared__ float sMax[kStoreThreads / 32];
-  __shared__ int sBad;
-  if (threadIdx.x == 0) sBad = 0;
-  __syncthreads();
-  // every CTA of the request checks all of its window's blocks, so they agree
   const int32_t* table = c.tables + (size_t)b * c.max_blocks;
-  for (int i = (int)(seq / c.tpb) + threadIdx.x; i <= last; i += kStoreThreads)
-    if (table[i] < 0 || table[i] >= c.num_blocks) sBad = 1;
+  const int blk = table[col];
+  const bool mapped = blk >= 0 && blk < c.num_blocks;
+  const int lane = threadIdx.x % kLanes;
   const int first = page == 0 ? (int)(seq % c.tpb) : 0;  // first row written
   const int i0 = (int)(col * c.tpb + first - seq);        // its window token
   const int rows = min(c.tpb - first, w - i0);
-  const int vpr = c.D / 8;  // vectors per row
-  const int nvec = rows * vpr;
-  const char* src = a.x[kind] + 2 * (b * a.sb[kind] + i0 * a.st[kind] + h * a.sh[kind]);
-  auto vec = [&](int v) {
-    return *reinterpret_cast<const uint4*>(src + 2 * (v / vpr * a.st[kind] + v % vpr * 8));
-  };
-  uint4 keep[kStoreVecs];
-  float amax = 0.f;
-  const int blk = table[col];
+  const int vpr = c.D / 8, shift = c.D == 128 ? 4 : 3;    // vectors per row: 16 or 8
+#pragma unroll 1
+  for (int group = group0; group < groups; group += a.split) {
+    const int unit = group * kUnits + (int)threadIdx.x / kLanes;  // kind * H + h
+    const bool real = unit < 2 * c.H;
+    const int kind = real && unit >= c.H, h = real ? unit - kind * c.H : 0;
+    const int nvec = real ? rows * vpr : 0;
+    const char* src = a.x[kind] + 2 * (b * a.sb[kind] + i0 * a.st[kind] + h * a.sh[kind]);
+    auto vec = [&](int v) {
+      return *reinterpret_cast<const uint4*>(src + 2 * ((v >> shift) * a.st[kind] + (v & (vpr - 1)) * 8));
+    };
+    uint4 keep[VECS];
+    float amax = 0.f;
 #pragma unroll
-  for (int q = 0; q < kStoreVecs; ++q) {
-    const int v = threadIdx.x + q * kStoreThreads;
-    if (v < nvec) keep[q] = vec(v);
-  }
-  // the old scale comes while the rows do
-  const bool mapped = blk >= 0 && blk < c.num_blocks;
-  float* ps = c.scales + c.scale_at(mapped ? blk : 0, kind, h);
-  const float old = first > 0 ? *ps : 0.f;
+    for (int q = 0; q < VECS; ++q) {
+      const int v = lane + q * kLanes;
+      if (v < nvec) keep[q] = vec(v);
+    }
+    // the old scale comes while the rows do
+    float* ps = c.scales + c.scale_at(mapped ? blk : 0, kind, h);
+    const float old = first > 0 ? *ps : 0.f;
+    // every CTA of the request checks all of its window's blocks, so they agree
+    int bad = 0;
+    if (group == group0)
+      for (int i = (int)(seq / c.tpb) + threadIdx.x; i <= last; i += kStoreThreads)
+        bad |= table[i] < 0 || table[i] >= c.num_blocks;
 #pragma unroll
-  for (int q = 0; q < kStoreVecs; ++q)
-    if (threadIdx.x + q * kStoreThreads < nvec) amax = amax8<T>(keep[q], amax);
-  for (int v = threadIdx.x + kStoreVecs * kStoreThreads; v < nvec; v += kStoreThreads)
-    amax = amax8<T>(vec(v), amax);
+    for (int q = 0; q < VECS; ++q)
+      if (lane + q * kLanes < nvec) amax = amax8<T>(keep[q], amax);
+    for (int v = lane + VECS * kLanes; v < nvec; v += kLanes) amax = amax8<T>(vec(v), amax);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
-  if ((threadIdx.x & 31) == 0) sMax[threadIdx.x >> 5] = amax;
-  __syncthreads();
-  if (sBad) return;
+    for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
+    if (WARPS > 1 && (threadIdx.x & 31) == 0) sMax[threadIdx.x >> 5] = amax;
+    if (__syncthreads_or(bad)) return;  // also: every warp has read the old scale
+    if (!real) continue;
+    if (WARPS > 1) {
 #pragma unroll
-  for (int i = 0; i < kStoreThreads / 32; ++i) amax = fmaxf(amax, sMax[i]);
-  float scale = scale_for(amax);
-  uint8_t* dst = c.pool + c.row(blk, kind, h, 0);
-  if (first > 0) {
-    if (old >= scale) {
-      scale = old;
-    } else {  // the live rows move to the larger scale
-      const float r = scale_ratio(old, scale);
-      for (int v = threadIdx.x; v < first * c.D / 16; v += kStoreThreads) {
-        uint4* p = reinterpret_cast<uint4*>(dst) + v;
-        *p = rescale_e4m3x16(*p, r);
+      for (int i = 0; i < kStoreThreads / 32; ++i) amax = fmaxf(amax, sMax[i]);
+    }
+    float scale = scale_for(amax);
+    uint8_t* dst = c.pool + c.row(blk, kind, h, 0);
+    if (first > 0) {
+      if (old >= scale) {
+        scale = old;
+      } else {  // the live rows move to the larger scale
+        const float r = scale_ratio(old, scale);
+        for (int v = lane; v < first * c.D / 16; v += kLanes) {
+          uint4* p = reinterpret_cast<uint4*>(dst) + v;
+          *p = rescale_e4m3x16(*p, r);
+        }
       }
     }
-  }
-  if (threadIdx.x == 0) *ps = scale;
-  const float inv = scale_ratio(1.f, scale);
-  uint2* out = reinterpret_cast<uint2*>(dst + (size_t)first * c.D);
+    if (lane == 0) *ps = scale;
+    const float inv = scale_ratio(1.f, scale);
+    uint2* out = reinterpret_cast<uint2*>(dst + (size_t)first * c.D);
 #pragma unroll
-  for (int q = 0; q < kStoreVecs; ++q) {
-    const int v = threadIdx.x + q * kStoreThreads;
-    if (v < nvec) out[v] = quant8<T>(keep[q], inv);
+    for (int q = 0; q < VECS; ++q) {
+      const int v = lane + q * kLanes;
+      if (v < nvec) out[v] = quant8<T>(keep[q], inv);
+    }
+    for (int v = lane + VECS * kLanes; v < nvec; v += kLanes) out[v] = quant8<T>(vec(v), inv);
+    if (WARPS > 1) break;  // such CTAs take one unit each
   }
-  for (int v = threadIdx.x + kStoreVecs * kStoreThreads; v < nvec; v += kStoreThreads)
-    out[v] = quant8<T>(vec(v), inv);
 }
 
 struct MoveArgs {
@@ -255,6 +267,34 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const MoveArgs a)
   }
 }
 
+// CTAs above which one takes all of a block's units (a warp per unit): some
+// eight times those that fit the GPU.  64 prompts of 4096 tokens, 8 heads of
+// 128: 282 us instead of 417 with blocks of 16 tokens, 280 instead of 291 with
+// 32; with the CTA per unit (64 tokens) it is the other way, 300 and 293.
+constexpr long kStoreMany = 8l * 152 * 8;
+
+template <class T, int WARPS, int VECS>
+int launch_store_as(StoreArgs& a, cudaStream_t st) {
+  const long blocks = (long)a.B * a.pages;
+  const int groups = ceil_div(2 * a.c.H, kStoreThreads / 32 / WARPS);
+  a.split = WARPS == 1 && blocks * groups > kStoreMany ? 1 : groups;
+  if (blocks * a.split > INT_MAX) return SPEC_EINVAL;
+  store_kernel<T, WARPS, VECS><<<(unsigned)(blocks * a.split), kStoreThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+// A warp per unit while a block's new rows fit its registers, else the CTA.
+// (The CTA for all took 814 us with blocks of 16 tokens and 491 with 32; and
+// 105 us for 2048 requests of 4 tokens, now 23.)
+template <class T>
+int launch_store(StoreArgs& a, cudaStream_t st) {
+  const int vecs = min(a.c.tpb, a.W) * a.c.D / 8;
+  if (vecs <= 32 * 4) return launch_store_as<T, 1, 4>(a, st);
+  if (vecs <= 32 * 8) return launch_store_as<T, 1, 8>(a, st);
+  if (vecs <= 32 * 16) return launch_store_as<T, 1, 16>(a, st);
+  return launch_store_as<T, 4, 8>(a, st);
+}
+
 }  // namespace
 
 }  // namespace sv
@@ -287,13 +327,8 @@ int spec_store_kv(const spec_kv_cache* cache, const void* k, const int64_t* k_st
   a.W = W;
   // blocks a window can touch; at most the whole table row
   a.pages = min((W - 2 + a.c.tpb) / a.c.tpb + 1, a.c.max_blocks);
-  const long grid = (long)B * a.pages * 2 * a.c.H;
-  if (grid > INT_MAX) return SPEC_EINVAL;
-  if (dtype == SPEC_BF16)
-    store_kernel<__nv_bfloat16><<<(unsigned)grid, kStoreThreads, 0, (cudaStream_t)stream>>>(a);
-  else
-    store_kernel<__half><<<(unsigned)grid, kStoreThreads, 0, (cudaStream_t)stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+  return dtype == SPEC_BF16 ? launch_store<__nv_bfloat16>(a, (cudaStream_t)stream)
+                            : launch_store<__half>(a, (cudaStream_t)stream);
 }
 
 int spec_relocate_quantised_kv(const spec_kv_cache* cache, const int32_t* base_lens,
