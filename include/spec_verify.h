@@ -518,7 +518,8 @@ typedef struct spec_kv_cache {
  * ties to even; an element that is not finite is stored as NaN.
  * A request with seq_lens < 0, w_b outside [0, W], a window past max_blocks
  * blocks, or a window block id outside [0, num_blocks) stores nothing.
- * Blocks holding a window must not be shared between requests. */
+ * Blocks holding a window must not be shared between requests, nor stand
+ * twice in a request's row. */
 int spec_store_kv(const spec_kv_cache *cache, const void *k, const int64_t *k_strides,
                   const void *v, const int64_t *v_strides, int dtype, const int32_t *seq_lens,
                   const int32_t *window_lens, int B, int W, spec_stream_t stream);

@@ -19,7 +19,7 @@
 //
 // Measured with 32 heads over 8 KV heads of 128 and windows of 4 tokens: 256
 // requests of 8192 positions 689 us, 6.2 TB/s (0.92 of the measured copy rate);
-// 256 of 512 to 8192, 406 us, 5.6 TB/s (0.83).  One token of one request over
+// 256 of 512 to 8192, 390 us, 5.9 TB/s (0.87).  One token of one request over
 // 1000 positions takes 12.3 us in a graph, both launches: latency (the shares,
 // the table, the rows, the four warps' merge, the join).
 #include "attend.cuh"
@@ -34,10 +34,15 @@ constexpr int kRWarps = 4;
 constexpr int kRThreads = kRWarps * 32;
 constexpr int kKeys = kStep * kRWarps;    // keys of a tile: one step of every warp
 constexpr int kStages = 4;
-constexpr int kUnitCost = 2;              // cells of a unit besides its tiles
+// Cells of a unit besides its tiles: what its start and its result take.  256
+// requests of 512 to 8192 positions, 4 tokens: 413 us with 2, 403 with 4, 390
+// with 6, 384 with 8; 512 of 100 to 900: 187, 169, 162, 162; one token of one
+// request over 4000 positions: 14.8, 14.5, 14.2, 16.3.
+constexpr int kUnitCost = 6;
 // Cells below which a share is not worth a CTA.  One request, one token, 8 KV
 // heads, 100 / 1000 / 30000 positions: 10.5 / 12.3 / 34.7 us with 3 cells, 9.5
-// / 12.5 / 34.4 with 4, 15.7 / 13.4 / 34.4 with 6, 25.4 / 19.5 / 33.1 with 12.
+// / 12.5 / 34.4 with 4, 15.7 / 13.4 / 34.4 with 6, 25.4 / 19.5 / 33.1 with 12
+// (with the join of that time; 9.7 / 12.4 / 24.6 now).
 constexpr int kLeastCells = 4;
 constexpr int kCtas = 3 * kSms;           // resident at 168 registers and 66 KB of shared memory
 using Div = Division<kRows, kKeys>;
