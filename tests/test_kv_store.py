@@ -167,6 +167,24 @@ def test_store_matches_the_oracle(B, W, H, D, tpb, hi, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,W,H,D,tpb", [(3300, 2, 5, 64, 16), (2500, 17, 3, 128, 16)])
+def test_store_of_many_requests(B, W, H, D, tpb):
+    # so many blocks that one CTA takes all heads of a block, the last round of them not full
+    rng = np.random.default_rng(B)
+    seq = rng.integers(0, 20, B)
+    win = rng.integers(0, W + 1, B)
+    pool, scales, tables = cache(rng, seq + W, H, D, tpb, extra_cols=0)
+    x = to_bf16(rng.normal(0, 1, (B, W, 2 * H, D)) * 2.0 ** rng.integers(-9, 10, (B, W, 1, 1)))
+    tables[7, seq[7] // tpb] = -1
+    win[7], win[8], seq[9] = W, W + 1, -1
+    t = dev(x).to(torch.bfloat16)
+    dp, ds = dev(pool), dev(scales)
+    sv.store_kv(t[:, :, :H], t[:, :, H:], dp, ds, dev(tables), dev(seq.astype(np.int32)),
+                window_lens=dev(win.astype(np.int32)))
+    same_cache(dp, ds, *kv.store(x[:, :, :H], x[:, :, H:], pool, scales, tables, seq, win))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [0.0, 2.0 ** -140, 2.0 ** 125])
 def test_store_of_extreme_rows(scale):
     # all zero, below the least scale, at the top of the type's range
