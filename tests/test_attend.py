@@ -443,3 +443,12 @@ def test_long_prefixes(G, W, D, B, seq):
         out, lse = sv.attend_kv(dq.repeat(B, 1, 1, 1), dev(pool), dev(scales), i32(tables), i32([seq] * B), want_lse=True)
     for b in range(B):
         check(out[b:b + 1], lse[b:b + 1], r, "bf16", D, np.ones((1, W), bool), np.abs(np.nan_to_num(kv.decode(pool))).max() * scales.max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (2, 1), (3, 2), (8, 1), (5, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_request_over_every_sm(G, W, D):
+    # one KV head's keys spread over hundreds of CTAs: the join of many parts, by
+    # as many warps per row as the row count leaves
+    run_case(np.random.default_rng(G), [30011], [W], W, 1, G, D, 32, "bf16")
