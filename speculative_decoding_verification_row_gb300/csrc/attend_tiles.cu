@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     bool more = true;
     const int my_tile = lane >> 3;
     // stage 1: block ids under way
-    int blk = -2, grp1 = 0, unit_h = 0, count1 = 0, keys1 = 0, all1 = 0;
-    bool first1 = false;
+    int blk = 0, grp1 = 0, unit_h = 0, count1 = 0, keys1 = 0, all1 = 0;
+    bool first1 = false, keyed1 = false;  // keyed1: the lane's group has keys, blk is a table entry
     // stage 2: scales under way
     const uint8_t* page = nullptr;
     float k_scale = 0.f, v_scale = 0.f;
@@ -632,10 +632,10 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         posted += max(count2, 1);
       }
       // a block that does not exist: block 0 is read, and the scores are NaN
-      const bool ok = (unsigned)blk < (unsigned)c.num_blocks;
+      const bool ok = keyed1 && (unsigned)blk < (unsigned)c.num_blocks;
       const int off = ok ? (int)(grp1 - col16(a, grp1) * (c.tpb / 16)) * 16 : 0;
       page = c.pool + ((((size_t)(ok ? blk : 0) * 2) * c.H + unit_h) * c.tpb + off) * D;
-      k_scale = blk == -2 ? 0.f : NAN;
+      k_scale = keyed1 ? NAN : 0.f;
       v_scale = 0.f;
       if (ok) {
         const float* sp = c.scales + c.scale_at(blk, 0, unit_h);
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       }
       count2 = count1, keys2 = keys1, all2 = all1, first2 = first1;
       count1 = 0;
-      blk = -2;
+      keyed1 = false;
       while (more && tile == tile1) {  // a new segment; those without keys are skipped
         bool left = false;
         if (lane == 0) left = v.next(a);
@@ -664,8 +664,8 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         first1 = tile == tile0;
         unit_h = u.h;
         grp1 = tile * kGroups + lane;
-        if (my_tile < count1 && grp1 * 16 < keys)
-          blk = c.tables[(size_t)u.b * c.max_blocks + col16(a, grp1)];
+        keyed1 = my_tile < count1 && grp1 * 16 < keys;
+        if (keyed1) blk = c.tables[(size_t)u.b * c.max_blocks + col16(a, grp1)];
         tile += count1;
       }
     };

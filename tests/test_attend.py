@@ -452,3 +452,23 @@ def test_one_request_over_every_sm(G, W, D):
     # one KV head's keys spread over hundreds of CTAs: the join of many parts, by
     # as many warps per row as the row count leaves
     run_case(np.random.default_rng(G), [30011], [W], W, 1, G, D, 32, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
+@pytest.mark.parametrize("col", [0, 3, 5])
+def test_block_ids_out_of_range_in_the_prefix(G, W, col):
+    # every id outside [0, num_blocks) reads NaN, whatever its value
+    rng = np.random.default_rng(col)
+    H, D, tpb, seq = 2, 64, 16, 100
+    pool, scales, tables = cache(rng, np.full(7, seq + W), H, D, tpb)
+    ids = np.array([-1, -2, -3, -2 ** 31, len(pool), 2 ** 31 - 1], np.int64)
+    tables[1:, col] = ids
+    q, dq = make_q(rng, (7, W, H * G, D), "bf16")
+    out, lse = sv.attend_kv(dq, dev(pool), dev(scales), i32(tables), i32([seq] * 7), want_lse=True)
+    for b in range(1, 7):
+        assert torch.isnan(out[b]).all() and torch.isnan(lse[b]).all(), ids[b - 1]
+    r = kv.attend(q, pool, scales, tables, [seq] * 7)
+    rows = np.zeros((7, W), bool)
+    rows[0] = True
+    check(out, lse, r, "bf16", D, rows, np.nanmax(np.abs(kv.decode(pool[:, 1]))) * scales[:, 1].max())
