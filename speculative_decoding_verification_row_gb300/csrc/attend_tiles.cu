@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     sDead = 0;
     sNan = 0;
   }
-  // none of this touches what the kernel before may still write
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Tensor memory only now: a kernel before this one that takes some after it has let its
+  // dependents start would wait for these columns while the wait above waits for its end.
   if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sTmem)),
@@ -263,8 +266,6 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid < kDescWords) a.desc[blockIdx.x * kDescWords + tid] = -1;
   if (!divide<kRows, kKeys, kUnitCost, kTThreads>(a, kLeastCells, sWalk[0])) {
     if (warp == kScoreWarp) give_back(sTmem);

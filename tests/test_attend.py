@@ -83,6 +83,18 @@ def test_refusals_before_any_launch():
                      torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
 
 
+def test_tensor_memory_is_taken_behind_the_wait_for_the_kernel_before():
+    # A launch that may start before the kernel in front has ended must not hold
+    # what that kernel may still ask for.  Checked in the source: on a GPU the
+    # other order would hang, and only beside another program's kernel.
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "speculative_decoding_verification_row_gb300", "csrc", "attend_tiles.cu")) as f:
+        kernel = f.read().split("attend_tiles_kernel(", 1)[1]
+    assert kernel.count("tcgen05.alloc") == kernel.count("griddepcontrol.wait") == 1
+    assert kernel.index("griddepcontrol.wait") < kernel.index("tcgen05.alloc")
+
+
 # ------------------------------------------------------------------ GPU parity
 def dev(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
