@@ -537,16 +537,16 @@ int spec_store_kv(const spec_kv_cache *cache, const void *k, const int64_t *k_st
  *   scale * q . k_t; lse = log sum exp of those scores (natural log).  A
  *   token that sees nothing gets out = 0 and lse = -inf.  Positions that a
  *   token does not see have no influence on it, whatever they hold (NaN and
- *   infinities included), but through V's largest scale below.
+ *   scales of any size included).
  *   out     [B, W, q_heads, head_dim] of `dtype`, dense.
  *   out_lse [B, W, q_heads] float32 or NULL.
  * The rows of a request with seq_lens < 0, w_b outside [0, W] (all W rows),
  * a window past max_blocks blocks, or a block id outside [0, num_blocks)
- * among those it reads are NaN.  Scores and sums are held in fp32.  The
- * weights, times their block's V scale over the largest V scale among the
- * blocks read, are rounded to fp16 (11 bits, in steps of at least 2^-32 of
- * the row's largest weight) before they meet V's codes: a block whose V scale
- * is more than 2^20 below the largest loses bits, one 2^32 below counts as 0.
+ * among those it reads are NaN.  Scores and sums are held in fp32; scores
+ * stay below 2^26 in magnitude.  The weights, times the V scales of their
+ * blocks, are rounded to fp16 before they meet V's codes: to 11 bits, in steps
+ * of at least 2^-32 of the largest such product among the positions that the
+ * token sees.
  *   scratch: spec_attend_scratch_size(...) bytes, 256-byte aligned, used
  *   during the call only; it need not be initialised and may hold anything,
  *   but calls that overlap on the GPU must not share it, and it must not be

@@ -214,12 +214,71 @@ __device__ __forceinline__ bool divide(const AttendArgs& a, int least, Walk<ROWS
   return true;
 }
 
-constexpr float kPBits = 8.f;    // weights are 2^(t - m + 8) ...
-constexpr float kLazy = 7.f;     // ... with m at most 7 below the row's largest t: below 2^15 in fp16
+// The sums of a row, over the positions t that it sees (scores in log2 units,
+// V = 2^v times its code):
+//   l = sum 2^(t - m + 8)             m follows the largest t,
+//   o = sum 2^(t + v - m - r + 8) code    m + r follows the largest t + v;
+// out = 2^r o / l.  Each reference moves only when a position exceeds it by
+// more than 7, and stays at or below the largest: the weights of o, which are
+// rounded to fp16, reach 2^8 and stay at or below 2^15.  Both references are
+// the row's own, so a position that it does not see takes none of its bits, and
+// no sum leaves fp32's range whatever V's scales are.  r is an integer: with
+// scales that are powers of two r - v is exact.  v is taken as at least r - 64:
+// with t <= m + 7 such a position adds at most 2^-57 of the largest, and
+// 2^(r - v) in l stays finite.  Before the first position m is the least float:
+// every sum is 0 then, and no difference is NaN.
+constexpr float kPBits = 8.f;
+constexpr float kLazy = 7.f;
+constexpr float kDeep = 64.f;
+constexpr float kNone = -3.402823466e38f;
 
-// Partial result slots: floats of one (ROWS x D weighted V, then max and sum).
+struct RowRef {
+  float m = kNone, r = 0.f;
+  // Moves to the largest t and t + v of some positions; *fl and *fo: what l and o are to be multiplied by.
+  __device__ __forceinline__ void move(float t, float tv, float* fl, float* fo) {
+    const float now = t > m + kLazy ? t : m, at = m + r;
+    // rounding r down lowers m + r by less than 1: one less of slack keeps the weights below 2^15
+    const float rn = floorf((tv > at + (kLazy - 1.f) ? tv : at) - now);
+    *fl = ex2(m - now);
+    *fo = ex2((m - now) + (r - rn));
+    m = now;
+    r = rn;
+  }
+  // r - v, v not below r - 64.
+  __device__ __forceinline__ float depth(float v) const { return fminf(r - v, kDeep); }
+};
+
+// Two weights as fp16.  With scores beyond 2^24, whose rounding exceeds the
+// references' slack, a weight may pass fp16's largest: it is cut off there.
+__device__ __forceinline__ uint32_t weights_f16(float x, float y) {
+  uint32_t w;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
+  return w;
+}
+
+// s = f * 2^e with f in (1/2, 1]; f is smaller below 2^-126, and 0 for s = 0.
+__device__ __forceinline__ float scale_exponent(float s, float* f) {
+  const uint32_t bits = __float_as_uint(s), frac = bits & 0x7fffffu;
+  const int field = (int)(bits >> 23);
+  if (field == 0) {
+    *f = s * 0x1p126f;
+    return -126.f;
+  }
+  *f = frac ? __uint_as_float(126u << 23 | frac) : 1.f;
+  return (float)(field - 127 + (frac != 0));
+}
+
+// 2^r / l as two factors that are in range one by one (|r| < 200); both 0 for l = 0.
+__device__ __forceinline__ float2 result_factors(float l, float r) {
+  const float lo = floorf(0.5f * r);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  return make_float2(inv * __uint_as_float((uint32_t)((int)lo + 127) << 23),
+                     __uint_as_float((uint32_t)((int)(r - lo) + 127) << 23));
+}
+
+// Partial result slots: floats of one (ROWS x D of o, then m, r and l).
 template <int ROWS>
-__host__ __device__ constexpr size_t part_floats(int D) { return (size_t)ROWS * (D + 2); }
+__host__ __device__ constexpr size_t part_floats(int D) { return (size_t)ROWS * (D + 3); }
 
 // desc words per CTA: {request, head, row tile, last CTA of the unit, its rows}; -1: none.
 constexpr int kDescWords = 8;
@@ -245,23 +304,39 @@ __device__ __forceinline__ float row_lse(float M, float L) {
 // end, in an order that depends on the division alone, so the result does not
 // depend on timing.
 constexpr int kJoinRows = 16;
-constexpr int kJoinBatch = 6;
+constexpr int kJoinBatch = 3;  // 6 spill: one token over 30000 positions 27.5 us instead of 26.4
 constexpr int kJoinThreads = kJoinRows * 32;
 
-// A row's partial result: its maximum, sum and the E elements of a lane.
+// A row's partial result: its references, l and the E elements of o of a lane.
 template <int E>
 struct Part {
-  float m, l, x[E];
-  __device__ __forceinline__ void add(float pm, float pl, const float* px) {
-    if (pm == -INFINITY && pl == 0.f) return;
-    const float now = fmaxf(m, pm);
-    const float fo = m == now ? 1.f : ex2(m - now), fn = pm == now ? 1.f : ex2(pm - now);
-    m = now;
-    l = l * fo + pl * fn;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = x[e] * fo + px[e] * fn;
-  }
+  float m, r, l, x[E];
 };
+
+// Adds N parts to one: their references first, so that no part waits for another's factors.
+template <int E, int N>
+__device__ __forceinline__ void add_parts(Part<E>& s, const Part<E> (&p)[N]) {
+  float now = s.m;
+#pragma unroll
+  for (int k = 0; k < N; ++k) now = fmaxf(now, p[k].m);
+  float rn = s.m - now + s.r;
+#pragma unroll
+  for (int k = 0; k < N; ++k) rn = fmaxf(rn, p[k].m - now + p[k].r);
+  rn = floorf(rn);
+  const float fl = ex2(s.m - now), fo = ex2((s.m - now) + (s.r - rn));
+  s.m = now;
+  s.r = rn;
+  s.l *= fl;
+#pragma unroll
+  for (int e = 0; e < E; ++e) s.x[e] *= fo;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float d = p[k].m - now, f = ex2(d + (p[k].r - rn));
+    s.l = fmaf(p[k].l, ex2(d), s.l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s.x[e] = fmaf(p[k].x[e], f, s.x[e]);
+  }
+}
 
 template <class T, int D, int ROWS, int KEYS>
 __global__ void __launch_bounds__(kJoinThreads, 2) attend_join_kernel(const AttendArgs a) {
@@ -279,42 +354,49 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attend_join_kernel(const Atte
   const int sets = mine > 8 ? 1 : mine > 4 ? 2 : mine > 2 ? 4 : 8;
   const int set = warp % sets, r = blockIdx.y * kJoinRows + warp / sets;
   const bool real = warp / sets < mine;
-  Part<E> sum{-INFINITY, 0.f, {}};
+  Part<E> sum{kNone, 0.f, 0.f, {}};
   if (real) {
     for (int i = first + set; i <= last; i += sets * kJoinBatch) {
-      float pm[kJoinBatch], pl[kJoinBatch], px[kJoinBatch][E];
+      Part<E> part[kJoinBatch];
 #pragma unroll
       for (int k = 0; k < kJoinBatch; ++k) {
         const int at = i + k * sets;
         const float* p = a.part + (2 * (size_t)at + (at == first)) * part_floats<ROWS>(D);
-        pm[k] = at <= last ? p[ROWS * D + r] : -INFINITY;
-        pl[k] = at <= last ? p[ROWS * D + ROWS + r] : 0.f;
-        if (E == 4) {
-          const float4 z = at <= last ? reinterpret_cast<const float4*>(p + r * D)[lane] : make_float4(0, 0, 0, 0);
-          px[k][0] = z.x, px[k][1] = z.y, px[k][E - 2] = z.z, px[k][E - 1] = z.w;
-        } else {
-          const float2 z = at <= last ? reinterpret_cast<const float2*>(p + r * D)[lane] : make_float2(0, 0);
-          px[k][0] = z.x, px[k][1] = z.y;
+        part[k] = Part<E>{kNone, 0.f, 0.f, {}};
+        if (at <= last) {
+          part[k].m = p[ROWS * D + r];
+          part[k].r = p[ROWS * (D + 1) + r];
+          part[k].l = p[ROWS * (D + 2) + r];
+          if (E == 4) {
+            const float4 z = reinterpret_cast<const float4*>(p + r * D)[lane];
+            part[k].x[0] = z.x, part[k].x[1] = z.y, part[k].x[E - 2] = z.z, part[k].x[E - 1] = z.w;
+          } else {
+            const float2 z = reinterpret_cast<const float2*>(p + r * D)[lane];
+            part[k].x[0] = z.x, part[k].x[1] = z.y;
+          }
         }
       }
-#pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) sum.add(pm[k], pl[k], px[k]);
+      add_parts(sum, part);
     }
   }
   if (sets > 1) {
     if (set) sPart[warp][lane] = sum;
     __syncthreads();
     if (!set)
-      for (int k = 1; k < sets; ++k) sum.add(sPart[warp + k][lane].m, sPart[warp + k][lane].l, sPart[warp + k][lane].x);
+      for (int k = 1; k < sets; ++k) {
+        const Part<E> part[1] = {sPart[warp + k][lane]};
+        add_parts(sum, part);
+      }
   }
   if (set || !real) return;
   const long row = (long)d.z * ROWS + r;
   const int i = (int)(row / a.G), head = d.y * a.G + (int)(row % a.G);
   const size_t orow = ((size_t)d.x * a.W + i) * a.Hq + head;
-  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+  const float2 f = result_factors(sum.l, sum.r);
   uint32_t y[E / 2];
 #pragma unroll
-  for (int e = 0; e < E; e += 2) y[e / 2] = pack_out(sum.x[e] * inv, sum.x[e + 1] * inv, (T*)nullptr);
+  for (int e = 0; e < E; e += 2)
+    y[e / 2] = pack_out(sum.x[e] * f.x * f.y, sum.x[e + 1] * f.x * f.y, (T*)nullptr);
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + 2 * (orow * D + lane * E));
   if (E == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[E / 2 - 1]);

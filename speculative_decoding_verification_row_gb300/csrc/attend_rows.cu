@@ -11,11 +11,11 @@
 // e4m3 -> fp16 is exact.  Q is scaled by a power of two per row to a largest
 // magnitude in [2^14, 2^15) and rounded to fp16: exact for bf16 and fp16
 // elements down to 2^-28 of the row's largest.  The scale of a key's block
-// multiplies the score.  The weights p = 2^(t - m + 8) are rounded to fp16
-// (11 bits; below 2^-22 of the row's largest in steps of 2^-32) and
-// multiplied by the ratio of their block's V scale to the largest V scale so
-// far, which the sums are held in.  m follows the maximum only when a score
-// exceeds it by more than 7, so that the sums are rarely rescaled.
+// multiplies the score.  The weights are those of RowRef: a power of two of the
+// score and of the exponent of their block's V scale, rounded to fp16 (11 bits;
+// below 2^-22 of the row's largest in steps of 2^-32).  The references move
+// only when a key exceeds them by more than 7, so that the sums are rarely
+// rescaled.
 //
 // Measured with 32 heads over 8 KV heads of 128 and windows of 4 tokens: 256
 // requests of 8192 positions 689 us, 6.2 TB/s (0.92 of the measured copy rate);
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
   constexpr int NT = D / 8;   // mma tiles along D
   constexpr int VW = D / 32;  // 32-bit words of V per thread and key
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float sM[kRWarps][kRows], sL[kRWarps][kRows], sV[kRWarps];
+  __shared__ float sM[kRWarps][kRows], sR[kRWarps][kRows], sL[kRWarps][kRows];
   __shared__ int sBad;
   const KvCache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
     if (tid == 0) sBad = u.w < 0;
     __syncthreads();
     float o[NT][4];
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0.f;
+    RowRef ref[2];
+    float l[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     if (u.w >= 0) {
@@ -300,49 +301,48 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           top[k] = fmaxf(fmaxf(s[0][2 * k], s[0][2 * k + 1]), fmaxf(s[1][2 * k], s[1][2 * k + 1]));
-        const bool up = top[0] > m[0] + kLazy || top[1] > m[1] + kLazy;
+        float vf;  // V's scale is vf * 2^ve
+        const float ve = scale_exponent(scales.y, &vf);
+        float depth[2] = {ref[0].r - ve, ref[1].r - ve};
+        const bool up = top[0] > ref[0].m + kLazy + fminf(depth[0], 0.f) ||
+                        top[1] > ref[1].m + kLazy + fminf(depth[1], 0.f);
         if (__any_sync(~0u, up)) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             top[k] = fmaxf(top[k], __shfl_xor_sync(~0u, top[k], 1));
             top[k] = fmaxf(top[k], __shfl_xor_sync(~0u, top[k], 2));
-            const float now = top[k] > m[k] + kLazy ? top[k] : m[k];
-            const float al = now == m[k] ? 1.f : ex2(m[k] - now);
-            m[k] = now;
-            l[k] *= al;
+            float fl, fo;
+            ref[k].move(top[k], top[k] + ve, &fl, &fo);
+            depth[k] = ref[k].r - ve;
+            l[k] *= fl;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) o[j][2 * k] *= al, o[j][2 * k + 1] *= al;
+            for (int j = 0; j < NT; ++j) o[j][2 * k] *= fo, o[j][2 * k + 1] *= fo;
           }
         }
         // ---- weights
         float p[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float sub = m[k] == -INFINITY ? 0.f : m[k] - kPBits;
+          depth[k] = fminf(depth[k], kDeep);
+          const float sub = ref[k].m - kPBits + depth[k];
+          float sum = 0.f;
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               p[n][2 * k + e] = ex2(s[n][2 * k + e] - sub);
-              l[k] += p[n][2 * k + e];
+              sum += p[n][2 * k + e];
             }
+          l[k] = fmaf(sum, ex2(depth[k]), l[k]);
         }
-        if (scales.y != vref) {
-          if (scales.y > vref) {  // the sums move to the larger scale
-            const float r = vref / scales.y;
-            vref = scales.y;
+        if (vf != 1.f) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) o[j][0] *= r, o[j][1] *= r, o[j][2] *= r, o[j][3] *= r;
-          } else {
-            const float r = scales.y / vref;
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) p[n][e] *= r;
-          }
+            for (int e = 0; e < 4; ++e) p[n][e] *= vf;
         }
-        const uint32_t pa[4] = {half2_of(p[0][0], p[0][1]), half2_of(p[0][2], p[0][3]),
-                                half2_of(p[1][0], p[1][1]), half2_of(p[1][2], p[1][3])};
+        const uint32_t pa[4] = {weights_f16(p[0][0], p[0][1]), weights_f16(p[0][2], p[0][3]),
+                                weights_f16(p[1][0], p[1][1]), weights_f16(p[1][2], p[1][3])};
         // ---- weighted V: keys 2 cc, 2 cc + 1 (tile 0) and 8 + 2 cc, 8 + 2 cc + 1 (tile 1);
         // mma tile j holds d = (D / 8) g + j
         const unsigned char* vp = sp + R::kHalf;
@@ -431,20 +431,22 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
         *reinterpret_cast<float4*>(row + NT + j) = make_float4(
             o[j][2 * k + 1], o[j + 1][2 * k + 1], o[j + 2][2 * k + 1], o[j + 3][2 * k + 1]);
       }
-      if (cc == 0) sM[warp][g + 8 * k] = m[k], sL[warp][g + 8 * k] = l[k];
+      if (cc == 0) sM[warp][g + 8 * k] = ref[k].m, sR[warp][g + 8 * k] = ref[k].r, sL[warp][g + 8 * k] = l[k];
     }
-    if (lane == 0) sV[warp] = vref;
     __syncthreads();
     {
       const int r = tid >> 3, part = tid & 7;  // 8 threads per row, D / 8 elements each
-      float M = -INFINITY, L = 0.f, f[kRWarps];
+      float M = kNone, R = kNone, L = 0.f, f[kRWarps];
 #pragma unroll
       for (int k = 0; k < kRWarps; ++k) M = fmaxf(M, sM[k][r]);
 #pragma unroll
+      for (int k = 0; k < kRWarps; ++k) R = fmaxf(R, sM[k][r] - M + sR[k][r]);
+      R = floorf(R);
+#pragma unroll
       for (int k = 0; k < kRWarps; ++k) {
-        f[k] = sM[k][r] == -INFINITY && sL[k][r] == 0.f ? 0.f : ex2(sM[k][r] - M);
-        L += sL[k][r] * f[k];
-        f[k] *= sV[k];
+        const float d = sM[k][r] - M;
+        f[k] = ex2(d + (sR[k][r] - R));
+        L = fmaf(sL[k][r], ex2(d), L);
       }
       if (sBad) L = NAN;
       float x[NT];
@@ -464,10 +466,11 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
         if (whole) {
           const int i = (r0 + r) / a.G, head = u.h * a.G + (r0 + r) % a.G;
           const size_t orow = ((size_t)u.b * a.W + i) * a.Hq + head;
-          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const float2 out = result_factors(L, R);
           uint32_t y[NT / 2];
 #pragma unroll
-          for (int j = 0; j < NT; j += 2) y[j / 2] = pack_out(x[j] * inv, x[j + 1] * inv, (T*)nullptr);
+          for (int j = 0; j < NT; j += 2)
+            y[j / 2] = pack_out(x[j] * out.x * out.y, x[j + 1] * out.x * out.y, (T*)nullptr);
           uint4* dst = reinterpret_cast<uint4*>(a.out + 2 * (orow * D + part * NT));
 #pragma unroll
           for (int j = 0; j < NT / 8; ++j)
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(kRThreads, 3) attend_rows_kernel(const AttendA
           for (int j = 0; j < NT; j += 4)
             *reinterpret_cast<float4*>(dst + r * D + part * NT + j) =
                 make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-          if (part == 0) dst[kRows * D + r] = M, dst[kRows * D + kRows + r] = L;
+          if (part == 0) dst[kRows * D + r] = M, dst[kRows * (D + 1) + r] = R, dst[kRows * (D + 2) + r] = L;
         }
       }
       if (!whole && tile0 == 0 && tid == 0) {

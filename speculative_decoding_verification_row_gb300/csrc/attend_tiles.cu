@@ -5,8 +5,8 @@
 // accumulators in tensor memory).  Warps by role:
 //   0-7    softmax: two threads per row, one for each half of the tile's
 //          keys (and of D).  Reads S from tensor memory, writes the weights P
-//          back there as fp16, rescales O when the maximum moves by more than
-//          2^7, and writes the result.  Loads Q at a unit's start.
+//          back there as fp16, rescales O when a reference moves, and writes
+//          the result.  Loads Q at a unit's start.
 //   8      one thread issues S = Q K^T, Q in tensor memory, K in shared memory.
 //   9      one thread issues O += P V, P in tensor memory, V in shared memory.
 //          (Issuing takes as long as the product: with one warp for both, its
@@ -19,7 +19,8 @@
 // with Q in shared memory it would be 160 KB and shared memory the bound.
 // Tensor memory: Q, S (two buffers; the weights replace the scores there), O.
 //
-// Scales, weights and lazy rescaling are as in attend_rows.cu.
+// Scales, weights and lazy rescaling are as in attend_rows.cu, but that a V
+// scale goes into the exponent whole, as its log2.
 //
 // Measured with 32 heads over 8 KV heads of 128: 16 trees of 60 tokens over
 // 8192 positions 174 us, 740 TFLOP/s (0.39 of the measured dense rate; 16 of
@@ -216,13 +217,13 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
   constexpr int ST = TL::kStages;
   extern __shared__ unsigned char smem_raw[];
   __shared__ Bars bars;
-  // of each 16-key group: K's scale; V's scale over the largest so far in the segment, as log2
-  // and as 1 / x; that largest scale, and the last one over it
-  __shared__ __align__(16) float sK[kRing][kGroups], sLog[kRing][kGroups], sInv[kRing][kGroups];
-  __shared__ float sRef[kRing], sGrow[kRing];
+  // of each 16-key group: K's scale, and log2 of V's
+  __shared__ __align__(16) float sK[kRing][kGroups], sLog[kRing][kGroups];
   __shared__ const uint8_t* sPage[kRing][kGroups];  // K rows of each 16-key group
   __shared__ int sKeys[kRing], sPrefix[kRing], sFirst[kRing];  // see the lookup
-  __shared__ float sTop[2][2][kRows], sAux[2][2][kRows];  // what the two threads of a row tell each other
+  // what the two threads of a row tell each other
+  __shared__ float2 sTop[2][2][kRows];
+  __shared__ float sAux[2][2][kRows];
   // the walk of the softmax warps and that of the lookup; the segment that thread 0 found
   using Walker = Walk<kRows, kKeys, kUnitCost>;
   __shared__ Walker sWalk[2];
@@ -346,7 +347,8 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     Unit u = {};
     int tile0 = 0, tile1 = 0, last = 0;
     bool whole = false, any = false;
-    float m = 0.f, l = 0.f, vref = 0.f;
+    RowRef ref;
+    float l = 0.f;
     auto finish = [&](int my_rows, int my_i, int my_head) {
       bool bad = u.w < 0;
       if (u.w >= 0) {
@@ -362,13 +364,12 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
         l += sAux[1][half ^ 1][r];
         bar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, dead);
         fence_after();
-        vref = sRef[(n - 1) % kRing];
       }
       if (bad || *dead) l = NAN;
       // ---- the result, or this CTA's part of it
       const size_t orow = ((size_t)u.b * a.W + my_i) * a.Hq + (size_t)u.h * a.G + my_head;
       float* part = a.part + (2 * (size_t)blockIdx.x + (tile0 == 0)) * part_floats<kRows>(D);
-      const float f = whole ? (l == 0.f ? 0.f : vref / l) : vref;
+      const float2 f = result_factors(l, ref.r);
       // the window tokens among this segment's keys, for NaN in V
       const long j0 = max(0l, (long)tile0 * kKeys - u.seq);
       const long j1 = sNan ? min((long)u.w, (long)tile1 * kKeys - u.seq) : 0;
@@ -405,16 +406,15 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               uint32_t y[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                y[e] = pack_out(o[k * 8 + e * 2] * f,
-                                o[k * 8 + e * 2 + 1] * f, (T*)nullptr);
+                y[e] = pack_out(o[k * 8 + e * 2] * f.x * f.y, o[k * 8 + e * 2 + 1] * f.x * f.y, (T*)nullptr);
               dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else {
 #pragma unroll
             for (int k = 0; k < 32; k += 8)  // whole sectors: every lane has a row of its own
               asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(part + (size_t)r * D + x + k),
-                           "f"(o[k] * f), "f"(o[k + 1] * f), "f"(o[k + 2] * f), "f"(o[k + 3] * f), "f"(o[k + 4] * f),
-                           "f"(o[k + 5] * f), "f"(o[k + 6] * f), "f"(o[k + 7] * f)
+                           "f"(o[k]), "f"(o[k + 1]), "f"(o[k + 2]), "f"(o[k + 3]), "f"(o[k + 4]), "f"(o[k + 5]),
+                           "f"(o[k + 6]), "f"(o[k + 7])
                            : "memory");
           }
         }
@@ -422,10 +422,11 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       }
       if (r < my_rows && half == 0) {
         if (whole) {
-          if (a.lse) a.lse[orow] = row_lse(m, l);
+          if (a.lse) a.lse[orow] = row_lse(ref.m, l);
         } else {
-          part[(size_t)kRows * D + r] = m;
-          part[(size_t)kRows * D + kRows + r] = l;
+          part[(size_t)kRows * D + r] = ref.m;
+          part[(size_t)kRows * (D + 1) + r] = ref.r;
+          part[(size_t)kRows * (D + 2) + r] = l;
         }
       }
       if (!whole && tile0 == 0 && tid == 0) {
@@ -464,17 +465,15 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
       any = true;
       soft_sync();  // sSeg has been read
       if (tid == 0) find_next();
-      m = -INFINITY, l = 0.f, vref = 0.f;
+      ref = RowRef{}, l = 0.f;
       if (u.w < 0) continue;
       for (int tile = tile0; tile < tile1; ++tile, ++n) {
         const int ring = n % kRing;
         bar_wait(&bars.pages[ring], (n / kRing) & 1, dead);
         const float4 k4 = reinterpret_cast<const float4*>(sK[ring])[half];
         const float4 log4 = reinterpret_cast<const float4*>(sLog[ring])[half];
-        const float4 inv4 = reinterpret_cast<const float4*>(sInv[ring])[half];
-        const float grow = sGrow[ring];
         float kf[4] = {k4.x * qs, k4.y * qs, k4.z * qs, k4.w * qs};
-        const float lv[4] = {log4.x, log4.y, log4.z, log4.w}, iv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
+        const float lv[4] = {log4.x, log4.y, log4.z, log4.w};
 #pragma unroll
         for (int y = 0; y < 4; ++y)  // -inf times it stays -inf; NaN (no such block) stays NaN
           kf[y] = kf[y] < 0x1p-120f ? 0x1p-120f : kf[y];
@@ -494,7 +493,7 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               if (!(bits >> k & 1)) s[x + k] = -INFINITY;
           }
         }
-        float top = -INFINITY;
+        float2 top = make_float2(-INFINITY, -INFINITY);  // largest score, and with V's scale
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           float t0 = -INFINITY, t1 = -INFINITY;
@@ -503,19 +502,18 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
             t0 = max3(t0, s[y * 16 + k], s[y * 16 + k + 1]);
             t1 = max3(t1, s[y * 16 + k + 2], s[y * 16 + k + 3]);
           }
-          top = fmaxf(top, fmaxf(t0, t1) * kf[y]);
+          const float t = fmaxf(t0, t1) * kf[y];
+          top = make_float2(fmaxf(top.x, t), fmaxf(top.y, t + lv[y]));
         }
         sTop[n & 1][half][r] = top;
         pair_sync(warp);
-        top = fmaxf(top, sTop[n & 1][half ^ 1][r]);
-        const bool move = top > m + kLazy;
-        if (__any_sync(~0u, move || grow != 1.f)) {
-          const float now = move ? top : m;
-          const float al = move ? ex2(m - now) : 1.f;
-          m = now;
-          l *= al;
-          if (tile > tile0) {
-            const float ar = al * grow;
+        const float2 other = sTop[n & 1][half ^ 1][r];
+        top = make_float2(fmaxf(top.x, other.x), fmaxf(top.y, other.y));
+        if (__any_sync(~0u, top.x > ref.m + kLazy || top.y > ref.m + ref.r + kLazy)) {
+          float fl, fo;
+          ref.move(top.x, top.y, &fl, &fo);
+          l *= fl;
+          if (tile > tile0 && __any_sync(~0u, fo != 1.f)) {
             bar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, dead);
             fence_after();
 #pragma unroll 1
@@ -524,19 +522,19 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               tmem_ld16(o, lanes + kColO + x);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ar);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fo);
               tmem_st16(lanes + kColO + x, o);
             }
           }
         }
         // V's scale goes into the exponent, and out of the sum again
-        const float add = m == -INFINITY ? 0.f : kPBits - m;
+        const float add = kPBits - ref.m;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           uint32_t p[16];
 #pragma unroll
           for (int y = 2 * z; y < 2 * z + 2; ++y) {
-            const float av = add + lv[y];
+            const float depth = ref.depth(lv[y]), av = add - depth;
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
@@ -544,9 +542,9 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
               float2 e = fma2(make_float2(s[x], s[x + 1]), make_float2(kf[y], kf[y]), make_float2(av, av));
               e = make_float2(ex2(e.x), ex2(e.y));
               sum = add2(sum, e);
-              p[(x & 31) / 2] = half2_of(e.x, e.y);
+              p[(x & 31) / 2] = weights_f16(e.x, e.y);
             }
-            l = fmaf(sum.x + sum.y, iv[y], l);
+            l = fmaf(sum.x + sum.y, ex2(depth), l);
           }
           // over this thread's scores, all of which it has read
           tmem_st16(lanes + kColS + (n & 1) * kKeys + half * 64 + z * 16, p);
@@ -602,23 +600,16 @@ __global__ void __launch_bounds__(kTThreads, 1) attend_tiles_kernel(const Attend
     int count2 = 0, keys2 = 0, all2 = 0;
     bool first2 = false;
     uint32_t posted = 0;
-    float ref = 0.f;
     bool ended = false;
     auto lookup = [&](bool post) {
       if (post && !ended) {
-        // V's scales against the segment's largest so far; below 2^-40 of it they
-        // are taken as that (such a block adds at most 2^-40 of the largest |V|)
-        const float last = first2 ? 0.f : ref;
-        ref = fmaxf(last, __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(v_scale))));
-        const float over = ref > 0.f ? __fdividef(1.f, ref) : 0.f;
-        const float vr = ref > 0.f ? fmaxf(v_scale * over, 0x1p-40f) : 1.f;
+        float vf;
+        const float ve = scale_exponent(v_scale, &vf);
         const int at = (posted + my_tile) % kRing, g = lane & 7;
         if (my_tile < count2) {
           sPage[at][g] = page;
           sK[at][g] = k_scale;
-          sLog[at][g] = __log2f(vr);
-          sInv[at][g] = __fdividef(1.f, vr);
-          if (g == 0) sRef[at] = ref, sGrow[at] = my_tile == 0 && ref > last ? last * over : 1.f;
+          sLog[at][g] = vf == 1.f ? ve : vf > 0.f ? ve + __log2f(vf) : -150.f;  // 448 * 2^-150 is 0 in any output
         }
         // keys of the tile, those that every row sees, and whether a segment begins;
         // no keys: the share has ended

@@ -484,3 +484,137 @@ def test_block_ids_out_of_range_in_the_prefix(G, W, col):
     rows = np.zeros((7, W), bool)
     rows[0] = True
     check(out, lse, r, "bf16", D, rows, np.nanmax(np.abs(kv.decode(pool[:, 1]))) * scales[:, 1].max())
+
+
+def near(out, r, D, rows, vmax, least):
+    """check's bound for bf16 outputs far from 1: vmax [..] is the largest
+    p_t |v_t| over the largest p_t of the positions that a row sees, `least`
+    half the least step of the values."""
+    got, want = out.double().cpu().numpy()[rows], r["out"][rows]
+    n, spread, amp = r["keys"][rows][..., None], r["spread"][rows][..., None], r["amp"][rows]
+    tol = ((2 * (D + 8) * U * spread + 2.0 ** -11 + 2.0 ** -20 + 2 * n * U) * amp + n * 2.0 ** -32 * vmax
+           + 2.0 ** -8 * np.abs(want) + least)
+    assert np.isfinite(got).all()
+    worst = (np.abs(got - want) / tol).max()
+    assert worst <= 1, f"worst {worst:.3g} of the bound"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,G,W,D", [(1, 1, 1, 128), (900, 1, 2, 64), (1, 4, 40, 128), (200, 4, 40, 64)])
+def test_values_at_the_top_of_the_types_range(B, G, W, D):
+    # Thousands of alike keys: a sum of V that is not yet divided by the weights'
+    # would pass the largest float.  One request is cut into many parts; of many
+    # requests most lie in one CTA whole.
+    rng = np.random.default_rng(B + W)
+    H, tpb, seq = 1, 64, 3000
+    pool, scales, tables = cache(rng, np.array([seq + W]), H, D, tpb, extra_cols=0)
+    pool[:, 0] = kv.encode(rng.normal(0, 0.01, pool[:, 0].shape))
+    pool[:, 1] = kv.encode(rng.uniform(200, 448, pool[:, 1].shape))
+    scales[:, 0], scales[:, 1] = 1, 2.0 ** 119
+    q, dq = make_q(rng, (1, W, H * G, D), "bf16")
+    r = kv.attend(q, pool, scales, tables, [seq])
+    out, lse = sv.attend_kv(dq.repeat(B, 1, 1, 1), dev(pool), dev(scales), i32(np.repeat(tables, B, 0)), i32([seq] * B),
+                            want_lse=True)
+    for b in range(0, B, 1 if B < 10 else 53):
+        near(out[b:b + 1], r, D, np.ones((1, W), bool), 448 * 2.0 ** 119, 0)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 4), (4, 4), (4, 40), (3, 130)])
+@pytest.mark.parametrize("ratio", [16, 20, 30, 60, 110])
+@pytest.mark.parametrize("prefix", [1, 25])
+def test_unseen_values_take_no_bits(G, W, ratio, prefix):
+    # the window's last token begins a block whose V scale is 2^ratio times the
+    # others'; the tokens before it do not see it and are exact to their own values
+    rng = np.random.default_rng(W + ratio)
+    H, D, tpb = 2, 64, 16
+    seq = 16 * (prefix + (W + 14) // 16) - (W - 1)
+    pool, scales, tables = cache(rng, np.array([seq + W]), H, D, tpb)
+    last = tables[0, (seq + W - 1) // tpb]
+    seen = np.setdiff1d(tables[0, :(seq + W - 1) // tpb], last)
+    vmax = np.nanmax(np.abs(kv.decode(pool[seen, 1]) * scales[seen, 1][..., None, None]))
+    scales[last, 1] = 2.0 ** ratio * scales[seen, 1].max()
+    q, dq = make_q(rng, (1, W, H * G, D), "bf16")
+    r = kv.attend(q, pool, scales, tables, [seq])
+    out, lse = sv.attend_kv(dq, dev(pool), dev(scales), i32(tables), i32([seq]), want_lse=True)
+    rows = np.ones((1, W), bool)
+    rows[0, -1] = False
+    check(out, lse, r, "bf16", D, rows, vmax)
+    near(out, r, D, ~rows, 448 * scales[last, 1].max(), 2.0 ** -25)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
+@pytest.mark.parametrize("where", [0, 5, 11])
+def test_a_light_key_of_large_values(G, W, where):
+    # one key weighs 2^-60 of the others and its V is 2^40 times theirs: what it
+    # adds (2^-20) leaves the others' bits alone, wherever it stands
+    rng = np.random.default_rng(where)
+    H, D, tpb, seq = 1, 64, 16, 192
+    pool, scales, tables = cache(rng, np.array([seq + W]), H, D, tpb)
+    pool[:, 0] = kv.encode(0.0)
+    pool[:, 1] = kv.encode(rng.uniform(0.5, 1.5, pool[:, 1].shape))
+    blk = tables[0, where]
+    pool[blk, 0] = kv.encode(-1.0)
+    scales[:] = 1
+    scales[blk, 1] = 2.0 ** 40
+    q, dq = make_q(rng, (1, W, H * G, D), "bf16", 0)
+    q[:], _ = 1.0, dq.fill_(1.0)
+    scale = 60 * np.log(2) / D  # the block's scores are 60 below the others' in log2 units
+    r = kv.attend(q, pool, scales, tables, [seq], scale=float(np.float32(scale)))
+    out, lse = sv.attend_kv(dq, dev(pool), dev(scales), i32(tables), i32([seq]), scale=scale, want_lse=True)
+    check(out, lse, r, "bf16", D, np.ones((1, W), bool), 1.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
+@pytest.mark.parametrize("exps", [(127,), (-130,), (-138,), (-126, -100), (100, -100, 0), (127, -149)])
+def test_value_scales_over_all_of_fp32(G, W, exps):
+    rng = np.random.default_rng(len(exps))
+    H, D, tpb, seq = 2, 64, 16, 300
+    pool, scales, tables = cache(rng, np.array([seq + W]), H, D, tpb)
+    if max(exps) > 119:  # V of at most 1 times the largest scale
+        pool[:, 1] = kv.encode(rng.uniform(-1, 1, pool[:, 1].shape))
+    else:
+        pool[:, 1] = kv.encode(rng.uniform(-448, 448, pool[:, 1].shape))
+    scales[:, 1] = np.ldexp(np.float32(1), rng.choice(exps, scales[:, 1].shape)).astype(np.float32)
+    if len(exps) == 1:
+        scales[:, 1] *= np.float32(1.375)  # not a power of two
+    q, dq = make_q(rng, (1, W, H * G, D), "bf16")
+    r = kv.attend(q, pool, scales, tables, [seq])
+    out, lse = sv.attend_kv(dq, dev(pool), dev(scales), i32(tables), i32([seq]), want_lse=True)
+    x = np.abs(kv.decode(pool[:, 1]) * scales[:, 1].astype(np.float64)[..., None, None])
+    near(out, r, D, np.ones((1, W), bool), np.nanmax(x), 2.0 ** -133)
+    assert np.allclose(lse.cpu().numpy(), r["lse"], rtol=0, atol=1e-3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
+def test_a_value_scale_of_zero(G, W):
+    # codes times 0 are 0, in a block whose weights count all the same
+    rng = np.random.default_rng(5)
+
+    def edit(pool, scales, tables):
+        scales[tables[0, 1:4], 1] = 0
+        scales[tables[1], 1] = 0  # nothing but zeros
+        pool[:, 1][(pool[:, 1] & 127) == 127] = 0
+    out, lse = run_case(rng, [200, 70], [W, W], W, 2, G, 64, 16, "bf16", edit=edit)
+    assert (out[1] == 0).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
+@pytest.mark.parametrize("exp", [4, 8, 12])
+def test_scores_of_millions(G, W, exp):
+    # scores up to 2^26, where fp32 hardly tells one from the next: a weighted mean of V all the same
+    rng = np.random.default_rng(exp)
+    H, D, tpb, seq = 2, 64, 16, 400
+    pool, scales, tables = cache(rng, np.array([seq + W]), H, D, tpb)
+    pool[:, 1] = kv.encode(rng.uniform(-1, 1, pool[:, 1].shape))
+    scales[:, 1], scales[:, 0] = 1, 2.0 ** exp
+    q, dq = make_q(rng, (1, W, H * G, D), "f16", 20.0)
+    out, lse = sv.attend_kv(dq, dev(pool), dev(scales), i32(tables), i32([seq]), want_lse=True)
+    r = kv.attend(q, pool, scales, tables, [seq])
+    assert out.abs().max() <= 1
+    assert (np.abs(lse.double().cpu().numpy() - r["lse"]) <= (D + 8) * U * r["spread"] + 100).all()
