@@ -562,7 +562,7 @@ typedef struct spec_attend_params {
     const int32_t *seq_lens;
     const int32_t *window_lens;  /* [B] or NULL */
     const int32_t *masks;        /* or NULL */
-    float scale;                 /* finite */
+    float scale;                 /* finite, times log2(e) too */
     void *out;
     float *out_lse;              /* or NULL */
 } spec_attend_params;

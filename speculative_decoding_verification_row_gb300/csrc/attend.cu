@@ -30,12 +30,13 @@ size_t spec_attend_scratch_size(int B, int W, int q_heads, int kv_heads, int hea
 
 int spec_attend_kv(const spec_kv_cache* cache, const spec_attend_params* p, void* scratch,
                    size_t scratch_bytes, spec_stream_t stream) {
+  constexpr double kLog2e = 1.4426950408889634073599246810019;
   AttendArgs a{};
   const int rc = kv_setup(cache, &a.c);
   if (rc != SPEC_OK) return rc;
   if (!p || p->size != sizeof(spec_attend_params) || !kv_strides_ok(p->q, p->q_strides) ||
       (p->dtype != SPEC_BF16 && p->dtype != SPEC_F16) || !p->seq_lens || !p->out ||
-      reinterpret_cast<uintptr_t>(p->out) % 16 != 0 || !isfinite(p->scale) ||
+      reinterpret_cast<uintptr_t>(p->out) % 16 != 0 || !isfinite((float)(p->scale * kLog2e)) ||
       (p->masks && p->W > SPEC_MAX_TREE_NODES) ||
       (long)a.c.max_blocks * a.c.tpb > kMaxPositions ||
       (long)p->B * p->W * p->q_heads > kMaxRows)
@@ -57,7 +58,7 @@ int spec_attend_kv(const spec_kv_cache* cache, const spec_attend_params* p, void
   a.masks = p->masks;
   a.words = (p->W + 31) / 32;
   a.tpb16_div = (unsigned)((1ull << 32) / (a.c.tpb / 16) + ((1ull << 32) % (a.c.tpb / 16) != 0));
-  a.scale_log2 = (float)((double)p->scale * 1.4426950408889634073599246810019);
+  a.scale_log2 = (float)(p->scale * kLog2e);
   a.out = static_cast<char*>(p->out);
   a.lse = p->out_lse;
   const cudaError_t e = few_rows(a.W, a.G, a.c.D)

@@ -83,6 +83,16 @@ def test_refusals_before_any_launch():
                      torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.4e38])
+def test_a_scale_whose_log2_form_is_infinite_is_refused(scale):
+    # it would turn scores of 0 into NaN
+    f = 16 * 1024
+    prm = sv.AttendParams(ctypes.sizeof(sv.AttendParams), f, (ctypes.c_int64 * 3)(256, 128, 64), 1, 2, 3, 4, f, None, None,
+                          scale, f, None)
+    rc = sv.lib().spec_attend_kv(ctypes.byref(_fake_cache()), ctypes.byref(prm), f, 1 << 40, None)
+    assert rc == sv.SPEC_EINVAL
+
+
 def test_tensor_memory_is_taken_behind_the_wait_for_the_kernel_before():
     # A launch that may start before the kernel in front has ended must not hold
     # what that kernel may still ask for.  Checked in the source: on a GPU the
