@@ -30,7 +30,7 @@ __device__ __forceinline__ unsigned col16(const AttendArgs& a, unsigned x) {
   return a.c.tpb == 16 ? x : __umulhi(x, a.tpb16_div);
 }
 constexpr long kMaxPositions = 1l << 30;
-// Most rows (tokens times query heads) of a call: its outputs would be 128 GB.
+// Most rows (tokens times query heads) of a call: its outputs would be 128 GB, 256 with D = 128.
 constexpr long kMaxRows = 1l << 30;
 
 // Rows of one request and KV head are numbered r = i * G + g (window token i,

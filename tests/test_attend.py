@@ -628,3 +628,118 @@ def test_scores_of_millions(G, W, exp):
     r = kv.attend(q, pool, scales, tables, [seq])
     assert out.abs().max() <= 1
     assert (np.abs(lse.double().cpu().numpy() - r["lse"]) <= (D + 8) * U * r["spread"] + 100).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tpb", [80, 256, 1024])
+@pytest.mark.parametrize("G,W,D", [(4, 1, 128), (2, 7, 64), (8, 33, 128), (4, 70, 64)])
+def test_large_and_odd_blocks(tpb, G, W, D):
+    rng = np.random.default_rng(tpb + W)
+    run_case(rng, [0, tpb - 1, 1500], [W, W, W // 2], W, 2, G, D, tpb, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,G,W", [(1, 4, 1), (3, 4, 4), (1, 4, 40), (5, 2, 90)])
+@pytest.mark.parametrize("fill", [0, 0x7f, 0xff])
+def test_scratch_may_hold_anything(B, G, W, fill):
+    rng = np.random.default_rng(B)
+    H, D, tpb, seq = 2, 128, 16, [2000, 0, 77, 500, 1][:B]
+    pool, scales, tables = cache(rng, np.array(seq) + W, H, D, tpb)
+    _, dq = make_q(rng, (B, W, H * G, D), "bf16")
+    a = [dq, dev(pool), dev(scales), i32(tables), i32(seq)]
+    want, want_lse = sv.attend_kv(*a, want_lse=True)
+    need = sv.lib().spec_attend_scratch_size(B, W, H * G, H, D)
+    scratch = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+    for _ in range(2):  # also: what the call itself left there
+        out, lse = sv.attend_kv(*a, want_lse=True, scratch=scratch)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.gpu
+def test_stored_scales_of_a_pool_beyond_32_bits():
+    H, D, tpb, W = 8, 128, 128, 4
+    n = (1 << 32) // (2 * H * tpb * D) + 200
+    rng = np.random.default_rng(12)
+    small, scales, tables = cache(rng, np.array([510 + W]), H, D, tpb, spare=0, extra_cols=0)
+    at = np.array([0, n - 1, n - 2, n - 150, n - 3])[:len(small)]
+    where = torch.from_numpy(at).cuda()
+    pool = torch.zeros((n, 2, H, tpb, D), dtype=torch.uint8, device="cuda")
+    pool[where] = dev(small)
+    big = torch.ones((n, 2, H), device="cuda")
+    big[where] = dev(scales)
+    k, dk = make_q(rng, (1, W, H, D), "bf16", 30.0)
+    sv.store_kv(dk, dk, pool, big, i32(at[tables]), i32([510]))
+    want, want_s = kv.store(k, k, small, scales, tables, [510])
+    assert np.array_equal(pool[where].cpu().numpy(), want)
+    assert np.array_equal(big[where].double().cpu().numpy(), want_s) and not np.array_equal(want_s, scales)
+    others = torch.ones(n, dtype=torch.bool, device="cuda")
+    others[where] = False
+    assert (big[others] == 1).all()
+
+
+@pytest.mark.gpu
+def test_a_captured_step_of_tree_decoding():
+    # every call of a step in one graph, replayed twice on the state of its start
+    import oracle
+    import workloads
+    rng = np.random.default_rng(13)
+    w = workloads.make("tree_b16_n60_l4_v151936_bf16", seed=4, B=4, V=4096)
+    B, N = w["B"], w["N"]
+    H, G, D, tpb = 2, 4, 64, 16
+    seq = np.array([30, 0, 47, 100], np.int32)
+    pool0, scales0, tables = cache(rng, seq, H, D, tpb, spare=40, extra_cols=5)
+    n, held = len(pool0), (-(-seq // tpb)).astype(np.int32)
+    pool0 &= 0x77  # no NaN codes
+    free = np.full(n, -1, np.int32)
+    spare = rng.permutation(np.setdiff1d(np.arange(n), tables))
+    free[:len(spare)] = spare
+    start = [pool0, scales0, tables, held, free, np.array([len(spare)], np.int32)]
+    k, dk = make_q(rng, (B, N, H, D), "bf16")
+    v, dv = make_q(rng, (B, N, H, D), "bf16")
+    q, dq = make_q(rng, (B, N, H * G, D), "bf16")
+    state = [dev(x) for x in start]
+    pool, scales, dtab, dheld, dfree, count = state
+    dseq, paths, tree = i32(seq), i32(w["paths"]), i32(w["tree_tokens"])
+    logits = dev(w["target"].view(np.int16)).view(torch.bfloat16)
+    ws = sv.Workspace()
+
+    def step():
+        slots, granted = sv.reserve_blocks(dseq, dtab, dheld, dfree, count, tpb, N)
+        masks = sv.tree_masks(paths, N)
+        sv.store_kv(dk, dv, pool, scales, dtab, dseq)
+        out, lse = sv.attend_kv(dq, pool, scales, dtab, dseq, masks=masks, want_lse=True)
+        _, acc, _, nodes = sv.verify_tree(logits, tree, paths, workspace=ws)
+        sv.relocate_quantised_kv(pool, scales, dtab, dseq, nodes, acc)
+        new, _, give = sv.rollback_paged(dseq, acc, N - 1, tpb, blocks_held=dheld)
+        sv.release_blocks(dtab, dheld, give, dfree, count)
+        return slots, granted, masks, out, lse, acc, nodes, new
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        slots, granted, masks, out, lse, acc, nodes, new = step()
+    # the oracle's step
+    slots_o, granted_o, t_o, h_o, c_o = kv.reserve(seq, None, tables, held, free, len(spare), tpb, N)
+    m_o = kv.tree_masks(w["paths"].astype(np.int32), N)
+    p_o, s_o = kv.store(k, v, pool0, scales0, t_o, seq)
+    r = kv.attend(q, p_o, s_o, t_o, seq, masks=m_o)
+    o = oracle.verify(w)
+    p_o, s_o = kv.relocate(p_o, s_o, t_o, seq, o["accepted_nodes"], o["num_accepted"])
+    len_o = seq + o["num_accepted"] + 1
+    t_o, h_o, f_o, c_o = kv.release(t_o, h_o, np.maximum(0, h_o - -(-len_o // tpb)), free, c_o)
+    for _ in range(2):
+        for x, x0 in zip(state, start):
+            x.copy_(dev(x0))
+        for x in (slots, granted, masks, acc, nodes, new, out, lse):
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for got, want in ((slots, slots_o), (granted, granted_o), (masks, m_o), (acc, o["num_accepted"]),
+                          (nodes, o["accepted_nodes"]), (new, len_o), (pool, p_o), (scales, s_o), (dtab, t_o),
+                          (dheld, h_o), (dfree, f_o), (count, [c_o])):
+            assert np.array_equal(got.cpu().numpy(), want)
+        check(out, lse, r, "bf16", D, np.ones((B, N), bool), 100)
