@@ -283,6 +283,32 @@ __host__ __device__ constexpr size_t part_floats(int D) { return (size_t)ROWS * 
 // desc words per CTA: {request, head, row tile, last CTA of the unit, its rows}; -1: none.
 constexpr int kDescWords = 8;
 
+// Four e4m3 bytes as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// Two of Q's elements as fp16.
+__device__ __forceinline__ uint32_t half2_of(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Bytes of w that are NaN codes, as bit 7 of each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+__device__ __forceinline__ float2 as_float2(uint32_t w, __nv_bfloat16*) {
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ float2 as_float2(uint32_t w, __half*) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 __device__ __forceinline__ uint32_t pack_out(float x, float y, __nv_bfloat16*) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -338,7 +364,7 @@ __device__ __forceinline__ void add_parts(Part<E>& s, const Part<E> (&p)[N]) {
   }
 }
 
-template <class T, int D, int ROWS, int KEYS>
+template <class T, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads, 2) attend_join_kernel(const AttendArgs a) {
   constexpr int E = D / 32;  // elements of a lane: 2 or 4
   __shared__ Part<E> sPart[kJoinRows][32];
@@ -405,7 +431,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attend_join_kernel(const Atte
   if (a.lse && lane == 0) a.lse[orow] = row_lse(sum.m, sum.l);
 }
 
-template <class T, int D, int ROWS, int KEYS>
+template <class T, int D, int ROWS>
 cudaError_t launch_join(const AttendArgs& a, int ctas, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, min(ROWS, ceil_div((long)a.W * a.G, 16) * 16) / kJoinRows);
@@ -416,7 +442,7 @@ cudaError_t launch_join(const AttendArgs& a, int ctas, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, ROWS, KEYS>, a);
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, ROWS>, a);
 }
 
 constexpr int kSms = 152;

@@ -83,37 +83,12 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Four e4m3 bytes as two fp16 pairs.
-__device__ __forceinline__ void e4m3x4_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
-      " cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t half2_of(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Bytes of w that are NaN codes, as bit 7 of each.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-
-__device__ __forceinline__ float2 as_float2(uint32_t w, __nv_bfloat16*) {
-  return make_float2(bf16_lo(w), bf16_hi(w));
-}
-__device__ __forceinline__ float2 as_float2(uint32_t w, __half*) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 template <class T, int D>
@@ -525,7 +500,7 @@ cudaError_t launch_rows(const AttendArgs& a, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
-  return launch_join<T, D, kRows, kKeys>(a, kCtas, st);
+  return launch_join<T, D, kRows>(a, kCtas, st);
 }
 
 }  // namespace

@@ -144,26 +144,6 @@ __host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn) {
   return 1u << 4 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kRows >> 4) << 24;
 }
 
-__device__ __forceinline__ void e4m3x4_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
-      " cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t half2_of(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-__device__ __forceinline__ float2 as_float2(uint32_t w, __nv_bfloat16*) {
-  return make_float2(bf16_lo(w), bf16_hi(w));
-}
-__device__ __forceinline__ float2 as_float2(uint32_t w, __half*) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -815,7 +795,7 @@ cudaError_t launch_tiles(const AttendArgs& a, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
-  return launch_join<T, D, kRows, kKeys>(a, kSms, st);
+  return launch_join<T, D, kRows>(a, kSms, st);
 }
 
 }  // namespace
