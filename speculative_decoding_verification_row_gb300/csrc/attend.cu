@@ -9,10 +9,10 @@ namespace {
 // Whether attend_rows.cu serves this many rows per KV head; else attend_tiles.cu.
 // The first reads the cache once for every 16 rows, the second once for 128 at
 // a step's fixed cost.  Measured with 64 requests of 4096 cached positions and
-// 8 KV heads: D = 128, rows 109 us for 16 rows and 194 for 20, tiles 172 for
-// both; D = 64, rows 67 us for 16 and 120 for 32, tiles 141 (and 224 against
-// 144 for 64).  With 4 requests of 30000 and D = 128: rows 61 us for 16 and 93
-// for 32, tiles 78.
+// 8 KV heads: D = 128, rows 106 us for 16 rows and 190 for 20, tiles 169 for
+// both; D = 64, rows 68 us for 16 and 120 for 32, tiles 138 (and 224 against
+// 141 for 64).  With 4 requests of 30000 and D = 128: rows 59 us for 16 and 91
+// for 32, tiles 77.
 bool few_rows(int W, int G, int D) { return (long)W * G <= (D == 64 ? 32 : 16); }
 
 }  // namespace

@@ -17,11 +17,11 @@
 // only when a key exceeds them by more than 7, so that the sums are rarely
 // rescaled.
 //
-// Measured with 32 heads over 8 KV heads of 128 and windows of 4 tokens: 256
-// requests of 8192 positions 689 us, 6.2 TB/s (0.92 of the measured copy rate);
-// 256 of 512 to 8192, 390 us, 5.9 TB/s (0.87).  One token of one request over
-// 1000 positions takes 12.3 us in a graph, both launches: latency (the shares,
-// the table, the rows, the four warps' merge, the join).
+// Measured in a graph with 32 heads over 8 KV heads of 128 and windows of 4
+// tokens: 256 requests of 8192 positions 682 us, 6.3 TB/s (0.93 of the measured
+// copy rate); 256 of 512 to 8192, 393 us, 5.8 TB/s (0.86).  One token of one
+// request over 1000 positions takes 12.6 us, both launches: latency (the
+// shares, the table, the rows, the four warps' merge, the join).
 #include "attend.cuh"
 
 namespace sv {
@@ -35,14 +35,15 @@ constexpr int kRThreads = kRWarps * 32;
 constexpr int kKeys = kStep * kRWarps;    // keys of a tile: one step of every warp
 constexpr int kStages = 4;
 // Cells of a unit besides its tiles: what its start and its result take.  256
-// requests of 512 to 8192 positions, 4 tokens: 413 us with 2, 403 with 4, 390
-// with 6, 384 with 8; 512 of 100 to 900: 187, 169, 162, 162; one token of one
-// request over 4000 positions: 14.8, 14.5, 14.2, 16.3.
+// requests of 512 to 8192 positions, 1 to 4 tokens each: 413 us with 2, 403 with
+// 4, 390 with 6, 384 with 8 (eager); 512 of 4 tokens over 100 to 900: 187, 169,
+// 162, 162 (160 now); one token of one request over 4000 positions: 14.8, 14.5,
+// 14.2, 16.3 (14.6 now).
 constexpr int kUnitCost = 6;
 // Cells below which a share is not worth a CTA.  One request, one token, 8 KV
 // heads, 100 / 1000 / 30000 positions: 10.5 / 12.3 / 34.7 us with 3 cells, 9.5
 // / 12.5 / 34.4 with 4, 15.7 / 13.4 / 34.4 with 6, 25.4 / 19.5 / 33.1 with 12
-// (with the join of that time; 9.7 / 12.4 / 24.6 now).
+// (with the join of that time; 10.0 / 12.4 / 24.5 now).
 constexpr int kLeastCells = 4;
 constexpr int kCtas = 3 * kSms;           // resident at 168 registers and 66 KB of shared memory
 using Div = Division<kRows, kKeys>;

@@ -23,8 +23,8 @@
 // scale goes into the exponent whole, as its log2.
 //
 // Measured with 32 heads over 8 KV heads of 128: 16 trees of 60 tokens over
-// 8192 positions 174 us, 740 TFLOP/s (0.39 of the measured dense rate; 16 of
-// the 256 rows are empty); over 512 to 8192, 108 us.  A tile takes about 2200
+// 8192 positions 169 us, 770 TFLOP/s (0.40 of the measured dense rate; 16 of
+// the 256 rows are empty); over 512 to 8192, 107 us.  A tile takes about 2200
 // clocks where its products take 1024: the hops weights -> product -> scores of
 // a row's chain, and the conversion of the pages, which the products wait for.
 #include "attend.cuh"

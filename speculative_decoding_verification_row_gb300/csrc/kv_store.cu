@@ -10,9 +10,10 @@
 //
 // At a step's sizes both are bound by latency: table -> rows -> maximum ->
 // codes.  In a graph (operands in L2) the store of 64 requests of 8 tokens, 8
-// heads of 128 takes 3.8 us, that of 4 prompts of 4001 tokens, 4 heads of 64,
-// 5.4 us; 64 prompts of 4096 tokens with 8 heads of 128, 280 us, 5.75 TB/s (0.85
-// of the measured copy rate).  The relocation of 16 requests' paths of 4 takes 3.9 us, of 256
+// heads of 128 takes 4.6 us (4.2 with 1 to 8 tokens each), that of 4 prompts of
+// 4001 tokens, 4 heads of 64, 7.2 us (of one beside three windows of 5 to 15
+// tokens, 5.7); 64 prompts of 4096 tokens with 8 heads of 128, 276 us, 5.8 TB/s
+// (0.86 of the measured copy rate).  The relocation of 16 requests' paths of 4 takes 3.9 us, of 256
 // requests' paths of 17 7.2 us.
 #include "kvcache.cuh"
 
