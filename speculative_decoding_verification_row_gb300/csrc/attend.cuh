@@ -259,7 +259,7 @@ __device__ __forceinline__ uint32_t weights_f16(float x, float y) {
 // s = f * 2^e with f in (1/2, 1]; f is smaller below 2^-126, and 0 for s = 0.
 __device__ __forceinline__ float scale_exponent(float s, float* f) {
   const uint32_t bits = __float_as_uint(s), frac = bits & 0x7fffffu;
-  const int field = (int)(bits >> 23);
+  const int field = (int)(bits >> 23 & 255u);  // without the sign: -0 is 0
   if (field == 0) {
     *f = s * 0x1p126f;
     return -126.f;

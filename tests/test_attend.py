@@ -615,6 +615,19 @@ def test_a_value_scale_of_zero(G, W):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
+def test_scales_of_minus_zero(G, W):
+    rng = np.random.default_rng(6)
+
+    def edit(pool, scales, tables):
+        scales[tables[0, 1:4]] = -0.0
+        scales[tables[1]] = -0.0
+        pool[(pool & 127) == 127] = 0
+    out, lse = run_case(rng, [200, 70], [W, W], W, 2, G, 64, 16, "bf16", edit=edit)
+    assert (out[1] == 0).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W", [(1, 1), (4, 4), (4, 40)])
 @pytest.mark.parametrize("exp", [4, 8, 12])
 def test_scores_of_millions(G, W, exp):
     # scores up to 2^26, where fp32 hardly tells one from the next: a weighted mean of V all the same
