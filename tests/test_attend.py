@@ -756,3 +756,59 @@ def test_a_captured_step_of_tree_decoding():
                           (dheld, h_o), (dfree, f_o), (count, [c_o])):
             assert np.array_equal(got.cpu().numpy(), want)
         check(out, lse, r, "bf16", D, np.ones((B, N), bool), 100)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,D", [(1, 64), (2, 128)])
+def test_the_longest_window(G, D):
+    # a prompt of 65536 tokens; a row of it is the row of a window of one behind its prefix
+    rng = np.random.default_rng(D)
+    H, tpb, W = 1, 64, 65536
+    pool, scales, tables = cache(rng, np.array([W]), H, D, tpb)
+    q, dq = make_q(rng, (1, W, H * G, D), "bf16")
+    out, lse = sv.attend_kv(dq, dev(pool), dev(scales), i32(tables), i32([0]), want_lse=True)
+    for i in (0, 1, 127, 128, 4095, 32768, 65534, 65535):
+        r = kv.attend(q[:, i:i + 1], pool, scales, tables, [i])
+        check(out[:, i:i + 1], lse[:, i:i + 1], r, "bf16", D, np.ones((1, 1), bool), 448 * scales.max())
+    assert torch.isfinite(out).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("W,H,G,D", [(1, 1, 1, 64), (1, 1, 4, 128), (3, 1, 16, 64)])
+def test_the_largest_batch(W, H, G, D):
+    # 8192 requests of 0 to 60 positions over shared pages
+    rng = np.random.default_rng(W)
+    B, tpb = 8192, 16
+    pool, scales, tables = cache(rng, np.array([60 + W]), H, D, tpb)
+    seq = rng.integers(0, 61, B)
+    _, dq = make_q(rng, (B, W, H * G, D), "f16")
+    out, lse = sv.attend_kv(dq, dev(pool), dev(scales), i32(np.repeat(tables, B, 0)), i32(seq), want_lse=True)
+    for b in [0, 1, B - 1] + list(rng.integers(0, B, 40)):
+        r = kv.attend(dq[b:b + 1].double().cpu().numpy(), pool, scales, tables, seq[b:b + 1])
+        check(out[b:b + 1], lse[b:b + 1], r, "f16", D, np.ones((1, W), bool), 448 * scales.max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("W,H,G", [(1, 1024, 1), (1, 1024, 16), (2, 1024, 16)])
+def test_the_most_heads(W, H, G):
+    rng = np.random.default_rng(G)
+    D, tpb, seq = 64, 16, [17, 3]
+    pool, scales, tables = cache(rng, np.array(seq) + W, H, D, tpb)
+    k, dk = make_q(rng, (2, W, H, D), "bf16")
+    p, s = dev(pool), dev(scales)
+    sv.store_kv(dk, dk, p, s, i32(tables), i32(seq))
+    q, dq = make_q(rng, (2, W, H * G, D), "bf16")
+    out, lse = sv.attend_kv(dq, p, s, i32(tables), i32(seq), want_lse=True)
+    pool, scales = kv.store(k, k, pool, scales, tables, seq)
+    assert np.array_equal(s.double().cpu().numpy(), scales)
+    r = kv.attend(q, pool, scales, tables, seq)
+    check(out, lse, r, "bf16", D, np.ones((2, W), bool), 448 * scales.max())
+
+
+@pytest.mark.gpu
+def test_the_widest_tree():
+    rng = np.random.default_rng(1024)
+    W, H, G, D, tpb = 1024, 1, 2, 64, 32
+    paths = random_paths(rng, W, W, 33)[None]
+    masks = kv.tree_masks(paths, W)
+    run_case(rng, [70], [W], W, H, G, D, tpb, "bf16", masks=masks)
