@@ -584,6 +584,193 @@ int spec_relocate_quantised_kv(const spec_kv_cache *cache, const int32_t *base_l
                                const int32_t *accepted_nodes, const int32_t *num_accepted, int B,
                                int L, spec_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * What a step needs around the verify and the cache: the target's logits
+ * penalised, biased and masked before the verify, queries and keys rotated to
+ * their positions before the store and the attention, and the positions of
+ * least attention dropped from a cache that has grown to its budget.  None of
+ * these calls uses a workspace or records a status.  Results do not depend on
+ * timing: equal inputs give equal bits.
+ * ---------------------------------------------------------------------- */
+
+/* Most entries of a request's bias list. */
+#define SPEC_MAX_BIAS 1024
+
+/* Penalties for repeated tokens, biases and grammar masks on the logits of a
+ * window's rows, for the verify calls to read.
+ *   logits, out [B, R, V] of `dtype` (SPEC_F32 or SPEC_BF16); R at most
+ *           SPEC_MAX_TREE_NODES.  `out` may be `logits`: then only the logits
+ *           that change are written.  Otherwise the two must not overlap.
+ *   tokens  [B, T] int32 or NULL: the request's tokens so far, the first
+ *           prompt_lens[b] of them its prompt, the others its output;
+ *           token_lens [B] (NULL: T) of them are real.  Lengths are taken into
+ *           [0, T] and [0, token_lens[b]]; prompt_lens NULL: no prompt.
+ *   draft_tokens: the window's tokens, which count as output for the rows
+ *           behind them.  Without masks [B, R - 1], a chain: row i follows
+ *           drafts 0..i-1.  With masks [B, R] and masks [B, R, ceil(R / 32)]
+ *           int32 (spec_tree_masks), a tree: row n follows the nodes m >= 1
+ *           whose bits of its mask are set (node 0 is the last of `tokens`).
+ *           NULL: none.
+ *   draft_lens [B] int32 or NULL (a chain's): only rows 0..draft_lens[b] are
+ *           read and written; none where it lies outside [0, R - 1].
+ *   repetition, frequency, presence [B] float32, each or NULL (1, 0, 0).
+ *           With c the times that token t stands in the output before the row,
+ *           and x its logit: if t stands in the prompt or c > 0, x becomes
+ *           x / repetition where x > 0 and x * repetition elsewhere; then, if
+ *           c > 0, x - frequency c - presence.
+ *   bias_ids, bias_values [B, num_bias]: then x + the sum of the values of t
+ *           (in the list's order; -inf bans it).  Ids outside [0, V), like
+ *           tokens outside it in the other lists, are ignored.
+ *   allowed [num_allowed, ceil(V / 32)] int32 or NULL: last, x becomes -inf
+ *           where bit t % 32 of word t / 32 of the row's mask is clear,
+ *           whatever x is (NaN included).  allowed_rows [B, R] is each row's
+ *           mask, below 0 for none (num_allowed or more: all of the row
+ *           becomes -inf); NULL: mask b * R + i, and num_allowed is B * R.
+ * Arithmetic in fp32, rounded once. */
+typedef struct spec_adjust_params {
+    size_t size;
+    const void *logits;
+    void *out;
+    int dtype;
+    int B, R, V;
+    const int32_t *tokens;
+    const int32_t *token_lens;
+    const int32_t *prompt_lens;
+    int T;
+    const int32_t *draft_tokens;
+    const int32_t *masks;
+    const int32_t *draft_lens;
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const int32_t *bias_ids;
+    const float *bias_values;
+    int num_bias;
+    const int32_t *allowed;
+    const int32_t *allowed_rows;
+    int num_allowed;
+} spec_adjust_params;
+int spec_adjust_logits(const spec_adjust_params *params, spec_stream_t stream);
+
+/* Rotary positions of a window's queries and keys.
+ *   q [B, W, q_heads, head_dim], k [B, W, k_heads, head_dim] of `dtype`
+ *         (SPEC_BF16 or SPEC_F16), strided as in spec_store_kv, and out_q,
+ *         out_k likewise; head_dim a multiple of 16 up to 512.  q or k is NULL
+ *         with no heads.  An output may be its input (same strides) and must
+ *         overlap no other array, nor itself.
+ *   starts [B] int32: the position of window token 0.  It may differ from the
+ *         cache's cursor (spec_evict_kv drops positions of the cache, not of
+ *         the text).  Token i has position starts[b] + i, or with masks
+ *         [B, W, ceil(W / 32)] (spec_tree_masks; W <= SPEC_MAX_TREE_NODES)
+ *         starts[b] + its depth, one less than the bits of its row (at least 0).
+ *   inv_freq [pairs] float64: radians per position; pairs a multiple of 8,
+ *         2 * pairs at most head_dim.  Pair i is
+ *         elements (i, i + pairs), or (2 i, 2 i + 1) where interleaved != 0;
+ *         elements from 2 * pairs on are copied.
+ *   (a, b) becomes gain * (a cos - b sin, b cos + a sin) of the angle position
+ *         * inv_freq.  The angle is reduced before it is rounded: while it
+ *         stays below 2^34 radians, sine and cosine are good to 2^-21 however
+ *         far the position.  Rounded once.
+ * Padded rows (window_lens) are neither read nor written; a length outside
+ * [0, W] has none. */
+typedef struct spec_rotate_params {
+    size_t size;
+    const void *q;
+    const void *k;
+    void *out_q;
+    void *out_k;
+    int64_t q_strides[3], k_strides[3], out_q_strides[3], out_k_strides[3];
+    int dtype;
+    int B, W, q_heads, k_heads, head_dim;
+    const int32_t *starts;
+    const int32_t *window_lens;  /* [B] or NULL */
+    const int32_t *masks;        /* or NULL */
+    const double *inv_freq;
+    int pairs, interleaved;
+    float gain;                  /* finite */
+} spec_rotate_params;
+int spec_rotate_qk(const spec_rotate_params *params, spec_stream_t stream);
+
+/* spec_rotate_qk and spec_store_kv in one call: q rotated to out_q, the
+ * rotated keys (rounded to their type, as spec_rotate_qk leaves them) and v
+ * into the cache at seq_lens, with the results of the two calls, bit for bit.
+ * out_k must be NULL, k_heads and head_dim are the cache's; v is strided like
+ * k.  The rows of q are rotated for every request whose window length is in
+ * [0, W], those that store nothing included. */
+int spec_rotate_store_kv(const spec_kv_cache *cache, const spec_rotate_params *params,
+                         const void *v, const int64_t *v_strides, const int32_t *seq_lens,
+                         spec_stream_t stream);
+
+/* The attention that each cached position drew from a window's rows.
+ *   q, q_strides, dtype, seq_lens, window_lens, scale: as for spec_attend_kv,
+ *         the window a chain.  (Of a tree, the accepted path is one: its rows
+ *         of q and lse, window length n + 1, after the relocation.)
+ *   lse   [B, W, q_heads] float32: spec_attend_kv's, of the same rows.
+ *   weights, out [B, kv_heads, T] float32: for the positions t of request b,
+ *         t < min(seq_lens[b] + w_b, T),
+ *         out[b, h, t] = decay * weights[b, h, t]   (t < seq_lens[b] only)
+ *                        + sum of exp(scale * q . k_t - lse)
+ *         over the window's tokens that see t and the query heads of KV head
+ *         h.  weights NULL: 0.  `out` may be `weights`, and is left as it is
+ *         at every other position.  A row whose lse is -inf adds nothing.
+ * Positions in a block whose id lies outside [0, num_blocks) read NaN; for a
+ * request with seq_lens < 0, w_b outside [0, W] or a window past max_blocks
+ * blocks nothing is written.  Scores and sums are held in fp32. */
+typedef struct spec_weigh_params {
+    size_t size;
+    const void *q;
+    int64_t q_strides[3];
+    int dtype;
+    int B, W, q_heads;
+    const int32_t *seq_lens;
+    const int32_t *window_lens;  /* [B] or NULL */
+    const float *lse;
+    float scale;                 /* finite, times log2(e) too */
+    const float *weights;        /* or NULL */
+    float decay;                 /* finite */
+    float *out;
+    int T;
+} spec_weigh_params;
+int spec_weigh_kv(const spec_kv_cache *cache, const spec_weigh_params *params, spec_stream_t stream);
+
+/* Drops cached positions, head by head, down to `keep` of them.
+ *   weights [B, kv_heads, T] float32 (spec_weigh_kv).  Of a request with
+ *         seq_lens[b] > keep, each KV head keeps the first `first` positions,
+ *         the last `recent`, and of those between the ones of largest weight,
+ *         the lowest position among equals (NaN counts as less than any
+ *         number, -0 as 0).  first + recent <= keep.
+ *   The kept rows of K and V move, in their order, to positions 0..keep-1.  A
+ *         block that receives rows gets, per kind and head, the largest scale
+ *         among them; codes whose scale grows are rounded again, as in
+ *         spec_relocate_quantised_kv.  Rows from position keep on are dead.
+ *   new_lens [B] = min(seq_lens[b], keep) (may alias seq_lens);
+ *   kept [B, kv_heads, keep] int32: the positions that the rows came from, -1
+ *         behind new_lens[b]; out_weights [B, kv_heads, T_out] float32, T_out
+ *         >= keep: their weights, left as it is from new_lens[b] on (may be
+ *         `weights` itself, with T_out = T);
+ *   free_blocks [B] or NULL = max(0, blocks_held[b] - ceil(new_len /
+ *         tokens_per_block)), for spec_release_blocks.
+ * A request of at most `keep` positions keeps all and moves nothing.  One with
+ * seq_lens < 0, more than max_blocks blocks or T positions, or a block id
+ * outside [0, num_blocks) among those it has is left untouched: new_lens =
+ * seq_lens, its kept rows all -1, free_blocks 0.  Blocks must not be shared
+ * between requests, nor stand twice in a request's row. */
+typedef struct spec_evict_params {
+    size_t size;
+    const float *weights;
+    int T;
+    int B;
+    const int32_t *seq_lens;
+    int keep, first, recent;
+    int32_t *new_lens;
+    int32_t *kept;
+    float *out_weights;
+    int T_out;
+    const int32_t *blocks_held;  /* [B] or NULL */
+    int32_t *free_blocks;        /* [B] or NULL */
+} spec_evict_params;
+int spec_evict_kv(const spec_kv_cache *cache, const spec_evict_params *params, spec_stream_t stream);
+
 /* Synchronise `stream`, read the workspace status word into *status_out
  * (SPEC_OK, SPEC_EBADINDEX or SPEC_ETIMEOUT) and clear it.  Returns SPEC_OK, SPEC_EINVAL or
  * SPEC_ECUDA. */

@@ -22,6 +22,14 @@ The paged 8-bit KV cache a step runs on:
   store_kv         a window's K and V rows into the cache
   attend_kv        attention of the window's rows over the cache
   relocate_quantised_kv  the accepted nodes' rows behind the prefix
+
+Around them:
+  adjust_logits    penalties, biases and grammar masks on a window's logits
+  rotate_qk        rotary positions of a window's queries and keys;
+                   rotary_frequencies gives the angles per position
+  rotate_store_kv  the same, keys and values going into the cache
+  weigh_kv         the attention each cached position drew from a window
+  evict_kv         the positions of least weight dropped from the cache
 """
 from __future__ import annotations
 
@@ -32,6 +40,7 @@ import threading
 
 import torch
 
+from .rotary import rotary_frequencies  # noqa: F401  (host arithmetic)
 from .stats import acceptance_stats, anchored_emitted  # noqa: F401  (host bookkeeping)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspecverify.so")
@@ -45,6 +54,7 @@ SPEC_MAX_TREE_NODES = 1024
 SPEC_MAX_PATH_LEN = 64
 SPEC_MAX_TOPK = 256
 SPEC_MAX_WINDOW = 65536
+SPEC_MAX_BIAS = 1024
 
 # Every entry point the header declares.
 SYMBOLS = ("spec_workspace_size", "spec_workspace_init", "spec_verify_chain",
@@ -54,7 +64,8 @@ SYMBOLS = ("spec_workspace_size", "spec_workspace_init", "spec_verify_chain",
            "spec_verify_chain_ex", "spec_verify_greedy_ex", "spec_rollback_paged",
            "spec_workspace_size_filtered", "spec_test_timeout_chain", "spec_test_timeout_greedy",
            "spec_verify_tree_sampled", "spec_reserve_blocks", "spec_release_blocks", "spec_tree_masks",
-           "spec_store_kv", "spec_attend_kv", "spec_attend_scratch_size", "spec_relocate_quantised_kv")
+           "spec_store_kv", "spec_attend_kv", "spec_attend_scratch_size", "spec_relocate_quantised_kv",
+           "spec_adjust_logits", "spec_rotate_qk", "spec_rotate_store_kv", "spec_weigh_kv", "spec_evict_kv")
 SPEC_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 class ChainParams(ctypes.Structure):
@@ -94,6 +105,48 @@ class AttendParams(ctypes.Structure):
                 ("q_heads", ctypes.c_int), ("seq_lens", ctypes.c_void_p),
                 ("window_lens", ctypes.c_void_p), ("masks", ctypes.c_void_p),
                 ("scale", ctypes.c_float), ("out", ctypes.c_void_p), ("out_lse", ctypes.c_void_p)]
+
+
+class AdjustParams(ctypes.Structure):
+    """spec_adjust_params (include/spec_verify.h), field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("logits", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("R", ctypes.c_int), ("V", ctypes.c_int),
+                ("tokens", ctypes.c_void_p), ("token_lens", ctypes.c_void_p), ("prompt_lens", ctypes.c_void_p),
+                ("T", ctypes.c_int), ("draft_tokens", ctypes.c_void_p), ("masks", ctypes.c_void_p),
+                ("draft_lens", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("num_bias", ctypes.c_int), ("allowed", ctypes.c_void_p), ("allowed_rows", ctypes.c_void_p),
+                ("num_allowed", ctypes.c_int)]
+
+
+class RotateParams(ctypes.Structure):
+    """spec_rotate_params (include/spec_verify.h), field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("out_q", ctypes.c_void_p), ("out_k", ctypes.c_void_p), ("q_strides", ctypes.c_int64 * 3),
+                ("k_strides", ctypes.c_int64 * 3), ("out_q_strides", ctypes.c_int64 * 3),
+                ("out_k_strides", ctypes.c_int64 * 3), ("dtype", ctypes.c_int), ("B", ctypes.c_int),
+                ("W", ctypes.c_int), ("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("starts", ctypes.c_void_p), ("window_lens", ctypes.c_void_p),
+                ("masks", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("pairs", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("gain", ctypes.c_float)]
+
+
+class WeighParams(ctypes.Structure):
+    """spec_weigh_params (include/spec_verify.h), field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("q", ctypes.c_void_p), ("q_strides", ctypes.c_int64 * 3),
+                ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("W", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("seq_lens", ctypes.c_void_p), ("window_lens", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("weights", ctypes.c_void_p), ("decay", ctypes.c_float),
+                ("out", ctypes.c_void_p), ("T", ctypes.c_int)]
+
+
+class EvictParams(ctypes.Structure):
+    """spec_evict_params (include/spec_verify.h), field for field."""
+    _fields_ = [("size", ctypes.c_size_t), ("weights", ctypes.c_void_p), ("T", ctypes.c_int), ("B", ctypes.c_int),
+                ("seq_lens", ctypes.c_void_p), ("keep", ctypes.c_int), ("first", ctypes.c_int),
+                ("recent", ctypes.c_int), ("new_lens", ctypes.c_void_p), ("kept", ctypes.c_void_p),
+                ("out_weights", ctypes.c_void_p), ("T_out", ctypes.c_int), ("blocks_held", ctypes.c_void_p),
+                ("free_blocks", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -138,6 +191,11 @@ def _bind(lib):
     lib.spec_attend_scratch_size.argtypes = [I, I, I, I, I]
     lib.spec_attend_scratch_size.restype = S
     lib.spec_relocate_quantised_kv.argtypes = [ctypes.POINTER(KvCache), P, P, P, I, I, P]
+    lib.spec_adjust_logits.argtypes = [ctypes.POINTER(AdjustParams), P]
+    lib.spec_rotate_qk.argtypes = [ctypes.POINTER(RotateParams), P]
+    lib.spec_rotate_store_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(RotateParams), P, S3, P, P]
+    lib.spec_weigh_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(WeighParams), P]
+    lib.spec_evict_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(EvictParams), P]
     lib.spec_status_string.argtypes = [I]
     lib.spec_status_string.restype = ctypes.c_char_p
     for f in ("spec_workspace_init", "spec_verify_chain", "spec_verify_greedy", "spec_verify_tree",
@@ -146,7 +204,8 @@ def _bind(lib):
               "spec_verify_chain_ex", "spec_verify_greedy_ex", "spec_rollback_paged",
               "spec_test_timeout_chain", "spec_test_timeout_greedy", "spec_verify_tree_sampled",
               "spec_reserve_blocks", "spec_release_blocks", "spec_tree_masks", "spec_store_kv",
-              "spec_attend_kv", "spec_relocate_quantised_kv"):
+              "spec_attend_kv", "spec_relocate_quantised_kv", "spec_adjust_logits", "spec_rotate_qk",
+              "spec_rotate_store_kv", "spec_weigh_kv", "spec_evict_kv"):
         getattr(lib, f).restype = I
     return lib
 
@@ -792,6 +851,286 @@ def relocate_quantised_kv(kv_pool, kv_scales, block_tables, base_lens, accepted_
     if rc != SPEC_OK:
         raise SpecError("spec_relocate_quantised_kv", rc)
     return kv_pool
+
+
+# ---------------------------------------------------------------- around the verify and the cache
+_ADJUST_BYTES, _ROTATE_BYTES = ctypes.sizeof(AdjustParams), ctypes.sizeof(RotateParams)
+_WEIGH_BYTES, _EVICT_BYTES = ctypes.sizeof(WeighParams), ctypes.sizeof(EvictParams)
+
+
+def adjust_logits(logits, *, tokens=None, token_lens=None, prompt_lens=None, repetition=None, frequency=None,
+                  presence=None, bias_ids=None, bias_values=None, allowed=None, allowed_rows=None,
+                  draft_tokens=None, draft_lens=None, masks=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on the logits
+    [B, R, V] (float32 or bfloat16) of a window's rows, before verify_chain,
+    verify_greedy (R = k + 1) or verify_tree (R = N); returns out [B, R, V].
+    out=logits changes them in place and touches only what changes.
+
+    tokens [B, T] int32: the request's tokens so far, token_lens [B] of them
+    real (T by default), the first prompt_lens [B] of these its prompt (none
+    by default).  draft_tokens: the window's tokens, counted as output by the
+    rows behind them: [B, R - 1] of a chain, or [B, R] (verify_tree's
+    tree_tokens) with masks [B, R, ceil(R / 32)] (tree_masks).  draft_lens [B]:
+    rows past it are left as they are in `out` (zeros in a tensor made here).
+    repetition, frequency, presence [B] float32: penalties; with none of them
+    the tokens change nothing.  bias_ids [B, M] int32 (-1: none), bias_values
+    [B, M] float32.  allowed [n, ceil(V / 32)] int32: token masks, and
+    allowed_rows [B, R] int32 each row's (below 0: none); by default one for
+    each row, [B, R, ceil(V / 32)] or [B * R, ...]."""
+    dev = _cuda(logits, "logits", ("B", "R", "V"))
+    B, R, V = logits.shape
+    code = _logit_code(logits, "logits")
+    words = -(-V // 32)
+    src = _at(logits, "logits", dev, logits.dtype, (B, R, V))
+
+    def optional(t, name, dtype, shape):
+        return None if t is None else _at(t, name, dev, dtype, shape)
+    # the arguments keep their names, so that a tensor made for the call lives until the launch
+    T = M = n = 0
+    if tokens is not None:
+        _cuda(tokens, "tokens", ("B", "T"))
+        T = tokens.shape[1]
+    elif token_lens is not None or prompt_lens is not None:
+        raise ValueError("token_lens and prompt_lens go with tokens")
+    if masks is not None and draft_tokens is None:
+        raise ValueError("masks go with draft_tokens")
+    if masks is not None and draft_lens is not None:
+        raise ValueError("draft_lens are a chain's: a tree has masks")
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids and bias_values go together")
+    if bias_ids is not None:
+        _cuda(bias_ids, "bias_ids", ("B", "M"))
+        M = bias_ids.shape[1]
+    if allowed is None and allowed_rows is not None:
+        raise ValueError("allowed_rows go with allowed")
+    mask_shape = None
+    if allowed is not None:
+        if allowed_rows is None:
+            n = B * R
+            mask_shape = (B, R, words) if isinstance(allowed, torch.Tensor) and allowed.dim() == 3 else (n, words)
+        else:
+            _cuda(allowed, "allowed", ("n", "ceil(V / 32)"))
+            n = allowed.shape[0]
+            mask_shape = (n, words)
+    said = optional(tokens, "tokens", _I32, (B, T))
+    lists = (optional(token_lens, "token_lens", _I32, (B,)), optional(prompt_lens, "prompt_lens", _I32, (B,)))
+    window = (optional(draft_tokens, "draft_tokens", _I32, (B, R if masks is not None else R - 1)),
+              optional(masks, "masks", _I32, (B, R, -(-R // 32))), optional(draft_lens, "draft_lens", _I32, (B,)))
+    penalties = (optional(repetition, "repetition", _F32, (B,)), optional(frequency, "frequency", _F32, (B,)),
+                 optional(presence, "presence", _F32, (B,)))
+    bias = optional(bias_ids, "bias_ids", _I32, (B, M)), optional(bias_values, "bias_values", _F32, (B, M))
+    grammar = optional(allowed, "allowed", _I32, mask_shape), optional(allowed_rows, "allowed_rows", _I32, (B, R))
+    if T == 0:  # no token: nothing to count
+        said = None
+    if M == 0:
+        bias = None, None
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        if out is None:
+            out = (torch.empty if draft_lens is None else torch.zeros)((B, R, V), dtype=logits.dtype, device=dev)
+        dst = _at(out, "out", dev, logits.dtype, (B, R, V))
+        prm = AdjustParams(_ADJUST_BYTES, src, dst, code, B, R, V, said, *lists, T, *window, *penalties, *bias, M, *grammar,
+                           n)
+        rc = lib().spec_adjust_logits(prm, sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_adjust_logits", rc)
+    return out
+
+
+_NO_STRIDES = _Strides(0, 0, 0)
+
+
+def _rotation(q, k, starts, inv_freq, interleaved, gain, window_lens, masks, out_q, dev, B, W, D, dtype):
+    """A RotateParams of everything but where the keys go."""
+    _cuda(inv_freq, "inv_freq", ("pairs",))
+    pairs = inv_freq.shape[0]
+    if pairs < 8 or pairs % 8 or 2 * pairs > D:
+        raise ValueError(f"inv_freq must have a multiple of 8 elements, at most {D // 2}, got {pairs}")
+    if masks is not None and W > SPEC_MAX_TREE_NODES:
+        raise ValueError(f"masks are for windows of at most {SPEC_MAX_TREE_NODES} tokens")
+    qp = kp = oq = None
+    qs = ks = os = _NO_STRIDES
+    Hq = Hk = 0
+    if q is not None:
+        _cuda(q, "q", ("B", "W", "Hq", "D"))
+        Hq = q.shape[2]
+        qp, qs = _rows(q, "q", dev, (B, W, Hq, D), dtype)
+        oq, os = _rows(out_q, "out_q", dev, (B, W, Hq, D), dtype)
+    if k is not None:
+        _cuda(k, "k", ("B", "W", "Hkv", "D"))
+        Hk = k.shape[2]
+        kp, ks = _rows(k, "k", dev, (B, W, Hk, D), dtype)
+    return RotateParams(_ROTATE_BYTES, qp, kp, oq, None, qs, ks, os, _NO_STRIDES,
+                        SPEC_BF16 if dtype is torch.bfloat16 else SPEC_F16, B, W, Hq, Hk, D,
+                        _at(starts, "starts", dev, _I32, (B,)),
+                        None if window_lens is None else _at(window_lens, "window_lens", dev, _I32, (B,)),
+                        None if masks is None else _at(masks, "masks", dev, _I32, (B, W, -(-W // 32))),
+                        _at(inv_freq, "inv_freq", dev, torch.float64, (pairs,)), pairs, int(bool(interleaved)), gain)
+
+
+def _outside(t, out, name):
+    """An output is its input (of the same strides) or lies apart from it."""
+    if out is not None and out is not t and t.data_ptr() == out.data_ptr() and t.stride() != out.stride():
+        raise ValueError(f"{name} is its input's memory with other strides")
+
+
+def rotate_qk(q, k, starts, inv_freq, *, interleaved=False, gain: float = 1.0, window_lens=None, masks=None,
+              out_q=None, out_k=None, stream=None):
+    """Rotary positions of a window's rows q [B, W, Hq, D] and k [B, W, Hkv, D]
+    (bfloat16 or float16, any 16-byte aligned strides; k or q may be None);
+    returns (q, k) rotated.  out_q=q and out_k=k rotate in place.
+
+    starts [B] int32: the position of token 0.  Token i of a chain has
+    position starts + i, a tree's node (masks [B, W, ceil(W / 32)], tree_masks)
+    starts + its depth.  inv_freq [pairs] float64 and gain: rotary_frequencies.
+    The first 2 * pairs elements turn, as pairs (i, i + pairs) or, interleaved,
+    (2 i, 2 i + 1).  Rows behind a window's end are left as they are in the
+    outputs (zeros in tensors made here)."""
+    x = q if q is not None else k
+    dev = _cuda(x, "q" if q is not None else "k", ("B", "W", "heads", "D"))
+    B, W, _, D = x.shape
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        make = torch.empty if window_lens is None else torch.zeros
+        if q is not None and out_q is None:
+            out_q = make(q.shape, dtype=x.dtype, device=dev)
+        if k is not None and out_k is None:
+            out_k = make(k.shape, dtype=x.dtype, device=dev)
+        if (q is None and out_q is not None) or (k is None and out_k is not None):
+            raise ValueError("an output without its input")
+        prm = _rotation(q, k, starts, inv_freq, interleaved, gain, window_lens, masks, out_q, dev, B, W, D, x.dtype)
+        if k is not None:
+            prm.out_k, prm.out_k_strides = _rows(out_k, "out_k", dev, k.shape, x.dtype)
+            _outside(k, out_k, "out_k")
+        if q is not None:
+            _outside(q, out_q, "out_q")
+        _apart(prm.out_q, prm.out_k)
+        _apart(prm.q, prm.out_k)
+        _apart(prm.out_q, prm.k)
+        rc = lib().spec_rotate_qk(prm, sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_rotate_qk", rc)
+    return out_q, out_k
+
+
+def rotate_store_kv(q, k, v, inv_freq, kv_pool, kv_scales, block_tables, seq_lens, *, starts=None,
+                    interleaved=False, gain: float = 1.0, window_lens=None, masks=None, out_q=None, stream=None):
+    """rotate_qk and store_kv in one call, with their results: returns q
+    [B, W, Hq, D] rotated, and writes the rotated k and v [B, W, Hkv, D] at
+    logical positions seq_lens[b] + i of the paged cache.  starts defaults to
+    seq_lens: pass the text's own positions once evict_kv has dropped some."""
+    cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
+    _cuda(k, "k", ("B", "W", "Hkv", "D"))
+    W, H, D = k.shape[1], cache.kv_heads, cache.head_dim
+    _cuda(q, "q", ("B", "W", "Hq", "D"))
+    vp, vs = _rows(v, "v", dev, (B, W, H, D), k.dtype)
+    _rows(k, "k", dev, (B, W, H, D), k.dtype)
+    seq = _at(seq_lens, "seq_lens", dev, _I32, (B,))
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        if out_q is None:
+            out_q = (torch.empty if window_lens is None else torch.zeros)(q.shape, dtype=k.dtype, device=dev)
+        prm = _rotation(q, k, seq_lens if starts is None else starts, inv_freq, interleaved, gain, window_lens, masks,
+                        out_q, dev, B, W, D, k.dtype)
+        _outside(q, out_q, "out_q")
+        _apart(prm.out_q, prm.k, vp, cache.pool)
+        rc = lib().spec_rotate_store_kv(cache, prm, vp, vs, seq, sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_rotate_store_kv", rc)
+    return out_q
+
+
+def weigh_kv(q, lse, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=None, scale: float | None = None,
+             weights=None, decay: float = 1.0, out=None, stream=None):
+    """The attention that each cached position drew from a window's rows: q
+    [B, W, Hq, D] and lse [B, W, Hq] float32 of attend_kv; returns out
+    [B, Hkv, T] float32, decay * weights (before seq_lens[b]; none without
+    weights) plus the window's probabilities, summed over its tokens and the
+    query heads of each KV head.
+
+    The window is a chain; of a tree, pass the accepted path's rows of q and lse
+    with window_lens = num_accepted + 1 after relocate_quantised_kv.  T is that
+    of weights or out, else the cache's max_blocks * tokens_per_block; positions
+    behind a request's end are left as they are in `out` (zeros in a tensor made
+    here).  out=weights updates in place."""
+    cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
+    _cuda(q, "q", ("B", "W", "Hq", "D"))
+    W, Hq, D, H = q.shape[1], q.shape[2], cache.head_dim, cache.kv_heads
+    if Hq % H:
+        raise ValueError(f"q must have a multiple of {H} heads, got {Hq}")
+    qp, qs = _rows(q, "q", dev, (B, W, Hq, D), q.dtype)
+    T = cache.max_blocks * cache.tokens_per_block
+    for t, name in ((weights, "weights"), (out, "out")):
+        if t is not None:
+            _cuda(t, name, ("B", "Hkv", "T"))
+            T = t.shape[2]
+    seq = _at(seq_lens, "seq_lens", dev, _I32, (B,))
+    win = None if window_lens is None else _at(window_lens, "window_lens", dev, _I32, (B,))
+    lp = _at(lse, "lse", dev, _F32, (B, W, Hq))
+    wp = None if weights is None else _at(weights, "weights", dev, _F32, (B, H, T))
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        if out is None:
+            out = torch.zeros((B, H, T), dtype=_F32, device=dev)
+        op = _at(out, "out", dev, _F32, (B, H, T))
+        _apart(op, lp, qp, cache.pool)
+        prm = WeighParams(_WEIGH_BYTES, qp, qs, SPEC_BF16 if q.dtype is torch.bfloat16 else SPEC_F16, B, W, Hq, seq, win,
+                          lp, D ** -0.5 if scale is None else scale, wp, decay, op, T)
+        rc = lib().spec_weigh_kv(cache, prm, sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_weigh_kv", rc)
+    return out
+
+
+def evict_kv(weights, kv_pool, kv_scales, block_tables, seq_lens, keep: int, *, first: int = 0, recent: int = 0,
+             blocks_held=None, out_lens=None, out_kept=None, out_weights=None, out_free=None, stream=None):
+    """Drops cached positions, head by head, down to `keep` of them: the first
+    `first`, the last `recent` and, between, those of largest weight (weights
+    [B, Hkv, T] float32, weigh_kv; the lowest position among equals) stay and
+    move together, in place.
+
+    Returns (new_lens [B], kept [B, Hkv, keep] int32 with -1 behind a request's
+    end, their weights [B, Hkv, keep], and with blocks_held [B] the whole blocks
+    that are free now, for release_blocks, else None).  out_lens=seq_lens and
+    out_weights=weights update in place.  Rotated keys keep their rotation: new
+    tokens go on from the text's positions (starts in rotate_store_kv), not from
+    new_lens."""
+    cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
+    H, keep = cache.kv_heads, int(keep)
+    _cuda(weights, "weights", ("B", "Hkv", "T"))
+    T = weights.shape[2]
+    if keep < 1 or first < 0 or recent < 0 or first + recent > keep:
+        raise ValueError(f"keep must be at least 1 and first + recent, got {keep}, {first} and {recent}")
+    wp = _at(weights, "weights", dev, _F32, (B, H, T))
+    seq = _at(seq_lens, "seq_lens", dev, _I32, (B,))
+    held = None if blocks_held is None else _at(blocks_held, "blocks_held", dev, _I32, (B,))
+    if held is None and out_free is not None:
+        raise ValueError("out_free goes with blocks_held")
+    sh, ctx = _on_stream(stream, dev)
+    with ctx:
+        if out_lens is None:
+            out_lens = torch.empty((B,), dtype=_I32, device=dev)
+        if out_kept is None:
+            out_kept = torch.empty((B, H, keep), dtype=_I32, device=dev)
+        if out_weights is None:
+            out_weights = torch.zeros((B, H, keep), dtype=_F32, device=dev)
+        if held is not None and out_free is None:
+            out_free = torch.empty((B,), dtype=_I32, device=dev)
+        _cuda(out_weights, "out_weights", ("B", "Hkv", "T_out"))
+        T_out = out_weights.shape[2]
+        if T_out < keep:
+            raise ValueError(f"out_weights must hold {keep} positions, got {T_out}")
+        lp, kp = _at(out_lens, "out_lens", dev, _I32, (B,)), _at(out_kept, "out_kept", dev, _I32, (B, H, keep))
+        op = _at(out_weights, "out_weights", dev, _F32, (B, H, T_out))
+        fp = None if held is None else _at(out_free, "out_free", dev, _I32, (B,))
+        others = (kp, fp, held, cache.pool, cache.scales, cache.block_tables)
+        for w, n in ((wp, seq), (op, seq), (wp, lp), (op, lp)):  # op may be wp, and lp seq
+            _apart(w, n, *others)
+        prm = EvictParams(_EVICT_BYTES, wp, T, B, seq, keep, int(first), int(recent), lp, kp, op, T_out, held, fp)
+        rc = lib().spec_evict_kv(cache, prm, sh)
+    if rc != SPEC_OK:
+        raise SpecError("spec_evict_kv", rc)
+    return out_lens, out_kept, out_weights, out_free
 
 
 def last_error(workspace: Workspace, stream=None) -> int:

@@ -94,11 +94,12 @@ cudaError_t launch_wide(const ChainArgs& a, int dtype, bool vec, cudaStream_t st
 // after that grid has completed and sees all of its writes (stream order is
 // kept; the next call's pass 1 no longer pays a full launch gap).
 template <class Kern, class Arg>
-cudaError_t launch_first(Kern kernel, long grid, int block, cudaStream_t st, const Arg& a) {
+cudaError_t launch_first(Kern kernel, long grid, int block, cudaStream_t st, const Arg& a,
+                         size_t smem = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -15,7 +15,9 @@
 // tokens, 5.7); 64 prompts of 4096 tokens with 8 heads of 128, 276 us, 5.8 TB/s
 // (0.86 of the measured copy rate).  The relocation of 16 requests' paths of 4 takes 3.9 us, of 256
 // requests' paths of 17 7.2 us.
-#include "kvcache.cuh"
+#include <type_traits>
+
+#include "rotary.cuh"
 
 namespace sv {
 
@@ -31,16 +33,13 @@ struct StoreArgs {
   int split;  // CTAs per block of a request's window
 };
 
-template <class T>
-__device__ __forceinline__ float2 unpack2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
-  return make_float2(bf16_lo(w), bf16_hi(w));
-}
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
+// With the window's queries and keys rotated to their positions on the way.
+struct TurnArgs : StoreArgs {
+  RotateArgs r;  // x[0]: the queries; no second kind
+  long first_q;  // CTAs of the store, before those of the queries
+};
+template <int TURN>
+using ArgsOf = typename std::conditional<TURN == 0, StoreArgs, TurnArgs>::type;
 
 // Largest finite magnitude of eight packed elements.
 template <class T>
@@ -78,11 +77,31 @@ constexpr int kStoreThreads = 128;
 // a lane; what a larger block holds beyond that is read again (from L2).  With
 // the CTA per unit 9 CTAs share an SM (56 registers; 80 and 6 without the
 // bound: 333 us instead of 300 with blocks of 64 tokens).
-template <class T, int WARPS, int VECS>
-__global__ void __launch_bounds__(kStoreThreads, WARPS > 1 ? 9 : 0) store_kernel(const StoreArgs a) {
+//
+// TURN (0: as they are, 1: pairs across the halves, 2: interleaved): keys are
+// rotated as they are loaded, and rounded to their type, so that all that
+// follows is the store of what spec_rotate_qk writes.  A unit of few rows takes
+// the angles from a table that its CTA's units share; one of many computes them
+// where it needs them.
+template <class T, int WARPS, int VECS, int TURN>
+__global__ void __launch_bounds__(kStoreThreads, WARPS > 1 && !TURN ? 9 : 0) store_kernel(const ArgsOf<TURN> a) {
   constexpr int kUnits = kStoreThreads / 32 / WARPS, kLanes = 32 * WARPS;
   const KvCache& c = a.c;
   const int groups = (2 * c.H + kUnits - 1) / kUnits;
+  constexpr int kAngles = TURN && WARPS == 1 ? 128 * VECS : 1;  // rows x pairs of a unit: 32 VECS / (D / 8) x D / 2
+  __shared__ float2 sAngle[kAngles];
+  __shared__ uint64_t sTurns[TURN ? 64 : 1];
+  if constexpr (TURN != 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x >= a.first_q) {
+      __shared__ float2 cs[64];
+      const long token = blockIdx.x - a.first_q;
+      const int b = (int)(token / a.W);
+      rotate_token<T, TURN == 2>(a.r, b, (int)(token - (long)b * a.W), cs);
+      return;
+    }
+  }
   int u = blockIdx.x;
   const int group0 = u % a.split;
   u /= a.split;
@@ -102,6 +121,18 @@ __global__ void __launch_bounds__(kStoreThreads, WARPS > 1 ? 9 : 0) store_kernel
   const int i0 = (int)(col * c.tpb + first - seq);        // its window token
   const int rows = min(c.tpb - first, w - i0);
   const int vpr = c.D / 8, shift = c.D == 128 ? 4 : 3;    // vectors per row: 16 or 8
+  if constexpr (TURN != 0) {
+    for (int p = threadIdx.x; p < a.r.pairs; p += kStoreThreads) sTurns[p] = turns_of(a.r.inv_freq[p]);
+    __syncthreads();
+    if (WARPS == 1) {
+      for (int x = threadIdx.x; x < rows * a.r.pairs; x += kStoreThreads) {
+        const int row = x / a.r.pairs;
+        sAngle[x] = angle_at(sTurns[x - row * a.r.pairs],
+                             (long)a.r.starts[b] + depth_of(a.r.masks, a.W, b, i0 + row), a.r.gain);
+      }
+      __syncthreads();
+    }
+  }
 #pragma unroll 1
   for (int group = group0; group < groups; group += a.split) {
     const int unit = group * kUnits + (int)threadIdx.x / kLanes;  // kind * H + h
@@ -110,7 +141,34 @@ __global__ void __launch_bounds__(kStoreThreads, WARPS > 1 ? 9 : 0) store_kernel
     const int nvec = real ? rows * vpr : 0;
     const char* src = a.x[kind] + 2 * (b * a.sb[kind] + i0 * a.st[kind] + h * a.sh[kind]);
     auto vec = [&](int v) {
-      return *reinterpret_cast<const uint4*>(src + 2 * ((v >> shift) * a.st[kind] + (v & (vpr - 1)) * 8));
+      const int row = v >> shift, e = (v & (vpr - 1)) * 8;
+      const char* at = src + 2 * (row * a.st[kind] + e);
+      uint4 x = *reinterpret_cast<const uint4*>(at);
+      if constexpr (TURN != 0) {
+        if (kind == 0 && e < 2 * a.r.pairs) {
+          constexpr int kPairs = TURN == 1 ? 8 : 4;
+          const bool back = TURN == 1 && e >= a.r.pairs;  // the pairs' second elements
+          const int p = TURN == 1 ? (back ? e - a.r.pairs : e) : e / 2;
+          uint4 y = make_uint4(0, 0, 0, 0);
+          if (TURN == 1) y = *reinterpret_cast<const uint4*>(at + 2 * (back ? -a.r.pairs : a.r.pairs));
+          float2 cs[kPairs];
+          if (WARPS == 1) {
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) cs[k] = sAngle[row * a.r.pairs + p + k];
+          } else {
+            const long position = (long)a.r.starts[b] + depth_of(a.r.masks, a.W, b, i0 + row);
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) cs[k] = angle_at(sTurns[p + k], position, a.r.gain);
+          }
+          if (TURN == 2)
+            turn_inside<T>(x, cs);
+          else if (back)
+            turn_across<T, 2>(y, x, cs);
+          else
+            turn_across<T, 1>(x, y, cs);
+        }
+      }
+      return x;
     };
     uint4 keep[VECS];
     float amax = 0.f;
@@ -274,26 +332,61 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const MoveArgs a)
 // 32; with the CTA per unit (64 tokens) it is the other way, 300 and 293.
 constexpr long kStoreMany = 8l * 152 * 8;
 
-template <class T, int WARPS, int VECS>
-int launch_store_as(StoreArgs& a, cudaStream_t st) {
+template <class T, int WARPS, int VECS, int TURN>
+int launch_store_as(ArgsOf<TURN>& a, cudaStream_t st) {
   const long blocks = (long)a.B * a.pages;
   const int groups = ceil_div(2 * a.c.H, kStoreThreads / 32 / WARPS);
   a.split = WARPS == 1 && blocks * groups > kStoreMany ? 1 : groups;
-  if (blocks * a.split > INT_MAX) return SPEC_EINVAL;
-  store_kernel<T, WARPS, VECS><<<(unsigned)(blocks * a.split), kStoreThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+  if constexpr (TURN != 0) {
+    a.first_q = blocks * a.split;
+    const long grid = a.first_q + (a.r.x[0].in ? (long)a.B * a.W : 0);
+    if (grid > INT_MAX) return SPEC_EINVAL;
+    return launch_first(store_kernel<T, WARPS, VECS, TURN>, grid, kStoreThreads, st, a) == cudaSuccess ? SPEC_OK
+                                                                                                       : SPEC_ECUDA;
+  } else {
+    if (blocks * a.split > INT_MAX) return SPEC_EINVAL;
+    store_kernel<T, WARPS, VECS, 0><<<(unsigned)(blocks * a.split), kStoreThreads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+  }
 }
 
 // A warp per unit while a block's new rows fit its registers, else the CTA.
 // (The CTA for all took 814 us with blocks of 16 tokens and 491 with 32; and
 // 105 us for 2048 requests of 4 tokens, now 23.)
-template <class T>
-int launch_store(StoreArgs& a, cudaStream_t st) {
+template <class T, int TURN>
+int launch_store(ArgsOf<TURN>& a, cudaStream_t st) {
   const int vecs = min(a.c.tpb, a.W) * a.c.D / 8;
-  if (vecs <= 32 * 4) return launch_store_as<T, 1, 4>(a, st);
-  if (vecs <= 32 * 8) return launch_store_as<T, 1, 8>(a, st);
-  if (vecs <= 32 * 16) return launch_store_as<T, 1, 16>(a, st);
-  return launch_store_as<T, 4, 8>(a, st);
+  if (vecs <= 32 * 4) return launch_store_as<T, 1, 4, TURN>(a, st);
+  if (vecs <= 32 * 8) return launch_store_as<T, 1, 8, TURN>(a, st);
+  if (vecs <= 32 * 16) return launch_store_as<T, 1, 16, TURN>(a, st);
+  return launch_store_as<T, 4, 8, TURN>(a, st);
+}
+
+// Host check of the store's arguments; fills `a`.
+int store_setup(const spec_kv_cache* cache, const void* k, const int64_t* k_strides, const void* v,
+                const int64_t* v_strides, int dtype, const int32_t* seq_lens, const int32_t* window_lens, int B,
+                int W, StoreArgs* a) {
+  const int rc = kv_setup(cache, &a->c);
+  if (rc != SPEC_OK) return rc;
+  if (!kv_strides_ok(k, k_strides) || !kv_strides_ok(v, v_strides) || !seq_lens ||
+      (dtype != SPEC_BF16 && dtype != SPEC_F16) || B < 1 || B > SPEC_MAX_BATCH || W < 1 ||
+      W > SPEC_MAX_WINDOW)
+    return SPEC_EINVAL;
+  const void* x[2] = {k, v};
+  const int64_t* st[2] = {k_strides, v_strides};
+  for (int i = 0; i < 2; ++i) {
+    a->x[i] = static_cast<const char*>(x[i]);
+    a->sb[i] = st[i][0];
+    a->st[i] = st[i][1];
+    a->sh[i] = st[i][2];
+  }
+  a->seq = seq_lens;
+  a->win = window_lens;
+  a->B = B;
+  a->W = W;
+  // blocks a window can touch; at most the whole table row
+  a->pages = min((W - 2 + a->c.tpb) / a->c.tpb + 1, a->c.max_blocks);
+  return SPEC_OK;
 }
 
 }  // namespace
@@ -308,28 +401,25 @@ int spec_store_kv(const spec_kv_cache* cache, const void* k, const int64_t* k_st
                   const void* v, const int64_t* v_strides, int dtype, const int32_t* seq_lens,
                   const int32_t* window_lens, int B, int W, spec_stream_t stream) {
   StoreArgs a{};
-  const int rc = kv_setup(cache, &a.c);
+  const int rc = store_setup(cache, k, k_strides, v, v_strides, dtype, seq_lens, window_lens, B, W, &a);
   if (rc != SPEC_OK) return rc;
-  if (!kv_strides_ok(k, k_strides) || !kv_strides_ok(v, v_strides) || !seq_lens ||
-      (dtype != SPEC_BF16 && dtype != SPEC_F16) || B < 1 || B > SPEC_MAX_BATCH || W < 1 ||
-      W > SPEC_MAX_WINDOW)
-    return SPEC_EINVAL;
-  const void* x[2] = {k, v};
-  const int64_t* st[2] = {k_strides, v_strides};
-  for (int i = 0; i < 2; ++i) {
-    a.x[i] = static_cast<const char*>(x[i]);
-    a.sb[i] = st[i][0];
-    a.st[i] = st[i][1];
-    a.sh[i] = st[i][2];
-  }
-  a.seq = seq_lens;
-  a.win = window_lens;
-  a.B = B;
-  a.W = W;
-  // blocks a window can touch; at most the whole table row
-  a.pages = min((W - 2 + a.c.tpb) / a.c.tpb + 1, a.c.max_blocks);
-  return dtype == SPEC_BF16 ? launch_store<__nv_bfloat16>(a, (cudaStream_t)stream)
-                            : launch_store<__half>(a, (cudaStream_t)stream);
+  return dtype == SPEC_BF16 ? launch_store<__nv_bfloat16, 0>(a, (cudaStream_t)stream)
+                            : launch_store<__half, 0>(a, (cudaStream_t)stream);
+}
+
+int spec_rotate_store_kv(const spec_kv_cache* cache, const spec_rotate_params* p, const void* v,
+                         const int64_t* v_strides, const int32_t* seq_lens, spec_stream_t stream) {
+  TurnArgs a{};
+  int rc = rotate_setup(p, &a.r);
+  if (rc != SPEC_OK) return rc;
+  rc = store_setup(cache, p->k, p->k_strides, v, v_strides, p->dtype, seq_lens, p->window_lens, p->B, p->W, &a);
+  if (rc != SPEC_OK) return rc;
+  if (p->out_k || !p->q != !p->out_q || p->k_heads != a.c.H || p->head_dim != a.c.D) return SPEC_EINVAL;
+  a.r.x[1].heads = 0;  // the keys go into the cache
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (p->dtype == SPEC_BF16)
+    return p->interleaved ? launch_store<__nv_bfloat16, 2>(a, st) : launch_store<__nv_bfloat16, 1>(a, st);
+  return p->interleaved ? launch_store<__half, 2>(a, st) : launch_store<__half, 1>(a, st);
 }
 
 int spec_relocate_quantised_kv(const spec_kv_cache* cache, const int32_t* base_lens,

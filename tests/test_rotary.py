@@ -1,0 +1,335 @@
+"""Rotary positions of a window's queries and keys, alone and on the way into
+the cache: oracle pins and refusals on the CPU, the CUDA calls against the
+oracle on the GPU.
+
+Tolerance of a rotated element gain (a cos - b sin): the angle is off by at
+most 2^-30 turns from its reduction, 2^-32 from cutting it to 32 bits and
+2^-25 half turns from its rounding to fp32, 2^-23 radians in all; sine and
+cosine are rounded by CUDA's sincospif to 2 ulp, 2^-23; the gain and three
+operations round by 2^-24 each.  In all at most 2^-21 gain (|a| + |b|), and
+then the type's rounding, eps / 2 of the value."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verification_row_gb300 as sv
+from oracle import kv, window
+from _kv import cache, random_paths, to_bf16, to_f16
+
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+# ------------------------------------------------------------------ CPU
+def test_oracle_turns_exactly_far_out():
+    for p, f in ((1, 1.0), (7, 0.3), (-5, 0.11), (12345, 1e-3)):
+        assert window._turn(p, f) == pytest.approx((math.sin(p * f), math.cos(p * f)), abs=1e-14)
+    # 2^30 radians: 170891318 turns and 5.92...; and additivity, which a lost product would break
+    s, c = window._turn(2**30, 1.0)
+    s1, c1 = window._turn(2**30 - 3, 1.0)
+    assert math.isclose(s, s1 * math.cos(3) + c1 * math.sin(3), abs_tol=1e-15)
+    assert math.isclose(c, c1 * math.cos(3) - s1 * math.sin(3), abs_tol=1e-15)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_oracle_keeps_lengths_and_differences(inter):
+    rng = np.random.default_rng(0)
+    q, k = rng.normal(0, 1, (2, 1, 4, 1, 32))
+    f, _ = sv.rotary_frequencies(16)
+    f = f.numpy()
+
+    def dot(a, b):
+        x = window.rotate(np.repeat(q[:1, :1], 1, 1)[:, :1], np.zeros((1, 1, 1, 32)), [a], f, inter)
+        y = window.rotate(k[:1, :1], np.zeros((1, 1, 1, 32)), [b], f, inter)
+        return float((x * y).sum())
+    assert dot(5, 2) == pytest.approx(dot(1005, 1002), abs=1e-12)  # only the distance counts
+    x = window.rotate(q, np.zeros_like(q), [9], f, inter, gain=1.5)
+    assert np.allclose((x[..., :16] ** 2).sum(-1), 2.25 * (q[..., :16] ** 2).sum(-1))
+    assert np.array_equal(x[..., 16:], q[..., 16:])
+
+
+def test_frequencies():
+    f, gain = sv.rotary_frequencies(8, 10000.0)
+    assert f.dtype == torch.float64 and gain == 1.0
+    assert f.tolist() == pytest.approx([1, 0.1, 0.01, 0.001])
+    assert sv.rotary_frequencies(8, scaling="linear", factor=4)[0].tolist() == pytest.approx([x / 4 for x in f.tolist()])
+    b = sv.rotary_frequencies(8, scaling="base", factor=4)[0]
+    assert b[0] == 1 and b[-1].item() == pytest.approx(0.001 / 4)
+    for name, g in (("ramp", 0.1 * math.log(8) + 1), ("smooth", 1.0)):
+        r, gain = sv.rotary_frequencies(64, scaling=name, factor=8, original_len=4096)
+        f = sv.rotary_frequencies(64)[0]
+        turns = 4096 * f / (2 * math.pi)
+        assert gain == pytest.approx(g)
+        assert torch.equal(r[turns >= 32], f[turns >= 32])
+        assert torch.allclose(r[turns <= 1], f[turns <= 1] / 8, rtol=1e-15)
+        assert ((r <= f) & (r >= f / 8 * (1 - 1e-15))).all()
+    assert sv.rotary_frequencies(8, scaling="linear", factor=1)[0].tolist() == sv.rotary_frequencies(8)[0].tolist()
+    for bad in (dict(rot_dim=7), dict(rot_dim=0), dict(rot_dim=8, base=0.0), dict(rot_dim=8, factor=0.5),
+                dict(rot_dim=8, scaling="dynamic"), dict(rot_dim=8, scaling="ramp"),
+                dict(rot_dim=8, scaling="smooth", original_len=100, fast=1.0, slow=1.0),
+                dict(rot_dim=2, scaling="base", factor=2.0)):
+        with pytest.raises(ValueError):
+            sv.rotary_frequencies(**bad)
+
+
+def _fake(**o):
+    f = 16 * 1024
+    s = (ctypes.c_int64 * 3)(256, 128, 64)
+    a = dict(size=ctypes.sizeof(sv.RotateParams), q=f, k=f, out_q=f, out_k=f, q_strides=s, k_strides=s, out_q_strides=s,
+             out_k_strides=s, dtype=sv.SPEC_BF16, B=2, W=3, q_heads=4, k_heads=2, head_dim=64, starts=f, window_lens=None,
+             masks=None, inv_freq=f, pairs=32, interleaved=0, gain=1.0)
+    a.update(o)
+    return sv.RotateParams(*[a[n] for n, _ in sv.RotateParams._fields_])
+
+
+_ODD = (ctypes.c_int64 * 3)(256, 132, 64)
+_OTHER = (ctypes.c_int64 * 3)(512, 128, 64)
+BAD = [dict(size=8), dict(dtype=sv.SPEC_F32), dict(dtype=9), dict(B=0), dict(B=8193), dict(W=0), dict(W=65537),
+       dict(head_dim=24), dict(head_dim=528), dict(head_dim=0), dict(pairs=0), dict(pairs=12), dict(pairs=40),
+       dict(starts=None), dict(inv_freq=None), dict(gain=math.inf), dict(gain=math.nan), dict(masks=16 * 1024, W=1025),
+       dict(q=None), dict(q_heads=0), dict(k_heads=-1), dict(q_heads=16385), dict(q=16 * 1024 + 8), dict(q_strides=_ODD),
+       dict(out_q=16 * 1024 + 2), dict(out_q_strides=_ODD), dict(out_q_strides=_OTHER)]
+
+
+@pytest.mark.parametrize("bad", BAD, ids=lambda b: ",".join(b))
+def test_refusals_before_any_launch(bad):
+    lib = sv.lib()
+    assert lib.spec_rotate_qk(_fake(**bad), None) == sv.SPEC_EINVAL
+    from test_kv_store import _fake_cache
+    s3 = (ctypes.c_int64 * 3)(128, 128, 64)
+    f = 16 * 1024
+    if "out_q_strides" not in bad:
+        assert lib.spec_rotate_store_kv(_fake_cache(), _fake(out_k=None, **bad), f, s3, f, None) == sv.SPEC_EINVAL
+
+
+def test_refusals_of_each_call():
+    from test_kv_store import BAD_CACHES, _fake_cache
+    lib, f = sv.lib(), 16 * 1024
+    s3, odd = (ctypes.c_int64 * 3)(128, 128, 64), (ctypes.c_int64 * 3)(128, 132, 64)
+    assert lib.spec_rotate_qk(None, None) == sv.SPEC_EINVAL
+    for bad in (dict(out_q=None), dict(out_k=None), dict(q=None, q_heads=0, k=None, k_heads=0, out_q=None, out_k=None),
+                dict(q=None, q_heads=0)):
+        assert lib.spec_rotate_qk(_fake(**bad), None) == sv.SPEC_EINVAL, bad
+
+    def store(c=None, p=None, v=f, vs=s3, seq=f):
+        return lib.spec_rotate_store_kv(c or _fake_cache(), p or _fake(out_k=None), v, vs, seq, None)
+    for bad in BAD_CACHES:
+        assert store(c=_fake_cache(**bad)) == sv.SPEC_EINVAL, bad
+    for bad in (dict(), dict(out_k=None, k_heads=3), dict(out_k=None, head_dim=128), dict(out_k=None, out_q=None),
+                dict(out_k=None, k=None, k_heads=0)):
+        assert store(p=_fake(**bad)) == sv.SPEC_EINVAL, bad
+    assert store(v=None) == store(vs=odd) == store(v=f + 4) == store(seq=None) == sv.SPEC_EINVAL
+    assert lib.spec_rotate_store_kv(None, _fake(out_k=None), f, s3, f, None) == sv.SPEC_EINVAL
+
+
+# ------------------------------------------------------------------ GPU
+def _i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+def _qkv(rng, B, W, Hq, H, D, dtype, pad=0):
+    """Slices of one row per token, as a fused projection leaves them."""
+    x = torch.from_numpy(rng.normal(0, 1, (B, W, Hq + 2 * H, D + pad))).to(TYPES[dtype]).cuda()[..., :D]
+    return x[:, :, :Hq], x[:, :, Hq:Hq + H], x[:, :, Hq + H:]
+
+
+def _close(got, x, want, rot, gain, inter, dtype):
+    x = np.abs(x)
+    half = rot // 2
+    bound = np.zeros_like(x)
+    if inter:
+        s = x[..., 0:rot:2] + x[..., 1:rot:2]
+        bound[..., 0:rot:2] = bound[..., 1:rot:2] = s
+    else:
+        s = x[..., :half] + x[..., half:rot]
+        bound[..., :half] = bound[..., half:rot] = s
+    eps = torch.finfo(TYPES[dtype])
+    tol = 2.0 ** -21 * abs(gain) * bound + np.maximum(eps.eps / 2 * np.abs(want), eps.smallest_normal * eps.eps)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), (err - tol).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,W,Hq,H,D,rot,inter", [(1, 1, 1, 1, 16, 16, False), (2, 3, 8, 2, 64, 64, False),
+                                                  (2, 3, 8, 2, 64, 64, True), (3, 5, 5, 1, 128, 32, False),
+                                                  (3, 5, 5, 1, 128, 112, True), (1, 9, 40, 8, 128, 128, False),
+                                                  (1, 2, 3, 3, 512, 512, False), (1, 2, 3, 3, 512, 496, True),
+                                                  (2, 2, 4, 2, 80, 16, False), (1, 40, 2, 1, 192, 64, True)])
+def test_rotate_matches_oracle(dtype, B, W, Hq, H, D, rot, inter):
+    rng = np.random.default_rng(D + rot)
+    q, k, _ = _qkv(rng, B, W, Hq, H, D, dtype)
+    starts = rng.integers(0, 131072, B)
+    starts[0] = 2**30 if rot > 32 else -77
+    f, gain = sv.rotary_frequencies(rot, scaling="ramp", factor=8, original_len=4096, device="cuda")
+    oq, ok = sv.rotate_qk(q, k, _i32(starts), f, interleaved=inter, gain=gain)
+    for x, y in ((q, oq), (k, ok)):
+        x = x.double().cpu().numpy()
+        want = window.rotate(x, np.zeros_like(x), starts, f.cpu().numpy(), inter, gain)
+        _close(y.double().cpu().numpy(), x, want, rot, gain, inter, dtype)
+
+
+@pytest.mark.gpu
+def test_frequencies_of_any_size():
+    rng = np.random.default_rng(1)
+    q, _, _ = _qkv(rng, 4, 3, 2, 1, 64, "f16")
+    f = np.array([0.0, 1.0, -1.0, 2.0**32, 1e-12, -3e-5, 6.283185307179586, 2.0**-64, 1e-300, 3.5, 1e4, -2.0**31, 0.5,
+                  2.0**-33, 7.7e-9, 1e-7] * 2)
+    starts = np.array([2**31 - 3, -2**31, 123456789, 0])
+    got, none = sv.rotate_qk(q, None, _i32(starts), torch.from_numpy(f).cuda())
+    x = q.double().cpu().numpy()
+    # 2^32 radians a position at 2^31: 2^63 radians, whose reduction by 1 / (2 pi) in 64 bits is off by 2^-3 turns and more:
+    # the bound of the header holds while position * inv_freq stays below 2^34
+    want = window.rotate(x, np.zeros_like(x), starts, f)
+    sure = np.abs(f) <= 8
+    keep = np.concatenate([sure, sure])
+    a, b, w = (z[..., keep] for z in (got.double().cpu().numpy(), x, want))
+    _close(a, b, w, int(keep.sum()), 1.0, False, "f16")
+    assert none is None and torch.isfinite(got).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_windows_trees_strides_and_in_place(inter):
+    rng = np.random.default_rng(2)
+    B, W, Hq, H, D, rot = 3, 37, 4, 2, 64, 48
+    q, k, _ = _qkv(rng, B, W, Hq, H, D, "bf16", pad=8)
+    paths = np.stack([random_paths(rng, W - 4, W, 7) for _ in range(B)])  # the last nodes are on no path
+    masks = kv.tree_masks(paths, W)
+    lens, starts = np.array([W, 0, 20]), np.array([5, 6, 70000])
+    f, _ = sv.rotary_frequencies(rot, device="cuda")
+    for m in (None, masks):
+        md = None if m is None else _i32(m)
+        oq, ok = sv.rotate_qk(q, k, _i32(starts), f, interleaved=inter, window_lens=_i32(lens), masks=md)
+        for x, y in ((q, oq), (k, ok)):
+            x = x.double().cpu().numpy()
+            want = window.rotate(x, np.zeros_like(x), starts, f.cpu().numpy(), inter, 1.0, lens, m)
+            _close(y.double().cpu().numpy(), x, want, rot, 1.0, inter, "bf16")
+            assert not y[1].any() and not y[2, 20:].any()
+        # in place, on strided slices: the same bits, and nothing else written
+        whole = torch.cat([q, k], 2).clone()
+        a, b = whole[:, :, :Hq], whole[:, :, Hq:]
+        old = whole.clone()
+        ra, rb = sv.rotate_qk(a, b, _i32(starts), f, interleaved=inter, window_lens=_i32(lens), masks=md, out_q=a, out_k=b)
+        assert ra is a and rb is b
+        for x, y, z in ((a, oq, old[:, :, :Hq]), (b, ok, old[:, :, Hq:])):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[2, :20], y[2, :20])
+            assert torch.equal(x[1], z[1]) and torch.equal(x[2, 20:], z[2, 20:])
+        k2 = sv.rotate_qk(None, k, _i32(starts), f, interleaved=inter, window_lens=_i32(lens), masks=md)
+        assert k2[0] is None and torch.equal(k2[1], ok)
+    bad = sv.rotate_qk(q, k, _i32(starts), f, window_lens=_i32([-1, W + 1, 1]))[0]
+    assert not bad[:2].any() and bad[2, 0].any()
+
+
+STORE = [(1, 1, 1, 1, 64, 16), (2, 5, 8, 2, 128, 16), (3, 40, 4, 2, 64, 32), (2, 33, 2, 1, 128, 32), (2, 200, 4, 4, 64, 64),
+         (1, 150, 4, 2, 128, 64), (2, 130, 2, 1, 128, 48), (1, 1100, 2, 1, 64, 1024), (5, 8, 32, 8, 128, 1024),
+         (2, 70, 3, 3, 64, 80), (300, 4, 2, 8, 64, 16)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,W,Hq,H,D,tpb", STORE)
+@pytest.mark.parametrize("inter,rot", [(False, 1.0), (True, 1.0), (False, 0.25), (True, 0.75)])
+def test_rotating_store_is_the_two_calls(dtype, B, W, Hq, H, D, tpb, inter, rot):
+    rng = np.random.default_rng(W + D)
+    lens = rng.integers(0, 3 * tpb, B)
+    wins = rng.integers(0, W + 1, B)
+    wins[0] = W
+    pool, scales, tables = cache(rng, lens + W, H, D, tpb)
+    if B > 2:
+        tables[1, 0] = -1  # what a bad table leaves out is left out by both
+        lens[2] = -1
+    pool, scales, tables = torch.from_numpy(pool).cuda(), torch.from_numpy(scales).cuda(), _i32(tables)
+    q, k, v = _qkv(rng, B, W, Hq, H, D, dtype)
+    f, gain = sv.rotary_frequencies(int(rot * D), scaling="ramp", factor=4, original_len=2048, device="cuda")
+    starts = _i32(rng.integers(0, 200000, B))
+    masks = None
+    if W <= 40 and B < 100:
+        masks = _i32(kv.tree_masks(np.stack([random_paths(rng, W, W, 9) for _ in range(B)]), W))
+    for win, m in ((_i32(wins), None), (None, masks)):
+        args = dict(interleaved=inter, gain=gain, window_lens=win, masks=m)
+        p2, s2 = pool.clone(), scales.clone()
+        q2, k2 = sv.rotate_qk(q, k, starts, f, **args)
+        sv.store_kv(k2, v, p2, s2, tables, _i32(lens), window_lens=win)
+        p1, s1 = pool.clone(), scales.clone()
+        q1 = sv.rotate_store_kv(q, k, v, f, p1, s1, tables, _i32(lens), starts=starts, **args)
+        assert torch.equal(q1, q2) and torch.equal(p1, p2) and torch.equal(s1, s2)
+
+
+@pytest.mark.gpu
+def test_rotating_store_starts_at_the_cursor():
+    rng = np.random.default_rng(4)
+    pool, scales, tables = (torch.from_numpy(x).cuda() for x in cache(rng, [30, 61], 2, 64, 16))
+    q, k, v = _qkv(rng, 2, 4, 4, 2, 64, "bf16")
+    f, _ = sv.rotary_frequencies(64, device="cuda")
+    seq = _i32([20, 50])
+    a = sv.rotate_store_kv(q, k, v, f, pool, scales, tables, seq)
+    assert torch.equal(a, sv.rotate_qk(q, None, seq, f)[0])
+    inplace = q.clone()
+    assert sv.rotate_store_kv(inplace, k, v, f, pool, scales, tables, seq, out_q=inplace) is inplace
+    assert torch.equal(inplace, a)
+
+
+@pytest.mark.gpu
+def test_largest_windows():
+    rng = np.random.default_rng(5)
+    W = sv.SPEC_MAX_WINDOW
+    q, k, _ = _qkv(rng, 1, W, 1, 1, 64, "bf16")
+    f, _ = sv.rotary_frequencies(64, device="cuda")
+    oq, _ = sv.rotate_qk(q, k, _i32([1000]), f)
+    for i in (0, 1, 40000, W - 1):
+        one = sv.rotate_qk(q[:, i:i + 1], None, _i32([1000 + i]), f)[0]
+        assert torch.equal(one, oq[:, i:i + 1])
+
+
+@pytest.mark.gpu
+def test_binding_refusals():
+    rng = np.random.default_rng(6)
+    q, k, v = _qkv(rng, 2, 3, 4, 2, 64, "bf16")
+    f, _ = sv.rotary_frequencies(64, device="cuda")
+    s = _i32([0, 1])
+
+    def call(q=q, k=k, s=s, f=f, **kw):
+        return sv.rotate_qk(q, k, s, f, **kw)
+    for bad in (dict(f=f.float()), dict(f=f[:12]), dict(f=torch.cat([f, f])), dict(f=f.cpu()), dict(s=s.long()),
+                dict(s=s[:1]), dict(q=q.float()), dict(k=k.half()), dict(k=k[:, :2]), dict(q=q[..., 1:49]),
+                dict(q=None, k=None), dict(q=None, out_q=q), dict(out_q=k), dict(out_q=q.half()),
+                dict(out_k=q[:, :, :2], out_q=q), dict(window_lens=s.float()),
+                dict(masks=torch.zeros((2, 3, 2), dtype=torch.int32, device="cuda")), dict(q=q.cpu())):
+        with pytest.raises(ValueError):
+            call(**bad)
+    pool, scales, tables = (torch.from_numpy(x).cuda() for x in cache(rng, [30, 61], 2, 64, 16))
+
+    def store(q=q, k=k, v=v, f=f, **kw):
+        return sv.rotate_store_kv(q, k, v, f, pool, scales, tables, s, **kw)
+    for bad in (dict(v=v.half()), dict(v=v[:, :2]), dict(k=q), dict(f=f[:4]), dict(out_q=q[:, :2]), dict(q=q[:1]),
+                dict(starts=s[:1])):
+        with pytest.raises(ValueError):
+            store(**bad)
+    with pytest.raises((ValueError, sv.SpecError)):
+        call(gain=math.nan)
+
+
+@pytest.mark.gpu
+def test_store_rounds_like_the_oracle():
+    """The whole path against the oracle: rotation, the keys' type, the cache's codes."""
+    rng = np.random.default_rng(8)
+    for dtype, rnd in (("bf16", to_bf16), ("f16", to_f16)):
+        pool, scales, tables = cache(rng, [60, 45], 2, 64, 16)
+        q, k, v = _qkv(rng, 2, 20, 2, 2, 64, dtype)
+        f, _ = sv.rotary_frequencies(64, device="cuda")
+        seq, starts = np.array([40, 25]), np.array([4000, 25])
+        p, s = torch.from_numpy(pool).cuda(), torch.from_numpy(scales).cuda()
+        sv.rotate_store_kv(q, k, v, f, p, s, _i32(tables), _i32(seq), starts=_i32(starts))
+        kr = rnd(window.rotate(k.double().cpu().numpy(), np.zeros(k.shape), starts, f.cpu().numpy()))
+        wp, ws = kv.store(kr, v.double().cpu().numpy(), pool, scales, tables, seq)
+        got, want = (kv.decode(a) * b[..., None, None] for a, b in
+                     ((p.cpu().numpy(), s.cpu().numpy().astype(np.float64)), (wp, ws)))
+        live = np.isfinite(want)
+        assert np.array_equal(live, np.isfinite(got))
+        # a key rounded the other way in its type is at most one e4m3 step off: 2^-3 of it, or 2^-9 of the scale
+        step = np.maximum(2.0 ** -3 * np.abs(want), 2.0 ** -9 * np.broadcast_to(ws[..., None, None], want.shape))
+        assert (np.abs(got - want)[live] <= step[live]).all()
+        assert (got == want)[live].mean() > 0.99
