@@ -1,14 +1,15 @@
 // Penalties, biases and grammar masks on the logits of a window's rows
 // (spec_adjust_logits).
 //
-// One pass over the logits.  A CTA takes a segment of one request's
-// vocabulary and a run of its rows: it counts the request's tokens that fall
-// into the segment in shared memory (the history is read again for every
-// segment: some KB from L2 beside the segment's rows, and no counts to keep,
-// clear or roll back between calls), and marks in a bitmap every token that
-// some row changes.  A vector of logits without a mark and without a banned
-// token is copied, or in place not read at all; one whose tokens are all
-// banned is not read either.
+// A CTA takes a segment of one request's vocabulary and a run of its rows.  It
+// counts the request's tokens that fall into the segment in shared memory (the
+// history is read again for every segment: some KB from L2 beside the
+// segment's rows, and no counts to keep, clear or roll back between calls) and
+// lists the tokens that change; meanwhile its other half copies the rows as
+// 16-byte vectors (in place: touches them only where a grammar bans something).
+// Then the listed tokens of every row, one by one, over what was copied.  (One
+// pass that looked for them in every vector was bound by instructions: 149 us
+// for 64 x 8 rows of 128256; counting before copying took 90.)
 #include <cuda_bf16.h>
 
 #include "kernels.cuh"
@@ -42,90 +43,92 @@ struct AdjustArgs {
 };
 
 constexpr int kSeg = 4096;  // tokens of a segment
-// A token's word: it stands in the prompt, in the window, and its times in the output.
-constexpr uint32_t kPrompt = 1u << 31, kDraft = 1u << 30;
+constexpr int kBuilders = kThreads / 2;  // threads that count; the others begin with the rows
+// A token's word: it stands in the prompt, in the window, it has a bias; and its times in the output.
+constexpr uint32_t kPrompt = 1u << 31, kDraft = 1u << 30, kBiased = 1u << 29, kTimes = kBiased - 1;
 
-// Eight bits from bit t (above -8) of n words; clear outside them.
+// Eight bits from bit t on of n words; clear behind them.
 __device__ __forceinline__ uint32_t bits8(const int32_t* words, int n, int t) {
-  if (t < 0) return n > 0 ? (uint32_t)words[0] << -t & 255u : 0u;
   const int w = t >> 5;
-  const uint32_t lo = w < n ? (uint32_t)words[w] : 0u;
+  const uint32_t lo = (uint32_t)words[w];
   const uint32_t hi = (t & 31) > 24 && w + 1 < n ? (uint32_t)words[w + 1] : 0u;
   return __funnelshift_r(lo, hi, t & 31) & 255u;
 }
 
-__device__ __forceinline__ uint32_t to_bf16(float x) {
-  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-
 // DT: SPEC_F32 or SPEC_BF16.  VEC: 16-byte vectors (the rows of in and out lie
 // alike in them, wherever they begin), else single elements.  SAME: in place.
-template <int DT, bool VEC, bool SAME>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
+// BAN: there are grammars.
+template <int DT, bool VEC, bool SAME, bool BAN>
+__global__ void __launch_bounds__(kThreads, 6) adjust_kernel(const AdjustArgs a) {
   using Vec = Io<DT, VEC>;
   constexpr int E = Vec::EPV, ES = Vec::ES;
-  constexpr int U = kSeg / kThreads / E < 4 ? kSeg / kThreads / E : 4;  // vectors in flight per thread
+  constexpr int U = 4;  // vectors in flight per thread
   constexpr uint32_t kAll = (1u << E) - 1;
   extern __shared__ uint32_t smem[];
-  __shared__ int32_t sMark[kSeg / 32];
-  __shared__ uint32_t sDraft[SPEC_MAX_TREE_NODES];  // window tokens of the segment: number << 16 | place
-  __shared__ int sDrafts;
-  uint32_t* count = smem;  // [kSeg] where tokens are counted
-  const bool counts = a.tokens || a.drafts;
-  float* bias = reinterpret_cast<float*>(smem + (counts ? kSeg : 0));  // [kSeg] where there are biases
-  const int tid = threadIdx.x;
+  __shared__ int sListed, sDrafts, sBiased, sNext;
+  int* masked = reinterpret_cast<int*>(smem);                   // rows' grammars
+  uint32_t* count = smem + (BAN ? (a.rows + 3) & ~3 : 0);       // [kSeg] tokens' words
+  uint32_t* draft = count + kSeg;                               // the window's: number << 16 | place
+  uint32_t* biased = draft + (a.drafts ? a.M : 0);              // biased places
+  float* bias = reinterpret_cast<float*>(biased + a.bias);      // and their biases
+  uint16_t* list = reinterpret_cast<uint16_t*>(bias + a.bias);  // places whose word is not 0
+  const int tid = threadIdx.x, lane = tid & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int u = blockIdx.x;
   const int seg = u % a.segs;
   u /= a.segs;
   const int b = u / a.splits, r0 = u % a.splits * a.rows;
-  int r1 = min(a.R, r0 + a.rows);
+  int rows = min(a.rows, a.R - r0);
   if (a.draft_lens) {
     const int kb = a.draft_lens[b];
     if (kb < 0 || kb >= a.R) return;
-    r1 = min(r1, kb + 1);
+    rows = min(rows, kb + 1 - r0);
   }
-  if (r0 >= r1) return;
+  if (rows <= 0) return;
   const int s0 = seg * kSeg, len = min(kSeg, a.V - s0);
-
-  // ---- what the segment's rows change
-  for (int i = tid; i < kSeg / 32; i += kThreads) sMark[i] = 0;
-  if (tid == 0) sDrafts = 0;
-  if (counts)
-    for (int i = tid; i < kSeg / 4; i += kThreads) reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
+  const size_t row0 = (size_t)b * a.R + r0;
+  const int words = (a.V + 31) >> 5;
+  const bool changes = a.tokens || a.drafts || a.bias;
+  if (tid == 0) sListed = sDrafts = sBiased = sNext = 0;
+  if (BAN)
+    for (int r = tid; r < rows; r += kThreads) masked[r] = a.allowed_rows ? a.allowed_rows[row0 + r] : (int)(row0 + r);
   __syncthreads();
-  auto mark = [&](int o) { atomicOr(&sMark[o >> 5], (int)(1u << (o & 31))); };
-  if (a.tokens) {
-    const int n = a.token_lens ? min(max(a.token_lens[b], 0), a.T) : a.T;
-    const int p = a.prompt_lens ? min(max(a.prompt_lens[b], 0), n) : 0;
-    const int32_t* tokens = a.tokens + (size_t)b * a.T;
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) {
-      const int o = tokens[i] - s0;
-      if (tokens[i] >= 0 && (unsigned)o < (unsigned)len) {
-        if (i < p)
-          atomicOr(&count[o], kPrompt);
-        else
-          atomicAdd(&count[o], 1u);
-        mark(o);
+
+  // ---- the tokens that change
+  if (changes && tid < kBuilders) {
+    for (int i = tid; i < kSeg / 4; i += kBuilders) reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(kBuilders) : "memory");
+    auto enlist = [&](int o, uint32_t before) {
+      if (before == 0) list[atomicAdd(&sListed, 1)] = (uint16_t)o;
+    };
+    if (a.tokens) {
+      const int n = a.token_lens ? min(max(a.token_lens[b], 0), a.T) : a.T;
+      const int p = a.prompt_lens ? min(max(a.prompt_lens[b], 0), n) : 0;
+      const int32_t* tokens = a.tokens + (size_t)b * a.T;
+      constexpr int N = 16;  // loads in flight: the atomics below keep the compiler from gathering them
+      for (int i0 = tid; i0 < n; i0 += kBuilders * N) {
+        int t[N];
+#pragma unroll
+        for (int y = 0; y < N; ++y) t[y] = i0 + y * kBuilders < n ? tokens[i0 + y * kBuilders] : -1;
+#pragma unroll
+        for (int y = 0; y < N; ++y) {
+          const int o = t[y] - s0;
+          if (t[y] >= 0 && (unsigned)o < (unsigned)len)
+            enlist(o, i0 + y * kBuilders < p ? atomicOr(&count[o], kPrompt) : atomicAdd(&count[o], 1u));
+        }
       }
     }
-  }
-  if (a.drafts)
-    for (int m = tid; m < a.M; m += kThreads) {
-      const int t = a.drafts[(size_t)b * a.M + m], o = t - s0;
-      if (t >= 0 && (unsigned)o < (unsigned)len) {
-        atomicOr(&count[o], kDraft);
-        sDraft[atomicAdd(&sDrafts, 1)] = (uint32_t)m << 16 | (uint32_t)o;
-        mark(o);
+    if (a.drafts)
+      for (int m = tid; m < a.M; m += kBuilders) {
+        const int t = a.drafts[(size_t)b * a.M + m], o = t - s0;
+        if (t >= 0 && (unsigned)o < (unsigned)len) {
+          draft[atomicAdd(&sDrafts, 1)] = (uint32_t)m << 16 | (uint32_t)o;
+          enlist(o, atomicOr(&count[o], kDraft));
+        }
       }
-    }
-  if (a.bias_ids) {
     const int32_t* ids = a.bias_ids + (size_t)b * a.bias;
-    for (int i = tid; i < kSeg; i += kThreads) bias[i] = 0.f;
-    __syncthreads();
-    for (int i = tid; i < a.bias; i += kThreads) {
+    for (int i = tid; i < a.bias; i += kBuilders) {
       const int t = ids[i], o = t - s0;
       if (t < 0 || (unsigned)o >= (unsigned)len) continue;
       bool first = true;  // the first entry of an id adds up all of them
@@ -134,121 +137,159 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
       float sum = 0.f;
       for (int j = i; j < a.bias; ++j)
         if (ids[j] == t) sum += a.bias_values[(size_t)b * a.bias + j];
-      bias[o] = sum;
-      mark(o);
+      const int at = atomicAdd(&sBiased, 1);
+      biased[at] = (uint32_t)o;
+      bias[at] = sum;
+      enlist(o, atomicOr(&count[o], kBiased));
     }
   }
-  __syncthreads();
+
+  // Tokens t, t + 1, ... that the grammar of row r bans, of the bits in `valid`.
+  auto banned = [&](int r, int t, uint32_t valid) {
+    const int x = masked[r];
+    if (x < 0) return 0u;
+    if (x >= a.num_allowed) return valid;
+    return ~bits8(a.allowed + (size_t)x * words, words, t) & valid;
+  };
+
+  // ---- the rows: whole vectors, 32 U of a row to a warp, and the few elements around them
+  if (!SAME || BAN) {
+    constexpr int kParts = kSeg / E / (32 * U);
+    // The first of the segment's tokens at a vector's beginning, in row r.
+    auto begin = [&](int r) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(a.in) + ((row0 + r) * a.V + s0) * ES;
+      return VEC ? (int)((16 - (at & 15)) & 15) / ES : 0;
+    };
+    for (;;) {
+      int x = 0;
+      if (lane == 0) x = atomicAdd(&sNext, 1);
+      x = __shfl_sync(~0u, x, 0);
+      if (x >= rows * kParts) break;
+      const int r = x / kParts, v0 = x % kParts * (32 * U) + lane, head = begin(r);
+      const int vecs = (len - head) / E;
+      const size_t at = ((row0 + r) * a.V + s0 + head) * ES + (size_t)v0 * (E * ES);
+      const char* in = a.in + at;
+      char* out = a.out + at;
+      uint32_t bans[U];
+#pragma unroll
+      for (int y = 0; y < U; ++y)
+        bans[y] = BAN && v0 + 32 * y < vecs ? banned(r, s0 + head + (v0 + 32 * y) * E, kAll) : 0u;
+      uint32_t w[U][Vec::NW];
+#pragma unroll
+      for (int y = 0; y < U; ++y) {
+        if (v0 + 32 * y >= vecs || (BAN && bans[y] == kAll) || (SAME && bans[y] == 0)) continue;
+        const char* p = in + 32 * y * E * ES;
+        if constexpr (SAME && VEC) {  // not through the read-only path: this kernel writes it
+          const uint4 z = *reinterpret_cast<const uint4*>(p);
+          w[y][0] = z.x, w[y][1] = z.y, w[y][2] = z.z, w[y][3] = z.w;
+        } else {
+          Vec::load(p, 0, w[y]);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < U; ++y) {
+        if (v0 + 32 * y >= vecs || (SAME && bans[y] == 0)) continue;
+        if (BAN && bans[y]) {
+          if constexpr (DT == SPEC_F32) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (bans[y] >> e & 1) w[y][e] = 0xff800000u;
+          } else if constexpr (VEC) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {  // -inf is 0xff80
+              const uint32_t m = (bans[y] >> e & 1 ? 0xffffu : 0u) | (bans[y] >> e & 2 ? 0xffff0000u : 0u);
+              w[y][e / 2] = (w[y][e / 2] & ~m) | (0xff80ff80u & m);
+            }
+          } else {
+            w[y][0] = 0xff800000u;
+          }
+        }
+        char* p = out + 32 * y * E * ES;
+        if constexpr (VEC)
+          *reinterpret_cast<uint4*>(p) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+        else if constexpr (DT == SPEC_BF16)
+          *reinterpret_cast<unsigned short*>(p) = (unsigned short)(w[y][0] >> 16);
+        else
+          *reinterpret_cast<uint32_t*>(p) = w[y][0];
+      }
+    }
+    if (VEC)
+      for (int x = tid; x < rows * 2 * E; x += kThreads) {
+        const int r = x / (2 * E), e = x % (2 * E), head = begin(r);
+        // the first E of a row stand for its head, the others for its tail
+        const int o = e < E ? e : head + max(0, (len - head) / E * E) + e - E;
+        if (e < E ? e >= min(head, len) : o >= len || head >= len) continue;
+        const size_t at = ((row0 + r) * a.V + s0 + o) * ES;
+        const bool ban = BAN && banned(r, s0 + o, 1u);
+        if (SAME && !ban) continue;
+        const float z = ban ? -INFINITY : load_logit<DT>(a.in + at, 0);
+        if (DT == SPEC_BF16)
+          *reinterpret_cast<unsigned short*>(a.out + at) = (unsigned short)(__float_as_uint(z) >> 16);
+        else
+          *reinterpret_cast<float*>(a.out + at) = z;
+      }
+  }
+  if (!changes) return;
+
+  // ---- the listed tokens of every row, over what was written above
   const float rep = a.repetition ? a.repetition[b] : 1.f;
   const float freq = a.frequency ? a.frequency[b] : 0.f;
   const float pres = a.presence ? a.presence[b] : 0.f;
-  const int words = (a.V + 31) >> 5;
-
-  for (int r = r0; r < r1; ++r) {
-    const size_t row = (size_t)b * a.R + r, at = (row * a.V + s0) * ES;
-    const char* in = a.in + at;
-    const int shift = VEC ? (int)(reinterpret_cast<uintptr_t>(in) & 15) / ES : 0;
-    in -= shift * ES;
-    char* out = a.out + at - shift * ES;
-    const int nvec = (len + shift + E - 1) / E;
-    const int32_t* allowed = nullptr;
-    int have = words;  // words of the mask; 0: everything is banned
-    if (a.allowed) {
-      const int x = a.allowed_rows ? a.allowed_rows[row] : (int)row;
-      if (x >= 0) allowed = a.allowed + (x < a.num_allowed ? (size_t)x * words : 0);
-      if (x >= a.num_allowed) have = 0;
+  __syncthreads();
+  const int listed = sListed, all = rows * listed;
+  constexpr int N = 2;  // in flight per thread
+  for (int x0 = tid; x0 < all; x0 += kThreads * N) {
+    float z[N];
+    int o[N];
+    size_t row[N];
+#pragma unroll
+    for (int y = 0; y < N; ++y) {
+      const int x = min(x0 + y * kThreads, all - 1), r = (unsigned)x / (unsigned)listed;
+      o[y] = list[x - r * listed];
+      row[y] = row0 + r;
+      z[y] = load_logit<DT>(a.in + (row[y] * a.V + s0) * ES, o[y]);
     }
-    const int32_t* tree = a.masks ? a.masks + row * ((a.R + 31) >> 5) : nullptr;
-    auto change = [&](float x, int o) {
-      if (counts) {
-        const uint32_t w = count[o];
-        int c = (int)(w & (kDraft - 1));
-        if (w & kDraft)
-          for (int i = 0; i < sDrafts; ++i) {
-            const int m = (int)(sDraft[i] >> 16);
-            if ((int)(sDraft[i] & 0xffffu) == o) c += tree ? m > 0 && tree[m >> 5] >> (m & 31) & 1 : m < r;
-          }
-        if (c > 0 || w & kPrompt) x = x > 0.f ? x / rep : x * rep;
-        if (c > 0) x = x - freq * (float)c - pres;
-      }
-      return a.bias_ids ? x + bias[o] : x;
-    };
-    for (int v0 = tid; v0 < nvec; v0 += kThreads * U) {
-      uint32_t w[U][Vec::NW], marks[U], bans[U], valid[U];
 #pragma unroll
-      for (int y = 0; y < U; ++y) {
-        const int v = v0 + y * kThreads, o = v * E - shift;
-        valid[y] = v < nvec ? kAll : 0u;
-        if (o < 0) valid[y] &= kAll << -o;
-        if (o + E > len) valid[y] &= len > o ? kAll >> (o + E - len) : 0u;
-        marks[y] = bans[y] = 0;
-        if (valid[y]) {
-          marks[y] = bits8(sMark, kSeg / 32, o) & valid[y];
-          if (allowed) bans[y] = ~bits8(allowed, have, s0 + o) & valid[y];
-        }
-        marks[y] &= ~bans[y];
-        const bool all = bans[y] == kAll;
-        if (valid[y] == kAll && !all && (!SAME || (marks[y] | bans[y]))) {
-          if constexpr (SAME && VEC) {  // not through the read-only path: this kernel writes it
-            const uint4 z = *reinterpret_cast<const uint4*>(in + (size_t)v * 16);
-            w[y][0] = z.x, w[y][1] = z.y, w[y][2] = z.z, w[y][3] = z.w;
-          } else if constexpr (SAME) {
-            w[y][0] = __float_as_uint(load_logit<DT>(in, v));
-          } else {
-            Vec::load(in, v, w[y]);
-          }
+    for (int y = 0; y < N; ++y) {
+      if (x0 + y * kThreads >= all) break;
+      if (BAN && banned((int)(row[y] - row0), s0 + o[y], 1u)) continue;
+      const uint32_t w = count[o[y]];
+      int c = (int)(w & kTimes);
+      if (w & kDraft) {
+        const int32_t* tree = a.masks ? a.masks + row[y] * ((a.R + 31) >> 5) : nullptr;
+        const int r = (int)(row[y] - (size_t)b * a.R);
+        for (int i = 0; i < sDrafts; ++i) {
+          const int m = (int)(draft[i] >> 16);
+          if ((int)(draft[i] & 0xffffu) == o[y]) c += tree ? m > 0 && tree[m >> 5] >> (m & 31) & 1 : m < r;
         }
       }
-#pragma unroll
-      for (int y = 0; y < U; ++y) {
-        const int v = v0 + y * kThreads, o = v * E - shift;
-        if (valid[y] == 0 || (SAME && !(marks[y] | bans[y]))) continue;
-        if (valid[y] != kAll) {  // a row's or segment's edge inside a vector
-          for (int e = 0; e < E; ++e) {
-            if (!(valid[y] >> e & 1)) continue;
-            float x = load_logit<DT>(in, v * E + e);
-            if (marks[y] >> e & 1) x = change(x, o + e);
-            if (bans[y] >> e & 1) x = -INFINITY;
-            if (DT == SPEC_BF16)
-              reinterpret_cast<unsigned short*>(out)[v * E + e] = (unsigned short)to_bf16(x);
-            else
-              reinterpret_cast<float*>(out)[v * E + e] = x;
-          }
-          continue;
-        }
-        float x[E];
-        if (marks[y] | bans[y]) {
-          if (bans[y] != kAll) Vec::unpack(w[y], x);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if (marks[y] >> e & 1) x[e] = change(x[e], o + e);
-            if (bans[y] >> e & 1) x[e] = -INFINITY;
-          }
-          if constexpr (DT == SPEC_F32) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) w[y][e] = __float_as_uint(x[e]);
-          } else if constexpr (VEC) {
-#pragma unroll
-            for (int e = 0; e < E; e += 2) w[y][e / 2] = to_bf16(x[e]) | to_bf16(x[e + 1]) << 16;
-          } else {
-            w[y][0] = to_bf16(x[0]) << 16;
-          }
-        }
-        if constexpr (VEC)
-          *reinterpret_cast<uint4*>(out + (size_t)v * 16) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
-        else if constexpr (DT == SPEC_BF16)
-          reinterpret_cast<unsigned short*>(out)[v] = (unsigned short)(w[y][0] >> 16);
-        else
-          reinterpret_cast<uint32_t*>(out)[v] = w[y][0];
+      float x = z[y];
+      if (c > 0 || w & kPrompt) x = x > 0.f ? x / rep : x * rep;
+      if (c > 0) x = x - freq * (float)c - pres;
+      if (w & kBiased) {
+        int i = 0;
+        while ((int)biased[i] != o[y]) ++i;
+        x += bias[i];
       }
+      char* out = a.out + (row[y] * a.V + s0 + o[y]) * ES;
+      if (DT == SPEC_BF16)
+        *reinterpret_cast<__nv_bfloat16*>(out) = __float2bfloat16_rn(x);
+      else
+        *reinterpret_cast<float*>(out) = x;
     }
   }
 }
 
-template <int DT, bool VEC>
-cudaError_t launch(const AdjustArgs& a, long grid, size_t smem, cudaStream_t st) {
-  return a.in == a.out ? launch_first(adjust_kernel<DT, VEC, true>, grid, kThreads, st, a, smem)
-                       : launch_first(adjust_kernel<DT, VEC, false>, grid, kThreads, st, a, smem);
+template <int DT, bool VEC, bool SAME>
+cudaError_t launch_as(const AdjustArgs& a, long grid, size_t smem, cudaStream_t st) {
+  return a.allowed ? launch_first(adjust_kernel<DT, VEC, SAME, true>, grid, kThreads, st, a, smem)
+                   : launch_first(adjust_kernel<DT, VEC, SAME, false>, grid, kThreads, st, a, smem);
+}
+
+template <int DT>
+cudaError_t launch(const AdjustArgs& a, bool vec, long grid, size_t smem, cudaStream_t st) {
+  if (a.in == a.out) return launch_as<DT, true, true>(a, grid, smem, st);
+  return vec ? launch_as<DT, true, false>(a, grid, smem, st) : launch_as<DT, false, false>(a, grid, smem, st);
 }
 
 }  // namespace
@@ -266,7 +307,7 @@ extern "C" int spec_adjust_logits(const spec_adjust_params* p, spec_stream_t str
   const uintptr_t in = reinterpret_cast<uintptr_t>(p->logits), out = reinterpret_cast<uintptr_t>(p->out);
   const size_t bytes = (size_t)p->B * p->R * p->V * es;
   if (in % es || out % es || (in != out && in < out + bytes && out < in + bytes)) return SPEC_EINVAL;
-  if ((p->tokens && (p->T < 1 || p->T >= 1 << 30)) || (p->masks && (!p->draft_tokens || p->draft_lens)) ||
+  if ((p->tokens && (p->T < 1 || p->T >= 1 << 29)) || (p->masks && (!p->draft_tokens || p->draft_lens)) ||
       (p->bias_ids && (!p->bias_values || p->num_bias < 1 || p->num_bias > SPEC_MAX_BIAS)) ||
       (p->allowed && p->num_allowed < 1) || (!p->allowed && p->allowed_rows) ||
       (p->allowed && !p->allowed_rows && p->num_allowed != (long)p->B * p->R))
@@ -292,7 +333,7 @@ extern "C" int spec_adjust_logits(const spec_adjust_params* p, spec_stream_t str
   a.presence = p->presence;
   a.bias_ids = p->bias_ids;
   a.bias_values = p->bias_values;
-  a.bias = p->num_bias;
+  a.bias = p->bias_ids ? p->num_bias : 0;
   a.allowed = p->allowed;
   a.allowed_rows = p->allowed_rows;
   a.num_allowed = p->num_allowed;
@@ -301,13 +342,12 @@ extern "C" int spec_adjust_logits(const spec_adjust_params* p, spec_stream_t str
   a.rows = ceil_div(a.R, min((long)a.R, max(1l, 8l * 152 / units)));
   a.splits = ceil_div(a.R, a.rows);
   if (units * a.splits > INT_MAX) return SPEC_EINVAL;
-  const size_t smem = ((a.tokens || a.drafts ? kSeg : 0) + (a.bias_ids ? kSeg : 0)) * 4;
+  const bool changes = a.tokens || a.drafts || a.bias_ids;
+  const size_t smem = (changes ? kSeg * 6 + ((a.drafts ? a.M : 0) + 2 * a.bias) * 4 : 0) +
+                      (a.allowed ? (a.rows + 3) / 4 * 16 : 0);
   const bool vec = (in - out) % 16 == 0;
   const cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = p->dtype == SPEC_F32
-                            ? (vec ? launch<SPEC_F32, true>(a, units * a.splits, smem, st)
-                                   : launch<SPEC_F32, false>(a, units * a.splits, smem, st))
-                            : (vec ? launch<SPEC_BF16, true>(a, units * a.splits, smem, st)
-                                   : launch<SPEC_BF16, false>(a, units * a.splits, smem, st));
+  const cudaError_t e = p->dtype == SPEC_F32 ? launch<SPEC_F32>(a, vec, units * a.splits, smem, st)
+                                             : launch<SPEC_BF16>(a, vec, units * a.splits, smem, st);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
