@@ -715,7 +715,10 @@ int spec_rotate_store_kv(const spec_kv_cache *cache, const spec_rotate_params *p
  *         at every other position.  A row whose lse is -inf adds nothing.
  * Positions in a block whose id lies outside [0, num_blocks) read NaN; for a
  * request with seq_lens < 0, w_b outside [0, W] or a window past max_blocks
- * blocks nothing is written.  Scores and sums are held in fp32. */
+ * blocks nothing is written.  Scores and sums are held in fp32.
+ *   scratch: spec_weigh_scratch_size(...) bytes, 256-byte aligned, with the
+ *         rules of spec_attend_kv's (which may serve where it is large enough).
+ * Limits: as spec_attend_kv's. */
 typedef struct spec_weigh_params {
     size_t size;
     const void *q;
@@ -731,7 +734,12 @@ typedef struct spec_weigh_params {
     float *out;
     int T;
 } spec_weigh_params;
-int spec_weigh_kv(const spec_kv_cache *cache, const spec_weigh_params *params, spec_stream_t stream);
+int spec_weigh_kv(const spec_kv_cache *cache, const spec_weigh_params *params, void *scratch,
+                  size_t scratch_bytes, spec_stream_t stream);
+
+/* Scratch of spec_weigh_kv for B requests of W window tokens (0 for invalid
+ * sizes). */
+size_t spec_weigh_scratch_size(int B, int W, int q_heads, int kv_heads, int head_dim);
 
 /* Drops cached positions, head by head, down to `keep` of them.
  *   weights [B, kv_heads, T] float32 (spec_weigh_kv).  Of a request with

@@ -65,7 +65,8 @@ SYMBOLS = ("spec_workspace_size", "spec_workspace_init", "spec_verify_chain",
            "spec_workspace_size_filtered", "spec_test_timeout_chain", "spec_test_timeout_greedy",
            "spec_verify_tree_sampled", "spec_reserve_blocks", "spec_release_blocks", "spec_tree_masks",
            "spec_store_kv", "spec_attend_kv", "spec_attend_scratch_size", "spec_relocate_quantised_kv",
-           "spec_adjust_logits", "spec_rotate_qk", "spec_rotate_store_kv", "spec_weigh_kv", "spec_evict_kv")
+           "spec_adjust_logits", "spec_rotate_qk", "spec_rotate_store_kv", "spec_weigh_kv", "spec_weigh_scratch_size",
+           "spec_evict_kv")
 SPEC_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 class ChainParams(ctypes.Structure):
@@ -194,7 +195,9 @@ def _bind(lib):
     lib.spec_adjust_logits.argtypes = [ctypes.POINTER(AdjustParams), P]
     lib.spec_rotate_qk.argtypes = [ctypes.POINTER(RotateParams), P]
     lib.spec_rotate_store_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(RotateParams), P, S3, P, P]
-    lib.spec_weigh_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(WeighParams), P]
+    lib.spec_weigh_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(WeighParams), P, S, P]
+    lib.spec_weigh_scratch_size.argtypes = [I, I, I, I, I]
+    lib.spec_weigh_scratch_size.restype = S
     lib.spec_evict_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(EvictParams), P]
     lib.spec_status_string.argtypes = [I]
     lib.spec_status_string.restype = ctypes.c_char_p
@@ -1041,7 +1044,7 @@ def rotate_store_kv(q, k, v, inv_freq, kv_pool, kv_scales, block_tables, seq_len
 
 
 def weigh_kv(q, lse, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=None, scale: float | None = None,
-             weights=None, decay: float = 1.0, out=None, stream=None):
+             weights=None, decay: float = 1.0, out=None, scratch=None, stream=None):
     """The attention that each cached position drew from a window's rows: q
     [B, W, Hq, D] and lse [B, W, Hq] float32 of attend_kv; returns out
     [B, Hkv, T] float32, decay * weights (before seq_lens[b]; none without
@@ -1052,7 +1055,8 @@ def weigh_kv(q, lse, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=
     with window_lens = num_accepted + 1 after relocate_quantised_kv.  T is that
     of weights or out, else the cache's max_blocks * tokens_per_block; positions
     behind a request's end are left as they are in `out` (zeros in a tensor made
-    here).  out=weights updates in place."""
+    here).  out=weights updates in place.  scratch: a uint8 tensor of
+    spec_weigh_scratch_size bytes; made for the call by default."""
     cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
     _cuda(q, "q", ("B", "W", "Hq", "D"))
     W, Hq, D, H = q.shape[1], q.shape[2], cache.head_dim, cache.kv_heads
@@ -1068,15 +1072,21 @@ def weigh_kv(q, lse, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=
     win = None if window_lens is None else _at(window_lens, "window_lens", dev, _I32, (B,))
     lp = _at(lse, "lse", dev, _F32, (B, W, Hq))
     wp = None if weights is None else _at(weights, "weights", dev, _F32, (B, H, T))
+    need = lib().spec_weigh_scratch_size(B, W, Hq, H, D)
+    if need == 0:
+        raise SpecError("spec_weigh_scratch_size", SPEC_EINVAL)
     sh, ctx = _on_stream(stream, dev)
     with ctx:
         if out is None:
             out = torch.zeros((B, H, T), dtype=_F32, device=dev)
+        if scratch is None:
+            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
         op = _at(out, "out", dev, _F32, (B, H, T))
-        _apart(op, lp, qp, cache.pool)
+        sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
+        _apart(op, lp, qp, cache.pool, sp)
         prm = WeighParams(_WEIGH_BYTES, qp, qs, SPEC_BF16 if q.dtype is torch.bfloat16 else SPEC_F16, B, W, Hq, seq, win,
                           lp, D ** -0.5 if scale is None else scale, wp, decay, op, T)
-        rc = lib().spec_weigh_kv(cache, prm, sh)
+        rc = lib().spec_weigh_kv(cache, prm, sp, scratch.numel(), sh)
     if rc != SPEC_OK:
         raise SpecError("spec_weigh_kv", rc)
     return out

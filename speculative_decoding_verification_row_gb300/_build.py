@@ -21,7 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["api.cu", "chain.cu", "argmax.cu", "noalloc.cu", "relocate.cu", "filter.cu",
            "tree_sampled.cu", "wide.cu", "paging.cu", "kv_store.cu", "attend.cu",
-           "attend_rows.cu", "attend_tiles.cu", "adjust.cu", "rotary.cu", "weigh.cu", "evict.cu"]
+           "attend_rows.cu", "attend_tiles.cu", "adjust.cu", "rotary.cu", "weigh.cu",
+           "weigh_tiles.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
 

@@ -7,7 +7,7 @@
 // over rows needs four shuffles per tile and no atomics.  e4m3 -> bf16 and
 // fp16 is exact, so the products are those of the stored values; a weight is
 // exp of a score less the row's lse, at most 1 but for rounding.
-#include "attend.cuh"
+#include "weigh.cuh"
 
 namespace sv {
 
@@ -44,14 +44,6 @@ constexpr int kWCost = 2;             // cells of a unit besides its tiles
 constexpr int kWLeast = 4;            // cells below which a share is not worth a CTA
 constexpr int kWCtas = 4 * kSms;
 
-struct WeighArgs : AttendArgs {  // what the work division reads, q, and the cache
-  const float* row_lse;
-  const float* old;
-  float scale, decay;
-  float* sum;
-  int T;
-};
-
 __device__ __forceinline__ void mma_k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half*) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -62,19 +54,6 @@ __device__ __forceinline__ void mma_k16(float (&d)[4], const uint32_t (&a)[4], u
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Four e4m3 codes as two pairs of T.
-__device__ __forceinline__ void e4m3x4_to(uint32_t w, uint32_t& lo, uint32_t& hi, __half*) {
-  e4m3x4_to_half(w, lo, hi);
-}
-__device__ __forceinline__ void e4m3x4_to(uint32_t w, uint32_t& lo, uint32_t& hi, __nv_bfloat16*) {
-  uint32_t a, b;
-  e4m3x4_to_half(w, a, b);
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  lo = pack_out(x.x, x.y, (__nv_bfloat16*)nullptr);
-  hi = pack_out(y.x, y.y, (__nv_bfloat16*)nullptr);
 }
 
 template <class T, int D>
@@ -203,22 +182,48 @@ __global__ void __launch_bounds__(kWThreads, 4) weigh_kernel(const WeighArgs a) 
 
 }  // namespace
 
+cudaError_t launch_weigh_rows(const WeighArgs& a, int dtype, cudaStream_t st) {
+  if (a.c.D == 64)
+    return dtype == SPEC_BF16 ? launch_first(weigh_kernel<__nv_bfloat16, 64>, kWCtas, kWThreads, st, a)
+                              : launch_first(weigh_kernel<__half, 64>, kWCtas, kWThreads, st, a);
+  return dtype == SPEC_BF16 ? launch_first(weigh_kernel<__nv_bfloat16, 128>, kWCtas, kWThreads, st, a)
+                            : launch_first(weigh_kernel<__half, 128>, kWCtas, kWThreads, st, a);
+}
+
+namespace {
+
+// Whether this file's kernel serves this many rows per KV head; else weigh_tiles.cu.
+bool few_rows(int W, int G) { return (long)W * G <= 32; }
+
+}  // namespace
+
 }  // namespace sv
 
 using namespace sv;
 
-extern "C" int spec_weigh_kv(const spec_kv_cache* cache, const spec_weigh_params* p, spec_stream_t stream) {
+extern "C" {
+
+size_t spec_weigh_scratch_size(int B, int W, int q_heads, int kv_heads, int head_dim) {
+  if (B < 1 || B > SPEC_MAX_BATCH || W < 1 || W > SPEC_MAX_WINDOW || kv_heads < 1 || kv_heads > 1024 ||
+      q_heads < 1 || q_heads > 16384 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return few_rows(W, q_heads / kv_heads) ? 256 : weigh_tiles_scratch();
+}
+
+int spec_weigh_kv(const spec_kv_cache* cache, const spec_weigh_params* p, void* scratch, size_t scratch_bytes,
+                  spec_stream_t stream) {
   constexpr double kLog2e = 1.4426950408889634073599246810019;
   WeighArgs a{};
   const int rc = kv_setup(cache, &a.c);
   if (rc != SPEC_OK) return rc;
   if (!p || p->size != sizeof(spec_weigh_params) || !kv_strides_ok(p->q, p->q_strides) ||
-      (p->dtype != SPEC_BF16 && p->dtype != SPEC_F16) || p->B < 1 || p->B > SPEC_MAX_BATCH || p->W < 1 ||
-      p->W > SPEC_MAX_WINDOW || p->q_heads < 1 || p->q_heads > 16384 || p->q_heads % a.c.H != 0 ||
-      !p->seq_lens || !p->lse || !p->out || p->T < 1 || !isfinite((float)(p->scale * kLog2e)) ||
-      !isfinite(p->decay) || (long)a.c.max_blocks * a.c.tpb > kMaxPositions ||
-      (long)p->B * p->W * p->q_heads > kMaxRows)
+      (p->dtype != SPEC_BF16 && p->dtype != SPEC_F16) || !p->seq_lens || !p->lse || !p->out || p->T < 1 ||
+      !isfinite((float)(p->scale * kLog2e)) || !isfinite(p->decay) ||
+      (long)a.c.max_blocks * a.c.tpb > kMaxPositions || (long)p->B * p->W * p->q_heads > kMaxRows)
     return SPEC_EINVAL;
+  const size_t need = spec_weigh_scratch_size(p->B, p->W, p->q_heads, a.c.H, a.c.D);
+  if (need == 0) return SPEC_EINVAL;
+  if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256 != 0 || scratch_bytes < need) return SPEC_EWORKSPACE;
   a.q = static_cast<const char*>(p->q);
   a.qb = p->q_strides[0];
   a.qt = p->q_strides[1];
@@ -237,13 +242,9 @@ extern "C" int spec_weigh_kv(const spec_kv_cache* cache, const spec_weigh_params
   a.sum = p->out;
   a.T = p->T;
   const cudaStream_t st = (cudaStream_t)stream;
-  const bool bf = p->dtype == SPEC_BF16;
-  cudaError_t e;
-  if (a.c.D == 64)
-    e = bf ? launch_first(weigh_kernel<__nv_bfloat16, 64>, kWCtas, kWThreads, st, a)
-           : launch_first(weigh_kernel<__half, 64>, kWCtas, kWThreads, st, a);
-  else
-    e = bf ? launch_first(weigh_kernel<__nv_bfloat16, 128>, kWCtas, kWThreads, st, a)
-           : launch_first(weigh_kernel<__half, 128>, kWCtas, kWThreads, st, a);
+  const cudaError_t e = few_rows(a.W, a.G) ? launch_weigh_rows(a, p->dtype, st)
+                                           : launch_weigh_tiles(a, p->dtype, scratch, st);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
+
+}  // extern "C"
