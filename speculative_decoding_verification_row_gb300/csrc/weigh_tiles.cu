@@ -32,7 +32,8 @@ constexpr int kLeast = 4;     // cells below which a share is not worth a CTA
 constexpr int kSumWarps = 8, kKeyWarps = 4, kRowWarp = kSumWarps + kKeyWarps, kRowWarps = 4,
               kMmaWarp = kRowWarp + kRowWarps;
 constexpr int kWThreads = (kMmaWarp + 1) * 32;
-constexpr int kStages = 4;
+constexpr int kStages = 8;
+constexpr int kFly = 4;  // steps of rows under way from L2, besides the one being issued
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kColA = 0, kColD = 256, kCols = 512;  // keys: two buffers of two tiles; scores likewise
 
@@ -342,12 +343,12 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
     const int t = tid - kRowWarp * 32, vec = t % V, row = t / V;
     const uint32_t base = smem_u32(rows_s), at = base + (vec >> 3) * (kWRows * 128) + row * 128;
     uint32_t done = 0;  // steps handed over
-    int real1 = 0, real2 = 0;  // rows that the last step and the one before it have, from their first on
-    auto hand = [&](int real) {  // step `done` has arrived
+    int left[kFly + 1] = {};  // rows that the steps under way have, the oldest first
+    auto hand = [&](int rows) {  // step `done` has arrived
       const int st = done % kStages;
       if (t < kWRows) {
         const float l = sNeg[st][t];
-        const float neg = t < real && l != -INFINITY ? -l : -INFINITY;
+        const float neg = t < rows && l != -INFINITY ? -l : -INFINITY;
         sNeg[st][t] = neg;
         const unsigned none = __ballot_sync(~0u, neg == -INFINITY);
         if (lane == 0) sSome[st][warp - kRowWarp] = none != 0;
@@ -376,20 +377,19 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
           cp4(smem_u32(&sNeg[st][t]), a.row_lse + ((size_t)v.b * a.W + i) * a.Hq + (size_t)v.h * a.G + g, real);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        if (n >= 2) {
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
-          hand(real2);
+#pragma unroll
+        for (int k = 0; k < kFly; ++k) left[k] = left[k + 1];
+        left[kFly] = v.rows - s * kWRows;
+        if (n >= kFly) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kFly) : "memory");
+          hand(left[0]);
         }
-        real2 = real1;
-        real1 = v.rows - s * kWRows;
       }
     }
-    if (n >= 2) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      hand(real2);
-    }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (n >= 1) hand(real1);
+#pragma unroll
+    for (int k = 1; k <= kFly; ++k)
+      if (n + k > kFly) hand(left[k]);
   } else {
     const uint64_t q_desc = smem_desc(smem_u32(rows_s), 16);
     for (; v.next(a); ++seg) {
