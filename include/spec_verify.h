@@ -762,7 +762,9 @@ size_t spec_weigh_scratch_size(int B, int W, int q_heads, int kv_heads, int head
  * seq_lens < 0, more than max_blocks blocks or T positions, or a block id
  * outside [0, num_blocks) among those it has is left untouched: new_lens =
  * seq_lens, its kept rows all -1, free_blocks 0.  Blocks must not be shared
- * between requests, nor stand twice in a request's row. */
+ * between requests, nor stand twice in a request's row.
+ *   scratch: spec_evict_scratch_size(...) bytes, 256-byte aligned, with the
+ *         rules of spec_attend_kv's. */
 typedef struct spec_evict_params {
     size_t size;
     const float *weights;
@@ -777,7 +779,11 @@ typedef struct spec_evict_params {
     const int32_t *blocks_held;  /* [B] or NULL */
     int32_t *free_blocks;        /* [B] or NULL */
 } spec_evict_params;
-int spec_evict_kv(const spec_kv_cache *cache, const spec_evict_params *params, spec_stream_t stream);
+int spec_evict_kv(const spec_kv_cache *cache, const spec_evict_params *params, void *scratch,
+                  size_t scratch_bytes, spec_stream_t stream);
+
+/* Scratch of spec_evict_kv (0 for invalid sizes). */
+size_t spec_evict_scratch_size(int B, int kv_heads, int keep, int tokens_per_block);
 
 /* Synchronise `stream`, read the workspace status word into *status_out
  * (SPEC_OK, SPEC_EBADINDEX or SPEC_ETIMEOUT) and clear it.  Returns SPEC_OK, SPEC_EINVAL or

@@ -66,7 +66,7 @@ SYMBOLS = ("spec_workspace_size", "spec_workspace_init", "spec_verify_chain",
            "spec_verify_tree_sampled", "spec_reserve_blocks", "spec_release_blocks", "spec_tree_masks",
            "spec_store_kv", "spec_attend_kv", "spec_attend_scratch_size", "spec_relocate_quantised_kv",
            "spec_adjust_logits", "spec_rotate_qk", "spec_rotate_store_kv", "spec_weigh_kv", "spec_weigh_scratch_size",
-           "spec_evict_kv")
+           "spec_evict_kv", "spec_evict_scratch_size")
 SPEC_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 class ChainParams(ctypes.Structure):
@@ -198,7 +198,9 @@ def _bind(lib):
     lib.spec_weigh_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(WeighParams), P, S, P]
     lib.spec_weigh_scratch_size.argtypes = [I, I, I, I, I]
     lib.spec_weigh_scratch_size.restype = S
-    lib.spec_evict_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(EvictParams), P]
+    lib.spec_evict_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(EvictParams), P, S, P]
+    lib.spec_evict_scratch_size.argtypes = [I, I, I, I]
+    lib.spec_evict_scratch_size.restype = S
     lib.spec_status_string.argtypes = [I]
     lib.spec_status_string.restype = ctypes.c_char_p
     for f in ("spec_workspace_init", "spec_verify_chain", "spec_verify_greedy", "spec_verify_tree",
@@ -1093,7 +1095,8 @@ def weigh_kv(q, lse, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=
 
 
 def evict_kv(weights, kv_pool, kv_scales, block_tables, seq_lens, keep: int, *, first: int = 0, recent: int = 0,
-             blocks_held=None, out_lens=None, out_kept=None, out_weights=None, out_free=None, stream=None):
+             blocks_held=None, out_lens=None, out_kept=None, out_weights=None, out_free=None, scratch=None,
+             stream=None):
     """Drops cached positions, head by head, down to `keep` of them: the first
     `first`, the last `recent` and, between, those of largest weight (weights
     [B, Hkv, T] float32, weigh_kv; the lowest position among equals) stay and
@@ -1104,7 +1107,8 @@ def evict_kv(weights, kv_pool, kv_scales, block_tables, seq_lens, keep: int, *, 
     that are free now, for release_blocks, else None).  out_lens=seq_lens and
     out_weights=weights update in place.  Rotated keys keep their rotation: new
     tokens go on from the text's positions (starts in rotate_store_kv), not from
-    new_lens."""
+    new_lens.  scratch: a uint8 tensor of spec_evict_scratch_size bytes; made for
+    the call by default."""
     cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
     H, keep = cache.kv_heads, int(keep)
     _cuda(weights, "weights", ("B", "Hkv", "T"))
@@ -1116,6 +1120,9 @@ def evict_kv(weights, kv_pool, kv_scales, block_tables, seq_lens, keep: int, *, 
     held = None if blocks_held is None else _at(blocks_held, "blocks_held", dev, _I32, (B,))
     if held is None and out_free is not None:
         raise ValueError("out_free goes with blocks_held")
+    need = lib().spec_evict_scratch_size(B, H, keep, cache.tokens_per_block)
+    if need == 0:
+        raise SpecError("spec_evict_scratch_size", SPEC_EINVAL)
     sh, ctx = _on_stream(stream, dev)
     with ctx:
         if out_lens is None:
@@ -1133,11 +1140,14 @@ def evict_kv(weights, kv_pool, kv_scales, block_tables, seq_lens, keep: int, *, 
         lp, kp = _at(out_lens, "out_lens", dev, _I32, (B,)), _at(out_kept, "out_kept", dev, _I32, (B, H, keep))
         op = _at(out_weights, "out_weights", dev, _F32, (B, H, T_out))
         fp = None if held is None else _at(out_free, "out_free", dev, _I32, (B,))
-        others = (kp, fp, held, cache.pool, cache.scales, cache.block_tables)
+        if scratch is None:
+            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
+        others = (kp, fp, held, sp, cache.pool, cache.scales, cache.block_tables)
         for w, n in ((wp, seq), (op, seq), (wp, lp), (op, lp)):  # op may be wp, and lp seq
             _apart(w, n, *others)
         prm = EvictParams(_EVICT_BYTES, wp, T, B, seq, keep, int(first), int(recent), lp, kp, op, T_out, held, fp)
-        rc = lib().spec_evict_kv(cache, prm, sh)
+        rc = lib().spec_evict_kv(cache, prm, sp, scratch.numel(), sh)
     if rc != SPEC_OK:
         raise SpecError("spec_evict_kv", rc)
     return out_lens, out_kept, out_weights, out_free

@@ -2,13 +2,15 @@
 // request and KV head, then the kept rows' move.
 //
 // Selection: one CTA finds the weight of the last position kept with a radix
-// selection over the weights' order keys (11, 11 and 10 bits), and writes the
-// kept positions in order in one more pass; equal weights are taken from the
-// front.
+// selection over the weights' order keys (11, 11 and 10 bits), writes the kept
+// positions in order in one more pass, equal weights from the front, and notes
+// for the move where each kept row lies, its block's scale and the new scales.
 //
-// Move: one CTA per request, KV head and kind.  A kept row never moves up, so
-// rows are gathered in order, group by group: all of a group is read before any
-// of it is written, and what is written lies below every row still to be read.
+// Move: CTAs per request, KV head and kind, each with a slice of the rows'
+// bytes (whole rows where there are enough of them to fill the GPU).  A kept
+// row never moves up, so a CTA gathers its slice batch by batch: all of a batch
+// is read before any of it is written, and what is written lies below every
+// row still to be read.
 #include "kvcache.cuh"
 
 namespace sv {
@@ -24,11 +26,22 @@ struct EvictArgs {
   int32_t* kept;
   float* out_weights;
   int32_t* free_blocks;
+  int2* from;       // scratch [B, H, keep]: a kept row's block and place in it
+  float2* had;      // [B, H, keep]: that block's scales of K and V
+  int* now;         // [B, H, pages, 2]: the scales of the blocks written, as bits
+  int pages;        // blocks of `keep` positions
+  unsigned div16;   // x / (tpb / 16) = umulhi(x, div16) for x < 2^26, tpb > 16
+  // Block table column of position t (below 2^30).
+  __device__ __forceinline__ int col(int t) const {
+    return c.tpb == 16 ? t >> 4 : (int)__umulhi((unsigned)t >> 4, div16);
+  }
   int B, T, T_out, keep, first, recent;
 };
 
-constexpr int kPickThreads = 1024;
+constexpr int kPickThreads = 512;
 constexpr int kBins = 2048;
+constexpr int kHeld = 4;   // tiles of kPickThreads kTake weights that stay in registers
+constexpr int kTake = 4;   // runs of 32 positions that a warp takes at a time
 
 // Order key of a weight: NaN below all, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float x) { return x == x ? ord32(x) : 0u; }
@@ -51,7 +64,7 @@ __device__ __forceinline__ uint32_t before_warp(uint32_t mine, uint32_t* sWarp, 
   return upto - mine;
 }
 
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a) {
   __shared__ int sHist[kBins];
   __shared__ uint32_t sWarp[kPickThreads / 32];
   __shared__ int sBin, sAbove;
@@ -80,6 +93,32 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictArgs a) {
   }
   const int lo = a.first, hi = n - a.recent;  // the positions that may go: [lo, hi)
   const int want = a.keep - a.first - a.recent;
+  // The weights, a warp's 32 kTake in a row: those of short requests stay in registers.
+  constexpr int kTile = kPickThreads * kTake;
+  const int mine = warp * kTake * 32 + lane;
+  float x[kHeld][kTake];
+  auto load = [&](float (&v)[kTake], int t0) {
+#pragma unroll
+    for (int y = 0; y < kTake; ++y) {
+      const int t = t0 + mine + y * 32;
+      v[y] = t < n ? w[t] : 0.f;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) load(x[i], i * kTile);
+  // f(weights, first position of the tile) in order
+  auto tiles = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * kTile < n) f(x[i], i * kTile);
+    for (int t0 = kHeld * kTile; t0 < n; t0 += 2 * kTile) {
+      float v[2][kTake];
+      load(v[0], t0);
+      load(v[1], t0 + kTile);
+      f(v[0], t0);
+      if (t0 + kTile < n) f(v[1], t0 + kTile);
+    }
+  };
   // ---- the key of the last one kept, and how many of that key
   uint32_t top = 0xffffffffu;  // nothing reaches it: NaN has key 0, every number less
   int ties = 0;
@@ -91,16 +130,22 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictArgs a) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? kBins : kBins / 2;
       for (int i = tid; i < kBins; i += kPickThreads) sHist[i] = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int t = lo + tid; t < hi; t += kPickThreads) {
-        const uint32_t k = weight_key(w[t]);
-        if ((k & known) == prefix) atomicAdd(&sHist[k >> shift & (bins - 1)], 1);
-      }
+      tiles([&](const float (&v)[kTake], int t0) {
+#pragma unroll
+        for (int y = 0; y < kTake; ++y) {
+          const int t = t0 + mine + y * 32;
+          const uint32_t k = weight_key(v[y]);
+          if (t >= lo && t < hi && (k & known) == prefix) atomicAdd(&sHist[k >> shift & (bins - 1)], 1);
+        }
+      });
       __syncthreads();
-      // the highest bin whose sum from the top reaches `left`: two bins a thread, from the top
-      const int b0 = bins - 1 - 2 * tid;
-      const int h0 = b0 >= 0 ? sHist[b0] : 0, h1 = b0 >= 1 ? sHist[b0 - 1] : 0;
-      int incl = h0 + h1;
+      // the highest bin whose sum from the top reaches `left`: some bins a thread, from the top
+      constexpr int kMine = kBins / kPickThreads;
+      const int b0 = bins - 1 - kMine * tid;
+      int count[kMine], incl = 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) incl += count[i] = b0 - i >= 0 ? sHist[b0 - i] : 0;
+      const int own = incl;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(~0u, incl, d);
@@ -108,10 +153,13 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictArgs a) {
       }
       if (lane == 31) sWarp[warp] = (uint32_t)incl;
       __syncthreads();
-      int above = incl - h0 - h1;
+      int above = incl - own;
       for (int i = 0; i < warp; ++i) above += (int)sWarp[i];
-      if (above < left && left <= above + h0) sBin = b0, sAbove = above;
-      if (above + h0 < left && left <= above + h0 + h1) sBin = b0 - 1, sAbove = above + h0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (above < left && left <= above + count[i]) sBin = b0 - i, sAbove = above;
+        above += count[i];
+      }
       __syncthreads();
       prefix |= (uint32_t)sBin << shift;
       known |= (uint32_t)(bins - 1) << shift;
@@ -122,49 +170,87 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictArgs a) {
     ties = left;
   }
   // ---- the kept positions in order
+  int* now = a.now + (size_t)blockIdx.x * a.pages * 2;
+  for (int i = tid; i < 2 * a.pages; i += kPickThreads) now[i] = 0;
   int before = 0, equal = 0;  // kept without the ties, and ties, of the tiles before
-  for (int t0 = 0; t0 < n; t0 += kPickThreads) {
-    const int t = t0 + tid;
-    const float x = t < n ? w[t] : 0.f;
-    const bool must = t < n && (t < lo || t >= hi);
-    const bool may = t >= lo && t < hi;
-    const uint32_t k = weight_key(x);
-    const bool above = must || (may && want > 0 && k > top), tie = may && want > 0 && k == top;
-    const unsigned am = __ballot_sync(~0u, above), tm = __ballot_sync(~0u, tie);
-    uint32_t total;
-    const uint32_t pre = before_warp((uint32_t)__popc(am) << 16 | (uint32_t)__popc(tm), sWarp, &total);
+  tiles([&](const float (&v)[kTake], int t0) {
+    unsigned am[kTake], tm[kTake];
+    uint32_t count = 0;
+#pragma unroll
+    for (int y = 0; y < kTake; ++y) {
+      const int t = t0 + mine + y * 32;
+      const bool must = t < n && (t < lo || t >= hi), may = t >= lo && t < hi && want > 0;
+      const uint32_t k = weight_key(v[y]);
+      am[y] = __ballot_sync(~0u, must || (may && k > top));
+      tm[y] = __ballot_sync(~0u, may && k == top);
+      count += (uint32_t)__popc(am[y]) << 16 | (uint32_t)__popc(tm[y]);
+    }
+    uint32_t total;  // at most kTile of each kind
+    const uint32_t pre = before_warp(count, sWarp, &total);
+    int at = before + (int)(pre >> 16), tied = equal + (int)(pre & 0xffffu);
     const unsigned mask = (1u << lane) - 1;
-    const int at = before + (int)(pre >> 16) + __popc(am & mask);
-    const int tied = equal + (int)(pre & 0xffffu) + __popc(tm & mask);
-    if (above || (tie && tied < ties)) {  // every weight of the tile has been read
-      const int j = at + min(tied, ties);
-      kept[j] = t;
-      out[j] = x;
+#pragma unroll
+    for (int y = 0; y < kTake; ++y) {
+      const int ties_before = tied + __popc(tm[y] & mask);
+      if (am[y] >> lane & 1 || (tm[y] >> lane & 1 && ties_before < ties)) {
+        const int j = at + __popc(am[y] & mask) + min(ties_before, ties);
+        kept[j] = t0 + mine + y * 32;
+        out[j] = v[y];  // in place: below every weight still to be read
+      }
+      at += __popc(am[y]);
+      tied += __popc(tm[y]);
     }
     before += (int)(total >> 16);
     equal += (int)(total & 0xffffu);
+  });
+  // ---- where the kept rows lie, and the scales of the blocks that receive them
+  __syncthreads();
+  const int32_t* table = c.tables + (size_t)b * c.max_blocks;
+  const int h = blockIdx.x - b * c.H;
+  int2* from = a.from + (size_t)blockIdx.x * a.keep;
+  float2* had = a.had + (size_t)blockIdx.x * a.keep;
+#pragma unroll 4
+  for (int j0 = warp * 32; j0 < a.keep; j0 += kPickThreads) {
+    const int j = min(j0 + lane, a.keep - 1), t = kept[j], col = a.col(t), blk = table[col];
+    const float* s = c.scales + c.scale_at(blk, 0, h);
+    const float2 had_j = make_float2(s[0], s[c.H]);
+    if (j0 + lane < a.keep) {
+      from[j] = make_int2(blk, t - col * c.tpb);
+      had[j] = had_j;
+    }
+    // 16 lanes write to one block: the lanes behind the last row repeat it
+    int top_k = __float_as_int(had_j.x), top_v = __float_as_int(had_j.y);  // scales are >= 0: ordered as integers
+#pragma unroll
+    for (int d = 8; d; d >>= 1) {
+      top_k = max(top_k, __shfl_xor_sync(~0u, top_k, d));
+      top_v = max(top_v, __shfl_xor_sync(~0u, top_v, d));
+    }
+    if ((lane & 15) == 0 && j0 + lane < a.keep) {
+      int* p = now + a.col(j0 + lane) * 2;
+      atomicMax(p, top_k);
+      atomicMax(p + 1, top_v);
+    }
   }
 }
 
 constexpr int kGatherThreads = 512;
-constexpr int kGatherRows = 512;  // rows read before any of them is written
-constexpr int kMostRows = 1024;   // rows of a group: whole blocks, at least one
+constexpr int kGatherVecs = 4;  // 16-byte vectors of a thread in a batch
 
-template <int D>
-__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const EvictArgs a) {
-  constexpr int V = D / 16;                                // 16-byte vectors of a row
-  constexpr int N = kGatherRows * V / kGatherThreads;      // of a thread and batch
-  __shared__ int2 sFrom[kMostRows];                        // a row's block and place in it
-  __shared__ float sHad[kMostRows];                        // that block's scale
-  __shared__ int sNew[kMostRows / 16];                     // the scales of the blocks written, as bits
+// V: 16-byte vectors of a row in a CTA's slice.
+template <int V>
+__global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const EvictArgs a, int slices) {
   const KvCache& c = a.c;
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int kind = blockIdx.x & 1, h = (blockIdx.x >> 1) % c.H, b = (blockIdx.x >> 1) / c.H;
-  const int32_t* kept = a.kept + ((size_t)b * c.H + h) * a.keep;
+  int u = blockIdx.x;
+  const int slice = u % slices;
+  u /= slices;
+  const int kind = u & 1, h = (u >> 1) % c.H, b = (u >> 1) / c.H;
+  const size_t head = (size_t)b * c.H + h;
+  const int32_t* kept = a.kept + head * a.keep;
   const int last = kept[a.keep - 1];
-  if (kind == 0 && h == 0 && tid == 0) {
+  if (kind == 0 && h == 0 && slice == 0 && tid == 0) {
     const int n = a.seq[b], now = last >= 0 ? a.keep : n;
     if (a.free_blocks) {
       const bool ok = n == 0 || kept[0] >= 0;
@@ -174,46 +260,59 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const EvictArgs 
   }
   if (last < a.keep) return;  // at most `keep` positions: nothing moves
   const int32_t* table = c.tables + (size_t)b * c.max_blocks;
-  const int group = c.tpb <= kGatherRows ? kGatherRows / c.tpb * c.tpb : c.tpb;
-  for (int j0 = 0; j0 < a.keep; j0 += group) {
-    const int rows = min(group, a.keep - j0);
-    for (int i = tid; i < kMostRows / 16; i += kGatherThreads) sNew[i] = 0;
-    __syncthreads();
-    for (int r = tid; r < rows; r += kGatherThreads) {
-      const int t = kept[j0 + r], col = t / c.tpb;
-      const int blk = table[col];
-      const float s = c.scales[c.scale_at(blk, kind, h)];
-      sFrom[r] = make_int2(blk, t - col * c.tpb);
-      sHad[r] = s;
-      atomicMax(&sNew[r / c.tpb], __float_as_int(s));  // scales are >= 0: ordered as integers
-    }
-    __syncthreads();
-    for (int r0 = 0; r0 < rows; r0 += kGatherRows) {
-      uint4 x[N];
+  const int2* from = a.from + head * a.keep;
+  const float* had = reinterpret_cast<const float*>(a.had + head * a.keep) + kind;
+  const float* now = reinterpret_cast<const float*>(a.now + head * a.pages * 2) + kind;
+  if (slice == 0)  // the old scales are in `had`
+    for (int i = tid; i < a.pages; i += kGatherThreads) c.scales[c.scale_at(table[i], kind, h)] = now[2 * i];
+  const int x0 = slice * V + tid % V;  // the thread's vector of its rows
+  constexpr int kStep = kGatherThreads / V;
+  for (int j0 = tid / V; j0 - tid / V < a.keep; j0 += kStep * kGatherVecs) {
+    uint4 x[kGatherVecs];
+    float ratio[kGatherVecs];
+    uint8_t* to[kGatherVecs];
+    int2 f[kGatherVecs];
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int v = tid + k * kGatherThreads, r = r0 + v / V;
-        if (r < rows) {
-          const int2 f = sFrom[r];
-          x[k] = reinterpret_cast<const uint4*>(c.pool + c.row(f.x, kind, h, f.y))[v % V];
-        }
-      }
-      __syncthreads();  // all of the batch has been read
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int v = tid + k * kGatherThreads, r = r0 + v / V;
-        if (r < rows) {
-          const float was = sHad[r], is = __int_as_float(sNew[r / c.tpb]);
-          if (was != is) x[k] = rescale_e4m3x16(x[k], scale_ratio(was, is));
-          const int j = j0 + r, col = j / c.tpb;
-          reinterpret_cast<uint4*>(c.pool + c.row(table[col], kind, h, j - col * c.tpb))[v % V] = x[k];
-        }
-      }
+    for (int k = 0; k < kGatherVecs; ++k) {
+      const int j = j0 + k * kStep;
+      f[k] = j < a.keep ? from[j] : make_int2(0, 0);
     }
-    for (int i = tid; i * c.tpb < rows; i += kGatherThreads)
-      c.scales[c.scale_at(table[j0 / c.tpb + i], kind, h)] = __int_as_float(sNew[i]);
-    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kGatherVecs; ++k) {
+      const int j = min(j0 + k * kStep, a.keep - 1), col = a.col(j);
+      x[k] = reinterpret_cast<const uint4*>(c.pool + c.row(f[k].x, kind, h, f[k].y))[x0];
+      const float was = had[2 * j], is = now[2 * col];
+      ratio[k] = was != is ? scale_ratio(was, is) : -1.f;  // -1: the codes stay
+      to[k] = c.pool + c.row(table[col], kind, h, j - col * c.tpb) + x0 * 16;
+    }
+    __syncthreads();  // all of the batch has been read
+#pragma unroll
+    for (int k = 0; k < kGatherVecs; ++k) {
+      if (ratio[k] >= 0.f) x[k] = rescale_e4m3x16(x[k], ratio[k]);
+      if (j0 + k * kStep < a.keep) *reinterpret_cast<uint4*>(to[k]) = x[k];
+    }
   }
+}
+
+template <int V>
+cudaError_t launch_gather(const EvictArgs& a, long units, cudaStream_t st) {
+  const int slices = a.c.D / 16 / V;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * slices));
+  cfg.blockDim = dim3(kGatherThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gather_kernel<V>, a, slices);
+}
+
+size_t scratch_bytes_of(int B, int kv_heads, int keep, int tpb) {
+  const size_t heads = (size_t)B * kv_heads;
+  return align256(heads * keep * sizeof(int2)) + align256(heads * keep * sizeof(float2)) +
+         align256(heads * ceil_div(keep, tpb) * 2 * sizeof(int));
 }
 
 }  // namespace
@@ -222,7 +321,17 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const EvictArgs 
 
 using namespace sv;
 
-extern "C" int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params* p, spec_stream_t stream) {
+extern "C" {
+
+size_t spec_evict_scratch_size(int B, int kv_heads, int keep, int tokens_per_block) {
+  if (B < 1 || B > SPEC_MAX_BATCH || kv_heads < 1 || kv_heads > 1024 || keep < 1 || keep > 1 << 30 ||
+      tokens_per_block < 16 || tokens_per_block > 1024 || tokens_per_block % 16 != 0)
+    return 0;
+  return scratch_bytes_of(B, kv_heads, keep, tokens_per_block);
+}
+
+int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params* p, void* scratch, size_t scratch_bytes,
+                  spec_stream_t stream) {
   EvictArgs a{};
   const int rc = kv_setup(cache, &a.c);
   if (rc != SPEC_OK) return rc;
@@ -232,6 +341,18 @@ extern "C" int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params
       (p->out_weights == p->weights && p->T_out != p->T) || !p->blocks_held != !p->free_blocks ||
       (long)a.c.max_blocks * a.c.tpb > 1l << 30)
     return SPEC_EINVAL;
+  if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256 != 0 ||
+      scratch_bytes < scratch_bytes_of(p->B, a.c.H, p->keep, a.c.tpb))
+    return SPEC_EWORKSPACE;
+  const long heads = (long)p->B * a.c.H;
+  char* s = static_cast<char*>(scratch);
+  a.from = reinterpret_cast<int2*>(s);
+  s += align256(heads * p->keep * sizeof(int2));
+  a.had = reinterpret_cast<float2*>(s);
+  s += align256(heads * p->keep * sizeof(float2));
+  a.now = reinterpret_cast<int*>(s);
+  a.pages = ceil_div(p->keep, a.c.tpb);
+  a.div16 = (unsigned)((1ull << 32) / (a.c.tpb / 16) + ((1ull << 32) % (a.c.tpb / 16) != 0));
   a.weights = p->weights;
   a.seq = p->seq_lens;
   a.held = p->blocks_held;
@@ -246,10 +367,14 @@ extern "C" int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params
   a.first = p->first;
   a.recent = p->recent;
   const cudaStream_t st = (cudaStream_t)stream;
-  const long heads = (long)a.B * a.c.H;
   cudaError_t e = launch_first(pick_kernel, heads, kPickThreads, st, a);
-  if (e == cudaSuccess)
-    e = a.c.D == 64 ? launch_first(gather_kernel<64>, 2 * heads, kGatherThreads, st, a)
-                    : launch_first(gather_kernel<128>, 2 * heads, kGatherThreads, st, a);
+  if (e != cudaSuccess) return SPEC_ECUDA;
+  // whole rows where they give the SMs two CTAs each, else 32 bytes (a sector) of them
+  if (2 * heads < 2 * 152)
+    e = launch_gather<2>(a, 2 * heads, st);
+  else
+    e = a.c.D == 64 ? launch_gather<4>(a, 2 * heads, st) : launch_gather<8>(a, 2 * heads, st);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
+
+}  // extern "C"

@@ -86,6 +86,15 @@ def test_refusals_before_any_launch():
 
     def weigh(cache, p, scratch=16 * 1024, size=1 << 24):
         return lib.spec_weigh_kv(cache, p, scratch, size, None)
+
+    def evict(cache, p, scratch=16 * 1024, size=1 << 24):
+        return lib.spec_evict_kv(cache, p, scratch, size, None)
+    for B, H, keep, tpb in ((0, 1, 1, 16), (8193, 1, 1, 16), (1, 0, 1, 16), (1, 1025, 1, 16), (1, 1, 0, 16),
+                            (1, 1, 2**30 + 1, 16), (1, 1, 1, 8), (1, 1, 1, 24), (1, 1, 1, 1040)):
+        assert lib.spec_evict_scratch_size(B, H, keep, tpb) == 0
+    need = lib.spec_evict_scratch_size(2, 2, 20, 16)
+    for bad in (dict(scratch=None), dict(scratch=16 * 1024 + 128), dict(size=need - 1)):
+        assert evict(_fake_cache(), _fake_evict(), **bad) == sv.SPEC_EWORKSPACE
     for B, W, q, k, D in ((0, 1, 4, 2, 64), (8193, 1, 4, 2, 64), (1, 0, 4, 2, 64), (1, 65537, 4, 2, 64), (1, 1, 4, 3, 64),
                           (1, 1, 0, 1, 64), (1, 1, 4, 0, 64), (1, 1, 16386, 2, 64), (1, 1, 4, 2, 96)):
         assert lib.spec_weigh_scratch_size(B, W, q, k, D) == 0
@@ -95,7 +104,7 @@ def test_refusals_before_any_launch():
             assert weigh(_fake_cache(), _fake_weigh(W=W), **bad) == sv.SPEC_EWORKSPACE
     for bad in BAD_CACHES:
         assert weigh(_fake_cache(**bad), _fake_weigh()) == sv.SPEC_EINVAL, bad
-        assert lib.spec_evict_kv(_fake_cache(**bad), _fake_evict(), None) == sv.SPEC_EINVAL, bad
+        assert evict(_fake_cache(**bad), _fake_evict()) == sv.SPEC_EINVAL, bad
     for bad in (dict(size=8), dict(q=None), dict(q=16 * 1024 + 4), dict(q_strides=odd), dict(dtype=sv.SPEC_F32), dict(B=0),
                 dict(B=8193), dict(W=0), dict(W=65537), dict(q_heads=0), dict(q_heads=3), dict(q_heads=16386),
                 dict(seq_lens=None), dict(lse=None), dict(out=None), dict(T=0), dict(scale=math.nan), dict(scale=3e38),
@@ -105,12 +114,12 @@ def test_refusals_before_any_launch():
                 dict(keep=2**30 + 1, T_out=2**31 - 1), dict(first=-1), dict(recent=-1), dict(first=15),
                 dict(first=2**31 - 1), dict(new_lens=None), dict(kept=None), dict(out_weights=None), dict(T_out=19),
                 dict(out_weights=16 * 1024), dict(blocks_held=None), dict(free_blocks=None)):
-        assert lib.spec_evict_kv(_fake_cache(), _fake_evict(**bad), None) == sv.SPEC_EINVAL, bad
+        assert evict(_fake_cache(), _fake_evict(**bad)) == sv.SPEC_EINVAL, bad
     long = dict(max_blocks=2**26, tokens_per_block=32)
     assert weigh(_fake_cache(**long), _fake_weigh()) == sv.SPEC_EINVAL
-    assert lib.spec_evict_kv(_fake_cache(**long), _fake_evict(), None) == sv.SPEC_EINVAL
-    assert weigh(_fake_cache(), None) == lib.spec_evict_kv(_fake_cache(), None, None) == sv.SPEC_EINVAL
-    assert weigh(None, _fake_weigh()) == lib.spec_evict_kv(None, _fake_evict(), None) == sv.SPEC_EINVAL
+    assert evict(_fake_cache(**long), _fake_evict()) == sv.SPEC_EINVAL
+    assert weigh(_fake_cache(), None) == evict(_fake_cache(), None) == sv.SPEC_EINVAL
+    assert weigh(None, _fake_weigh()) == evict(None, _fake_evict()) == sv.SPEC_EINVAL
 
 
 # ------------------------------------------------------------------ GPU: weights
