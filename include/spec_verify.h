@@ -696,10 +696,16 @@ int spec_rotate_qk(const spec_rotate_params *params, spec_stream_t stream);
  * into the cache at seq_lens, with the results of the two calls, bit for bit.
  * out_k must be NULL, k_heads and head_dim are the cache's; v is strided like
  * k.  The rows of q are rotated for every request whose window length is in
- * [0, W], those that store nothing included. */
+ * [0, W], those that store nothing included.
+ *   scratch: spec_rotate_store_scratch_size(...) bytes (room for the rotated
+ *         keys of long windows), 256-byte aligned, with the rules of
+ *         spec_attend_kv's. */
 int spec_rotate_store_kv(const spec_kv_cache *cache, const spec_rotate_params *params,
                          const void *v, const int64_t *v_strides, const int32_t *seq_lens,
-                         spec_stream_t stream);
+                         void *scratch, size_t scratch_bytes, spec_stream_t stream);
+
+/* Scratch of spec_rotate_store_kv (0 for invalid sizes). */
+size_t spec_rotate_store_scratch_size(int B, int W, int kv_heads, int head_dim, int tokens_per_block);
 
 /* The attention that each cached position drew from a window's rows.
  *   q, q_strides, dtype, seq_lens, window_lens, scale: as for spec_attend_kv,

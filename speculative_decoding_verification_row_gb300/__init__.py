@@ -65,7 +65,8 @@ SYMBOLS = ("spec_workspace_size", "spec_workspace_init", "spec_verify_chain",
            "spec_workspace_size_filtered", "spec_test_timeout_chain", "spec_test_timeout_greedy",
            "spec_verify_tree_sampled", "spec_reserve_blocks", "spec_release_blocks", "spec_tree_masks",
            "spec_store_kv", "spec_attend_kv", "spec_attend_scratch_size", "spec_relocate_quantised_kv",
-           "spec_adjust_logits", "spec_rotate_qk", "spec_rotate_store_kv", "spec_weigh_kv", "spec_weigh_scratch_size",
+           "spec_adjust_logits", "spec_rotate_qk", "spec_rotate_store_kv", "spec_rotate_store_scratch_size",
+           "spec_weigh_kv", "spec_weigh_scratch_size",
            "spec_evict_kv", "spec_evict_scratch_size")
 SPEC_NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -194,7 +195,9 @@ def _bind(lib):
     lib.spec_relocate_quantised_kv.argtypes = [ctypes.POINTER(KvCache), P, P, P, I, I, P]
     lib.spec_adjust_logits.argtypes = [ctypes.POINTER(AdjustParams), P]
     lib.spec_rotate_qk.argtypes = [ctypes.POINTER(RotateParams), P]
-    lib.spec_rotate_store_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(RotateParams), P, S3, P, P]
+    lib.spec_rotate_store_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(RotateParams), P, S3, P, P, S, P]
+    lib.spec_rotate_store_scratch_size.argtypes = [I, I, I, I, I]
+    lib.spec_rotate_store_scratch_size.restype = S
     lib.spec_weigh_kv.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(WeighParams), P, S, P]
     lib.spec_weigh_scratch_size.argtypes = [I, I, I, I, I]
     lib.spec_weigh_scratch_size.restype = S
@@ -1019,11 +1022,14 @@ def rotate_qk(q, k, starts, inv_freq, *, interleaved=False, gain: float = 1.0, w
 
 
 def rotate_store_kv(q, k, v, inv_freq, kv_pool, kv_scales, block_tables, seq_lens, *, starts=None,
-                    interleaved=False, gain: float = 1.0, window_lens=None, masks=None, out_q=None, stream=None):
+                    interleaved=False, gain: float = 1.0, window_lens=None, masks=None, out_q=None, scratch=None,
+                    stream=None):
     """rotate_qk and store_kv in one call, with their results: returns q
     [B, W, Hq, D] rotated, and writes the rotated k and v [B, W, Hkv, D] at
     logical positions seq_lens[b] + i of the paged cache.  starts defaults to
-    seq_lens: pass the text's own positions once evict_kv has dropped some."""
+    seq_lens: pass the text's own positions once evict_kv has dropped some.
+    scratch: a uint8 tensor of spec_rotate_store_scratch_size bytes; made for the
+    call by default."""
     cache, B, dev = _cache(kv_pool, kv_scales, block_tables)
     _cuda(k, "k", ("B", "W", "Hkv", "D"))
     W, H, D = k.shape[1], cache.kv_heads, cache.head_dim
@@ -1038,8 +1044,12 @@ def rotate_store_kv(q, k, v, inv_freq, kv_pool, kv_scales, block_tables, seq_len
         prm = _rotation(q, k, seq_lens if starts is None else starts, inv_freq, interleaved, gain, window_lens, masks,
                         out_q, dev, B, W, D, k.dtype)
         _outside(q, out_q, "out_q")
-        _apart(prm.out_q, prm.k, vp, cache.pool)
-        rc = lib().spec_rotate_store_kv(cache, prm, vp, vs, seq, sh)
+        if scratch is None:
+            need = lib().spec_rotate_store_scratch_size(B, W, H, D, cache.tokens_per_block)
+            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
+        _apart(prm.out_q, prm.k, vp, cache.pool, sp)
+        rc = lib().spec_rotate_store_kv(cache, prm, vp, vs, seq, sp, scratch.numel(), sh)
     if rc != SPEC_OK:
         raise SpecError("spec_rotate_store_kv", rc)
     return out_q

@@ -233,12 +233,11 @@ __global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a
   }
 }
 
-constexpr int kGatherThreads = 512;
 constexpr int kGatherVecs = 4;  // 16-byte vectors of a thread in a batch
 
 // V: 16-byte vectors of a row in a CTA's slice.
-template <int V>
-__global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const EvictArgs a, int slices) {
+template <int V, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) gather_kernel(const EvictArgs a, int slices) {
   const KvCache& c = a.c;
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -264,19 +263,19 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const EvictAr
   const float* had = reinterpret_cast<const float*>(a.had + head * a.keep) + kind;
   const float* now = reinterpret_cast<const float*>(a.now + head * a.pages * 2) + kind;
   if (slice == 0)  // the old scales are in `had`
-    for (int i = tid; i < a.pages; i += kGatherThreads) c.scales[c.scale_at(table[i], kind, h)] = now[2 * i];
+    for (int i = tid; i < a.pages; i += THREADS) c.scales[c.scale_at(table[i], kind, h)] = now[2 * i];
   const int x0 = slice * V + tid % V;  // the thread's vector of its rows
-  constexpr int kStep = kGatherThreads / V;
+  constexpr int kStep = THREADS / V;
+  int2 f[kGatherVecs];  // of the batch to come
+  auto places = [&](int j0) {
+#pragma unroll
+    for (int k = 0; k < kGatherVecs; ++k) f[k] = from[min(j0 + k * kStep, a.keep - 1)];
+  };
+  places(tid / V);
   for (int j0 = tid / V; j0 - tid / V < a.keep; j0 += kStep * kGatherVecs) {
     uint4 x[kGatherVecs];
     float ratio[kGatherVecs];
     uint8_t* to[kGatherVecs];
-    int2 f[kGatherVecs];
-#pragma unroll
-    for (int k = 0; k < kGatherVecs; ++k) {
-      const int j = j0 + k * kStep;
-      f[k] = j < a.keep ? from[j] : make_int2(0, 0);
-    }
 #pragma unroll
     for (int k = 0; k < kGatherVecs; ++k) {
       const int j = min(j0 + k * kStep, a.keep - 1), col = a.col(j);
@@ -285,6 +284,7 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const EvictAr
       ratio[k] = was != is ? scale_ratio(was, is) : -1.f;  // -1: the codes stay
       to[k] = c.pool + c.row(table[col], kind, h, j - col * c.tpb) + x0 * 16;
     }
+    places(j0 + kStep * kGatherVecs);
     __syncthreads();  // all of the batch has been read
 #pragma unroll
     for (int k = 0; k < kGatherVecs; ++k) {
@@ -294,19 +294,19 @@ __global__ void __launch_bounds__(kGatherThreads, 2) gather_kernel(const EvictAr
   }
 }
 
-template <int V>
+template <int V, int THREADS>
 cudaError_t launch_gather(const EvictArgs& a, long units, cudaStream_t st) {
   const int slices = a.c.D / 16 / V;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * slices));
-  cfg.blockDim = dim3(kGatherThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gather_kernel<V>, a, slices);
+  return cudaLaunchKernelEx(&cfg, gather_kernel<V, THREADS>, a, slices);
 }
 
 size_t scratch_bytes_of(int B, int kv_heads, int keep, int tpb) {
@@ -369,11 +369,17 @@ int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params* p, void* 
   const cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = launch_first(pick_kernel, heads, kPickThreads, st, a);
   if (e != cudaSuccess) return SPEC_ECUDA;
-  // whole rows where they give the SMs two CTAs each, else 32 bytes (a sector) of them
-  if (2 * heads < 2 * 152)
-    e = launch_gather<2>(a, 2 * heads, st);
+  // Whole rows where they give every SM several CTAs, else half of them, or 32
+  // bytes (a sector) with larger CTAs.  64 requests, 2048 of up to 8192
+  // positions kept: 149 us with 4 CTAs of 256 per SM, 158 with 2 of 512; one
+  // request, 4096 of 16000: 42 with CTAs of 256, 36 with 512.
+  const bool wide = a.c.D == 128;
+  if (2 * heads >= 8 * 152)
+    e = wide ? launch_gather<8, 256>(a, 2 * heads, st) : launch_gather<4, 256>(a, 2 * heads, st);
+  else if (wide && 2 * heads >= 4 * 152)
+    e = launch_gather<4, 256>(a, 2 * heads, st);
   else
-    e = a.c.D == 64 ? launch_gather<4>(a, 2 * heads, st) : launch_gather<8>(a, 2 * heads, st);
+    e = launch_gather<2, 512>(a, 2 * heads, st);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 

@@ -80,17 +80,15 @@ constexpr int kStoreThreads = 128;
 //
 // TURN (0: as they are, 1: pairs across the halves, 2: interleaved): keys are
 // rotated as they are loaded, and rounded to their type, so that all that
-// follows is the store of what spec_rotate_qk writes.  A unit of few rows takes
-// the angles from a table that its CTA's units share; one of many computes them
-// where it needs them.
+// follows is the store of what spec_rotate_qk writes; the angles of a unit's
+// rows lie in a table that its CTA's units share.
 template <class T, int WARPS, int VECS, int TURN>
 __global__ void __launch_bounds__(kStoreThreads, WARPS > 1 && !TURN ? 9 : 0) store_kernel(const ArgsOf<TURN> a) {
   constexpr int kUnits = kStoreThreads / 32 / WARPS, kLanes = 32 * WARPS;
   const KvCache& c = a.c;
   const int groups = (2 * c.H + kUnits - 1) / kUnits;
-  constexpr int kAngles = TURN && WARPS == 1 ? 128 * VECS : 1;  // rows x pairs of a unit: 32 VECS / (D / 8) x D / 2
-  __shared__ float2 sAngle[kAngles];
-  __shared__ uint64_t sTurns[TURN ? 64 : 1];
+  static_assert(!TURN || WARPS == 1, "rotated units are a warp's");
+  __shared__ float2 sAngle[TURN ? 128 * VECS : 1];  // rows x pairs of a unit: 32 VECS / (D / 8) x D / 2
   if constexpr (TURN != 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -122,16 +120,17 @@ __global__ void __launch_bounds__(kStoreThreads, WARPS > 1 && !TURN ? 9 : 0) sto
   const int rows = min(c.tpb - first, w - i0);
   const int vpr = c.D / 8, shift = c.D == 128 ? 4 : 3;    // vectors per row: 16 or 8
   if constexpr (TURN != 0) {
-    for (int p = threadIdx.x; p < a.r.pairs; p += kStoreThreads) sTurns[p] = turns_of(a.r.inv_freq[p]);
+    __shared__ uint64_t sTurns[64];
+    __shared__ long sPosition[16];  // rows of a unit: 128 vectors of 8 or 16 a row
+    if (threadIdx.x < a.r.pairs) sTurns[threadIdx.x] = turns_of(a.r.inv_freq[threadIdx.x]);
+    if (threadIdx.x >= 64 && threadIdx.x - 64 < rows)
+      sPosition[threadIdx.x - 64] = (long)a.r.starts[b] + depth_of(a.r.masks, a.W, b, i0 + threadIdx.x - 64);
     __syncthreads();
-    if (WARPS == 1) {
-      for (int x = threadIdx.x; x < rows * a.r.pairs; x += kStoreThreads) {
-        const int row = x / a.r.pairs;
-        sAngle[x] = angle_at(sTurns[x - row * a.r.pairs],
-                             (long)a.r.starts[b] + depth_of(a.r.masks, a.W, b, i0 + row), a.r.gain);
-      }
-      __syncthreads();
+    for (int x = threadIdx.x; x < rows * a.r.pairs; x += kStoreThreads) {
+      const int row = x / a.r.pairs;
+      sAngle[x] = angle_at(sTurns[x - row * a.r.pairs], sPosition[row], a.r.gain);
     }
+    __syncthreads();
   }
 #pragma unroll 1
   for (int group = group0; group < groups; group += a.split) {
@@ -146,20 +145,11 @@ __global__ void __launch_bounds__(kStoreThreads, WARPS > 1 && !TURN ? 9 : 0) sto
       uint4 x = *reinterpret_cast<const uint4*>(at);
       if constexpr (TURN != 0) {
         if (kind == 0 && e < 2 * a.r.pairs) {
-          constexpr int kPairs = TURN == 1 ? 8 : 4;
           const bool back = TURN == 1 && e >= a.r.pairs;  // the pairs' second elements
           const int p = TURN == 1 ? (back ? e - a.r.pairs : e) : e / 2;
           uint4 y = make_uint4(0, 0, 0, 0);
           if (TURN == 1) y = *reinterpret_cast<const uint4*>(at + 2 * (back ? -a.r.pairs : a.r.pairs));
-          float2 cs[kPairs];
-          if (WARPS == 1) {
-#pragma unroll
-            for (int k = 0; k < kPairs; ++k) cs[k] = sAngle[row * a.r.pairs + p + k];
-          } else {
-            const long position = (long)a.r.starts[b] + depth_of(a.r.masks, a.W, b, i0 + row);
-#pragma unroll
-            for (int k = 0; k < kPairs; ++k) cs[k] = angle_at(sTurns[p + k], position, a.r.gain);
-          }
+          const float2* cs = sAngle + row * a.r.pairs + p;
           if (TURN == 2)
             turn_inside<T>(x, cs);
           else if (back)
@@ -332,34 +322,51 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const MoveArgs a)
 // 32; with the CTA per unit (64 tokens) it is the other way, 300 and 293.
 constexpr long kStoreMany = 8l * 152 * 8;
 
-template <class T, int WARPS, int VECS, int TURN>
-int launch_store_as(ArgsOf<TURN>& a, cudaStream_t st) {
-  const long blocks = (long)a.B * a.pages;
+template <int WARPS>
+int split_of(const StoreArgs& a) {
   const int groups = ceil_div(2 * a.c.H, kStoreThreads / 32 / WARPS);
-  a.split = WARPS == 1 && blocks * groups > kStoreMany ? 1 : groups;
-  if constexpr (TURN != 0) {
-    a.first_q = blocks * a.split;
-    const long grid = a.first_q + (a.r.x[0].in ? (long)a.B * a.W : 0);
-    if (grid > INT_MAX) return SPEC_EINVAL;
-    return launch_first(store_kernel<T, WARPS, VECS, TURN>, grid, kStoreThreads, st, a) == cudaSuccess ? SPEC_OK
-                                                                                                       : SPEC_ECUDA;
-  } else {
-    if (blocks * a.split > INT_MAX) return SPEC_EINVAL;
-    store_kernel<T, WARPS, VECS, 0><<<(unsigned)(blocks * a.split), kStoreThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
-  }
+  return WARPS == 1 && (long)a.B * a.pages * groups > kStoreMany ? 1 : groups;
 }
+
+template <class T, int WARPS, int VECS>
+int launch_store_as(StoreArgs& a, cudaStream_t st) {
+  a.split = split_of<WARPS>(a);
+  const long grid = (long)a.B * a.pages * a.split;
+  if (grid > INT_MAX) return SPEC_EINVAL;
+  store_kernel<T, WARPS, VECS, 0><<<(unsigned)grid, kStoreThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+// 16-byte vectors of a block's new rows, at most.
+int store_vecs(int tpb, int W, int D) { return min(tpb, W) * D / 8; }
 
 // A warp per unit while a block's new rows fit its registers, else the CTA.
 // (The CTA for all took 814 us with blocks of 16 tokens and 491 with 32; and
 // 105 us for 2048 requests of 4 tokens, now 23.)
+template <class T>
+int launch_store(StoreArgs& a, cudaStream_t st) {
+  const int vecs = store_vecs(a.c.tpb, a.W, a.c.D);
+  if (vecs <= 32 * 4) return launch_store_as<T, 1, 4>(a, st);
+  if (vecs <= 32 * 8) return launch_store_as<T, 1, 8>(a, st);
+  if (vecs <= 32 * 16) return launch_store_as<T, 1, 16>(a, st);
+  return launch_store_as<T, 4, 8>(a, st);
+}
+
+// Whether the rotating store is one launch, its units few rows each.  Longer
+// windows are rotated into scratch and stored from there: rotating in the
+// store's registers takes 157 of them for 16 vectors, and every KV head's unit
+// makes its rows' angles anew.  64 windows of 8 tokens, 8 heads of 128: 8.3 us
+// in one launch, 9.6 in two; 16 trees of 60: 18.5 against 11; 16 prompts of 4096:
+// 621 against 268 (times of the two calls).
+bool turn_in_store(int tpb, int W, int D) { return store_vecs(tpb, W, D) <= 32 * 4; }
+
 template <class T, int TURN>
-int launch_store(ArgsOf<TURN>& a, cudaStream_t st) {
-  const int vecs = min(a.c.tpb, a.W) * a.c.D / 8;
-  if (vecs <= 32 * 4) return launch_store_as<T, 1, 4, TURN>(a, st);
-  if (vecs <= 32 * 8) return launch_store_as<T, 1, 8, TURN>(a, st);
-  if (vecs <= 32 * 16) return launch_store_as<T, 1, 16, TURN>(a, st);
-  return launch_store_as<T, 4, 8, TURN>(a, st);
+int launch_turned(TurnArgs& a, cudaStream_t st) {
+  a.split = split_of<1>(a);
+  a.first_q = (long)a.B * a.pages * a.split;
+  const long grid = a.first_q + (a.r.x[0].in ? (long)a.B * a.W : 0);
+  if (grid > INT_MAX) return SPEC_EINVAL;
+  return launch_first(store_kernel<T, 1, 4, TURN>, grid, kStoreThreads, st, a) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
 // Host check of the store's arguments; fills `a`.
@@ -403,23 +410,48 @@ int spec_store_kv(const spec_kv_cache* cache, const void* k, const int64_t* k_st
   StoreArgs a{};
   const int rc = store_setup(cache, k, k_strides, v, v_strides, dtype, seq_lens, window_lens, B, W, &a);
   if (rc != SPEC_OK) return rc;
-  return dtype == SPEC_BF16 ? launch_store<__nv_bfloat16, 0>(a, (cudaStream_t)stream)
-                            : launch_store<__half, 0>(a, (cudaStream_t)stream);
+  return dtype == SPEC_BF16 ? launch_store<__nv_bfloat16>(a, (cudaStream_t)stream)
+                            : launch_store<__half>(a, (cudaStream_t)stream);
+}
+
+size_t spec_rotate_store_scratch_size(int B, int W, int kv_heads, int head_dim, int tokens_per_block) {
+  if (B < 1 || B > SPEC_MAX_BATCH || W < 1 || W > SPEC_MAX_WINDOW || kv_heads < 1 || kv_heads > 1024 ||
+      (head_dim != 64 && head_dim != 128) || tokens_per_block < 16 || tokens_per_block > 1024 ||
+      tokens_per_block % 16 != 0)
+    return 0;
+  return turn_in_store(tokens_per_block, W, head_dim) ? 256 : align256((size_t)B * W * kv_heads * head_dim * 2);
 }
 
 int spec_rotate_store_kv(const spec_kv_cache* cache, const spec_rotate_params* p, const void* v,
-                         const int64_t* v_strides, const int32_t* seq_lens, spec_stream_t stream) {
+                         const int64_t* v_strides, const int32_t* seq_lens, void* scratch, size_t scratch_bytes,
+                         spec_stream_t stream) {
   TurnArgs a{};
   int rc = rotate_setup(p, &a.r);
   if (rc != SPEC_OK) return rc;
   rc = store_setup(cache, p->k, p->k_strides, v, v_strides, p->dtype, seq_lens, p->window_lens, p->B, p->W, &a);
   if (rc != SPEC_OK) return rc;
   if (p->out_k || !p->q != !p->out_q || p->k_heads != a.c.H || p->head_dim != a.c.D) return SPEC_EINVAL;
-  a.r.x[1].heads = 0;  // the keys go into the cache
+  if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256 != 0 ||
+      scratch_bytes < spec_rotate_store_scratch_size(a.B, a.W, a.c.H, a.c.D, a.c.tpb))
+    return SPEC_EWORKSPACE;
   const cudaStream_t st = (cudaStream_t)stream;
-  if (p->dtype == SPEC_BF16)
-    return p->interleaved ? launch_store<__nv_bfloat16, 2>(a, st) : launch_store<__nv_bfloat16, 1>(a, st);
-  return p->interleaved ? launch_store<__half, 2>(a, st) : launch_store<__half, 1>(a, st);
+  const bool bf = p->dtype == SPEC_BF16;
+  if (turn_in_store(a.c.tpb, a.W, a.c.D)) {
+    a.r.x[1].heads = 0;  // the keys go into the cache
+    if (bf) return p->interleaved ? launch_turned<__nv_bfloat16, 2>(a, st) : launch_turned<__nv_bfloat16, 1>(a, st);
+    return p->interleaved ? launch_turned<__half, 2>(a, st) : launch_turned<__half, 1>(a, st);
+  }
+  RotateRows& k = a.r.x[1];
+  k.out = static_cast<char*>(scratch);
+  k.oh = a.c.D;
+  k.ot = k.oh * a.c.H;
+  k.ob = k.ot * a.W;
+  if (launch_rotate(a.r, p->dtype, st) != cudaSuccess) return SPEC_ECUDA;
+  a.x[0] = k.out;
+  a.sb[0] = k.ob;
+  a.st[0] = k.ot;
+  a.sh[0] = k.oh;
+  return bf ? launch_store<__nv_bfloat16>(a, st) : launch_store<__half>(a, st);
 }
 
 int spec_relocate_quantised_kv(const spec_kv_cache* cache, const int32_t* base_lens,

@@ -62,6 +62,10 @@ int rotate_setup(const spec_rotate_params* p, RotateArgs* a) {
   return SPEC_OK;
 }
 
+cudaError_t launch_rotate(const RotateArgs& a, int dtype, cudaStream_t st) {
+  return dtype == SPEC_BF16 ? launch<__nv_bfloat16>(a, st) : launch<__half>(a, st);
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -71,7 +75,6 @@ extern "C" int spec_rotate_qk(const spec_rotate_params* p, spec_stream_t stream)
   const int rc = rotate_setup(p, &a);
   if (rc != SPEC_OK) return rc;
   if ((!a.x[0].in && !a.x[1].in) || !a.x[0].in != !a.x[0].out || !a.x[1].in != !a.x[1].out) return SPEC_EINVAL;
-  const cudaError_t e = p->dtype == SPEC_BF16 ? launch<__nv_bfloat16>(a, (cudaStream_t)stream)
-                                              : launch<__half>(a, (cudaStream_t)stream);
+  const cudaError_t e = launch_rotate(a, p->dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }

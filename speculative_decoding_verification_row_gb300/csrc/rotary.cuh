@@ -178,5 +178,7 @@ __device__ __forceinline__ void rotate_token(const RotateArgs& a, int b, int i, 
 
 // Host check of a rotation's arguments; fills `a`.
 int rotate_setup(const spec_rotate_params* p, RotateArgs* a);
+// Enqueues the rotation of all rows (rotary.cu).
+cudaError_t launch_rotate(const RotateArgs& a, int dtype, cudaStream_t st);
 
 }  // namespace sv

@@ -101,7 +101,7 @@ def test_refusals_before_any_launch(bad):
     s3 = (ctypes.c_int64 * 3)(128, 128, 64)
     f = 16 * 1024
     if "out_q_strides" not in bad:
-        assert lib.spec_rotate_store_kv(_fake_cache(), _fake(out_k=None, **bad), f, s3, f, None) == sv.SPEC_EINVAL
+        assert lib.spec_rotate_store_kv(_fake_cache(), _fake(out_k=None, **bad), f, s3, f, f, 1 << 30, None) == sv.SPEC_EINVAL
 
 
 def test_refusals_of_each_call():
@@ -113,15 +113,22 @@ def test_refusals_of_each_call():
                 dict(q=None, q_heads=0)):
         assert lib.spec_rotate_qk(_fake(**bad), None) == sv.SPEC_EINVAL, bad
 
-    def store(c=None, p=None, v=f, vs=s3, seq=f):
-        return lib.spec_rotate_store_kv(c or _fake_cache(), p or _fake(out_k=None), v, vs, seq, None)
+    def store(c=None, p=None, v=f, vs=s3, seq=f, scratch=f, size=1 << 30):
+        return lib.spec_rotate_store_kv(c or _fake_cache(), p or _fake(out_k=None), v, vs, seq, scratch, size, None)
+    for W in (3, 40):
+        need = lib.spec_rotate_store_scratch_size(2, W, 2, 64, 16)
+        for bad in (dict(scratch=None), dict(scratch=f + 64), dict(size=need - 1)):
+            assert store(p=_fake(out_k=None, W=W), **bad) == sv.SPEC_EWORKSPACE
+    for bad in ((0, 1, 1, 64, 16), (8193, 1, 1, 64, 16), (1, 0, 1, 64, 16), (1, 65537, 1, 64, 16), (1, 1, 0, 64, 16),
+                (1, 1, 1025, 64, 16), (1, 1, 1, 96, 16), (1, 1, 1, 64, 8), (1, 1, 1, 64, 1040), (1, 1, 1, 64, 24)):
+        assert lib.spec_rotate_store_scratch_size(*bad) == 0
     for bad in BAD_CACHES:
         assert store(c=_fake_cache(**bad)) == sv.SPEC_EINVAL, bad
     for bad in (dict(), dict(out_k=None, k_heads=3), dict(out_k=None, head_dim=128), dict(out_k=None, out_q=None),
                 dict(out_k=None, k=None, k_heads=0)):
         assert store(p=_fake(**bad)) == sv.SPEC_EINVAL, bad
     assert store(v=None) == store(vs=odd) == store(v=f + 4) == store(seq=None) == sv.SPEC_EINVAL
-    assert lib.spec_rotate_store_kv(None, _fake(out_k=None), f, s3, f, None) == sv.SPEC_EINVAL
+    assert lib.spec_rotate_store_kv(None, _fake(out_k=None), f, s3, f, f, 1 << 30, None) == sv.SPEC_EINVAL
 
 
 # ------------------------------------------------------------------ GPU
