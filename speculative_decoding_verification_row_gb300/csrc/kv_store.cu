@@ -68,6 +68,7 @@ __device__ __forceinline__ uint2 quant8(uint4 v, float r) {
 }
 
 constexpr int kStoreThreads = 128;
+constexpr int kTurnVecs = 2;  // 16-byte vectors a lane of a rotated unit
 
 // A unit is one block of one request's window, one kind, one head: the
 // largest magnitude of the new rows, the scale, the codes.  WARPS warps serve
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kStoreThreads, WARPS > 1 && !TURN ? 9 : 0) sto
   const int vpr = c.D / 8, shift = c.D == 128 ? 4 : 3;    // vectors per row: 16 or 8
   if constexpr (TURN != 0) {
     __shared__ uint64_t sTurns[64];
-    __shared__ long sPosition[16];  // rows of a unit: 128 vectors of 8 or 16 a row
+    __shared__ long sPosition[4 * VECS];  // rows of a unit: 32 VECS vectors, 8 or 16 a row
     if (threadIdx.x < a.r.pairs) sTurns[threadIdx.x] = turns_of(a.r.inv_freq[threadIdx.x]);
     if (threadIdx.x >= 64 && threadIdx.x - 64 < rows)
       sPosition[threadIdx.x - 64] = (long)a.r.starts[b] + depth_of(a.r.masks, a.W, b, i0 + threadIdx.x - 64);
@@ -353,12 +354,11 @@ int launch_store(StoreArgs& a, cudaStream_t st) {
 }
 
 // Whether the rotating store is one launch, its units few rows each.  Longer
-// windows are rotated into scratch and stored from there: rotating in the
-// store's registers takes 157 of them for 16 vectors, and every KV head's unit
-// makes its rows' angles anew.  64 windows of 8 tokens, 8 heads of 128: 8.3 us
-// in one launch, 9.6 in two; 16 trees of 60: 18.5 against 11; 16 prompts of 4096:
-// 621 against 268 (times of the two calls).
-bool turn_in_store(int tpb, int W, int D) { return store_vecs(tpb, W, D) <= 32 * 4; }
+// windows are rotated into scratch and stored from there: every KV head's unit
+// makes its rows' angles anew.  64 windows of 1 token, 8 heads of 128: 3.9 us in
+// one launch, 5.9 in two; 256 of 4: 10.4 and 11.4; 64 of 8: 9.5 and 7.8; 16
+// trees of 60: 18.5 and 11.1; 16 prompts of 4096: 621 and 281.
+bool turn_in_store(int tpb, int W, int D) { return store_vecs(tpb, W, D) <= 32 * kTurnVecs; }
 
 template <class T, int TURN>
 int launch_turned(TurnArgs& a, cudaStream_t st) {
@@ -366,7 +366,7 @@ int launch_turned(TurnArgs& a, cudaStream_t st) {
   a.first_q = (long)a.B * a.pages * a.split;
   const long grid = a.first_q + (a.r.x[0].in ? (long)a.B * a.W : 0);
   if (grid > INT_MAX) return SPEC_EINVAL;
-  return launch_first(store_kernel<T, 1, 4, TURN>, grid, kStoreThreads, st, a) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+  return launch_first(store_kernel<T, 1, kTurnVecs, TURN>, grid, kStoreThreads, st, a) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
 // Host check of the store's arguments; fills `a`.

@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kWWarps = 4, kWThreads = kWWarps * 32;
 constexpr int kWKeys = 16 * kWWarps;  // keys of a tile
-constexpr int kWRows = 64;            // rows staged at a time
+constexpr int kWRows = 32;            // most rows of a KV head
 constexpr int kWCost = 2;             // cells of a unit besides its tiles
 constexpr int kWLeast = 4;            // cells below which a share is not worth a CTA
 constexpr int kWCtas = 4 * kSms;
@@ -58,10 +58,11 @@ __device__ __forceinline__ void mma_k16(float (&d)[4], const uint32_t (&a)[4], u
 
 template <class T, int D>
 __global__ void __launch_bounds__(kWThreads, 4) weigh_kernel(const WeighArgs a) {
-  constexpr int U = D / 64;              // 16-byte chunks of a key per thread
-  constexpr int kPitch = 2 * D + 16;     // bytes of a staged row: its 16-byte reads hit all banks once
+  constexpr int U = D / 64;           // 16-byte chunks of a key per thread
+  constexpr int kPitch = 2 * D + 16;  // bytes of a staged row: its 16-byte reads hit all banks once
+  constexpr float kLog2e = 1.4426950408889634f;
   __shared__ __align__(16) unsigned char sQ[kWRows * kPitch];
-  __shared__ float sLse[kWRows];
+  __shared__ __align__(8) float sNeg[kWRows];  // -lse; -inf: no weight
   __shared__ Walk<kAllRows, kWKeys, kWCost> v;
   __shared__ int sMore;
   const KvCache& c = a.c;
@@ -70,113 +71,125 @@ __global__ void __launch_bounds__(kWThreads, 4) weigh_kernel(const WeighArgs a) 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!divide<kAllRows, kWKeys, kWCost, kWThreads>(a, kWLeast, v)) return;
   __syncthreads();  // every thread has stored the walk's beginning
-  const int tpb16 = c.tpb / 16;
   for (;;) {
     if (tid == 0) sMore = v.next(a);
     __syncthreads();
     if (!sMore) break;
     const Unit u = v.u;
-    const int tile0 = v.tile0, tile1 = v.tile1;
-    __syncthreads();  // the walk has been read
-    const int rows = u.w * a.G, chunks = (rows + kWRows - 1) / kWRows;
+    const int tile0 = v.tile0, tile1 = v.tile1, rows = u.w * a.G;
     const long end = (long)u.seq + u.w;  // positions the request has
     const int32_t* table = c.tables + (size_t)u.b * c.max_blocks;
-    auto stage = [&](int chunk) {
-      constexpr int V = 2 * D / 16;  // 16-byte vectors of a row
-      __syncthreads();
-      for (int x = tid; x < kWRows * V; x += kWThreads) {
-        const int r = x / V, at = x % V, row = chunk * kWRows + r;
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (row < rows) {
-          const int i = row / a.G, head = u.h * a.G + row % a.G;
-          q = reinterpret_cast<const uint4*>(a.q + 2 * (u.b * a.qb + i * a.qt + head * a.qh))[at];
-        }
-        *reinterpret_cast<uint4*>(sQ + r * kPitch + at * 16) = q;
-      }
-      for (int r = tid; r < kWRows; r += kWThreads) {
-        const int row = chunk * kWRows + r;
-        float l = INFINITY;  // no weight
-        if (row < rows) {
-          l = a.row_lse[((size_t)u.b * a.W + row / a.G) * a.Hq + u.h * a.G + row % a.G];
-          if (l == -INFINITY) l = INFINITY;
-        }
-        sLse[r] = l;
-      }
-      __syncthreads();
+
+    // ---- keys of a tile: the block looked up two tiles ahead, its rows one
+    uint4 raw[2 * U];
+    float raw_scale = 0.f;
+    int blk = -1, raw_blk = -1;
+    auto lookup = [&](int tile) {
+      const unsigned x = (unsigned)tile * kWWarps + warp;  // group of 16 keys
+      blk = tile < tile1 && (long)x * 16 < end ? table[col16(a, x)] : -1;
     };
-    if (chunks == 1) stage(0);
-    for (int tile = tile0; tile < tile1; ++tile) {
-      const long t0 = (long)tile * kWKeys + warp * 16;
-      const int col16 = tile * kWWarps + warp;
-      int blk = t0 < end ? table[col16 / tpb16] : -1;
-      if (blk >= c.num_blocks) blk = -1;
-      // ---- the keys of this warp, as fragments
-      uint32_t k[U * 4][4];
-      float cs = 0.f;
-      if (blk >= 0) {
-        const uint8_t* kp = c.pool + c.row(blk, 0, u.h, col16 % tpb16 * 16);
-        cs = a.scale * c.scales[c.scale_at(blk, 0, u.h)];
+    auto fetch = [&](int tile) {
+      raw_blk = blk < c.num_blocks ? blk : -1;
+      if (raw_blk >= 0) {
+        const unsigned x = (unsigned)tile * kWWarps + warp;
+        const uint8_t* kp = c.pool + c.row(raw_blk, 0, u.h, (int)(x - col16(a, x) * (c.tpb / 16)) * 16);
+        raw_scale = c.scales[c.scale_at(raw_blk, 0, u.h)];
 #pragma unroll
         for (int y = 0; y < U; ++y) {
-          const uint4 p = reinterpret_cast<const uint4*>(kp + (size_t)g * D)[cc + 4 * y];
-          const uint4 q = reinterpret_cast<const uint4*>(kp + (size_t)(g + 8) * D)[cc + 4 * y];
-          const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            e4m3x4_to(pw[x], k[y * 4 + x][0], k[y * 4 + x][2], (T*)nullptr);
-            e4m3x4_to(qw[x], k[y * 4 + x][1], k[y * 4 + x][3], (T*)nullptr);
-          }
+          raw[2 * y] = reinterpret_cast<const uint4*>(kp + g * D)[cc + 4 * y];
+          raw[2 * y + 1] = reinterpret_cast<const uint4*>(kp + (g + 8) * D)[cc + 4 * y];
         }
-      } else {
-#pragma unroll
-        for (int x = 0; x < U * 4; ++x) k[x][0] = k[x][1] = k[x][2] = k[x][3] = 0;
       }
-      // the first row that sees the lane's keys: place j of the window is seen from its own token on
-      long from[2];
+      lookup(tile + 1);
+    };
+    lookup(tile0);
+
+    // ---- the rows, once for all tiles
+    constexpr int V = 2 * D / 16;  // 16-byte vectors of a row
+    for (int x = tid; x < kWRows * V; x += kWThreads) {
+      const int r = x / V, at = x % V;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int i = (unsigned)r / (unsigned)a.G, head = u.h * a.G + r - i * a.G;
+        q = reinterpret_cast<const uint4*>(a.q + 2 * (u.b * a.qb + i * a.qt + head * a.qh))[at];
+      }
+      *reinterpret_cast<uint4*>(sQ + r * kPitch + at * 16) = q;
+    }
+    float neg = -INFINITY;
+    if (tid < rows) {
+      const int i = (unsigned)tid / (unsigned)a.G;
+      neg = -a.row_lse[((size_t)u.b * a.W + i) * a.Hq + u.h * a.G + tid - i * a.G];
+      if (neg == INFINITY) neg = -INFINITY;
+    }
+    if (tid < kWRows) sNeg[tid] = neg;
+    fetch(tile0);
+    const bool some = __syncthreads_or(tid < rows && neg == -INFINITY);
+
+    for (int tile = tile0; tile < tile1; ++tile) {
+      const long t0 = (long)tile * kWKeys + warp * 16;
+      // ---- the keys of this warp, as fragments
+      uint32_t k[U * 4][4];
+      const bool real = raw_blk >= 0;
+      const float cs = a.scale * raw_scale;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) from[x] = max(0l, t0 + g + 8 * x - u.seq) * a.G;
-      const long first = max(0l, t0 - u.seq) * a.G;  // of the warp's keys
-      float sum[2] = {0.f, 0.f};
-      for (int chunk = (int)(max(0l, (long)tile * kWKeys - u.seq) * a.G / kWRows); chunk < chunks; ++chunk) {
-        if (chunks > 1) stage(chunk);
-        float part[2] = {0.f, 0.f};  // a chunk's sum on its own: fewer roundings on the way
-        for (int n = 0; n < kWRows / 8; ++n) {
-          const int row = chunk * kWRows + n * 8;
-          if (row >= rows) break;
-          if (row + 8 <= first) continue;
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int y = 0; y < U; ++y) {
+        const uint4 p = real ? raw[2 * y] : make_uint4(0, 0, 0, 0), q = real ? raw[2 * y + 1] : make_uint4(0, 0, 0, 0);
+        const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-          for (int y = 0; y < U; ++y) {
-            const uint4* qp = reinterpret_cast<const uint4*>(sQ + (n * 8 + g) * kPitch + (cc + 4 * y) * 32);
-            const uint4 p = qp[0], q = qp[1];
-            const uint32_t b[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        for (int x = 0; x < 4; ++x) {
+          e4m3x4_to(pw[x], k[y * 4 + x][0], k[y * 4 + x][2], (T*)nullptr);
+          e4m3x4_to(qw[x], k[y * 4 + x][1], k[y * 4 + x][3], (T*)nullptr);
+        }
+      }
+      fetch(tile + 1);
+      const long t = t0 + g + 8 * cc;  // the position that a lane of cc < 2 writes
+      const bool mine = cc < 2 && t < end && t < a.T;
+      const size_t at = ((size_t)u.b * c.H + u.h) * a.T + t;
+      const float old = a.old && mine && t < u.seq ? a.old[at] : 0.f;
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // by key, of even and odd rows
+      const bool plain = t0 + 15 <= u.seq && !some;  // every row sees every key
+      for (int n = 0; n * 8 < rows; ++n) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) mma_k16(s, k[y * 4 + x], b[2 * x], b[2 * x + 1], (T*)nullptr);
+        for (int y = 0; y < U; ++y) {
+          const uint4* qp = reinterpret_cast<const uint4*>(sQ + (n * 8 + g) * kPitch + (cc + 4 * y) * 32);
+          const uint4 p = qp[0], q = qp[1];
+          const uint32_t b[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma_k16(s, k[y * 4 + x], b[2 * x], b[2 * x + 1], (T*)nullptr);
+        }
+        // element e: key g + 8 (e / 2), row 2 cc + e % 2
+        const float2 l = *reinterpret_cast<const float2*>(sNeg + n * 8 + 2 * cc);
+        if (plain && n * 8 + 8 <= rows) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 e = mul2(fma2(make_float2(s[2 * x], s[2 * x + 1]), make_float2(cs, cs), l),
+                                  make_float2(kLog2e, kLog2e));
+            sum[x] = add2(sum[x], make_float2(ex2(e.x), ex2(e.y)));
           }
-          // element e: key g + 8 (e / 2), row 2 cc + e % 2
-          const float2 l = *reinterpret_cast<const float2*>(sLse + n * 8 + 2 * cc);
+        } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float le = e & 1 ? l.y : l.x;
-            const float p = ex2(fmaf(s[e], cs, -le) * 1.4426950408889634f);
-            if (row + 2 * cc + (e & 1) >= from[e >> 1] && le != INFINITY) part[e >> 1] += p;
+            const float ln = e & 1 ? l.y : l.x, p = ex2(fmaf(s[e], cs, ln) * kLog2e);
+            // place j of the window is seen from its own token on
+            const long from = max(0l, t0 + g + 8 * (e >> 1) - u.seq) * a.G;
+            if (n * 8 + 2 * cc + (e & 1) >= from && ln != -INFINITY) (e & 1 ? sum[e >> 1].y : sum[e >> 1].x) += p;
           }
         }
-        sum[0] += part[0], sum[1] += part[1];
       }
+      float total[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        sum[x] += __shfl_xor_sync(~0u, sum[x], 1);
-        sum[x] += __shfl_xor_sync(~0u, sum[x], 2);
+        total[x] = sum[x].x + sum[x].y;
+        total[x] += __shfl_xor_sync(~0u, total[x], 1);
+        total[x] += __shfl_xor_sync(~0u, total[x], 2);
       }
-      const long t = t0 + g + 8 * cc;
-      if (cc < 2 && t < end && t < a.T) {
-        const size_t at = ((size_t)u.b * c.H + u.h) * a.T + t;
-        float x = blk < 0 ? NAN : cc ? sum[1] : sum[0];
-        if (a.old && t < u.seq) x = fmaf(a.decay, a.old[at], x);
-        a.sum[at] = x;
+      if (mine) {
+        const float x = !real ? NAN : cc ? total[1] : total[0];
+        a.sum[at] = a.old && t < u.seq ? fmaf(a.decay, old, x) : x;
       }
     }
+    __syncthreads();  // the rows, and the walk, have been read
   }
 }
 
@@ -193,7 +206,7 @@ cudaError_t launch_weigh_rows(const WeighArgs& a, int dtype, cudaStream_t st) {
 namespace {
 
 // Whether this file's kernel serves this many rows per KV head; else weigh_tiles.cu.
-bool few_rows(int W, int G) { return (long)W * G <= 32; }
+bool few_rows(int W, int G) { return (long)W * G <= kWRows; }
 
 }  // namespace
 
@@ -235,6 +248,7 @@ int spec_weigh_kv(const spec_kv_cache* cache, const spec_weigh_params* p, void* 
   a.seq = p->seq_lens;
   a.win = p->window_lens;
   a.mtiles = 1;
+  a.tpb16_div = (unsigned)((1ull << 32) / (a.c.tpb / 16) + ((1ull << 32) % (a.c.tpb / 16) != 0));
   a.row_lse = p->lse;
   a.scale = p->scale;
   a.old = p->weights;
