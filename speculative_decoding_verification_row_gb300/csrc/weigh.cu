@@ -2,11 +2,14 @@
 // (spec_weigh_kv).
 //
 // Tensor cores through mma.sync m16n8k16, the keys as the left operand: a
-// warp holds 16 keys in registers, converted from e4m3 once, and lets the
-// rows pass; each lane adds up the weights of its two keys, so that the sum
-// over rows needs four shuffles per tile and no atomics.  e4m3 -> bf16 and
-// fp16 is exact, so the products are those of the stored values; a weight is
-// exp of a score less the row's lse, at most 1 but for rounding.
+// warp holds 16 keys in registers, converted from e4m3 to fp16 (exact) once,
+// and lets the rows pass; each lane adds up the weights of its two keys, so that
+// the sum over rows needs four shuffles per tile and no atomics.  bf16 rows are
+// scaled by a power of two to a largest magnitude in [2^14, 2^15) and rounded to
+// fp16: exact down to 2^-28 of the row's largest.  (Keys as bf16 instead took 128
+// of a tile's some 250 instructions: 78 us for 64 windows of 1 to 4 tokens over
+// 512 to 8192 positions, 32/8 heads of 128.)  A weight is exp of a score less
+// the row's lse, at most 1 but for rounding.
 #include "weigh.cuh"
 
 namespace sv {
@@ -44,14 +47,8 @@ constexpr int kWCost = 2;             // cells of a unit besides its tiles
 constexpr int kWLeast = 4;            // cells below which a share is not worth a CTA
 constexpr int kWCtas = 4 * kSms;
 
-__device__ __forceinline__ void mma_k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half*) {
+__device__ __forceinline__ void mma_k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                        __nv_bfloat16*) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -63,6 +60,8 @@ __global__ void __launch_bounds__(kWThreads, 4) weigh_kernel(const WeighArgs a) 
   constexpr float kLog2e = 1.4426950408889634f;
   __shared__ __align__(16) unsigned char sQ[kWRows * kPitch];
   __shared__ __align__(8) float sNeg[kWRows];  // -lse; -inf: no weight
+  __shared__ __align__(8) float sUnit[kWRows];  // a row's power of two, inverted
+  constexpr bool kScaled = !__is_same(T, __half);
   __shared__ Walk<kAllRows, kWKeys, kWCost> v;
   __shared__ int sMore;
   const KvCache& c = a.c;
@@ -80,24 +79,29 @@ __global__ void __launch_bounds__(kWThreads, 4) weigh_kernel(const WeighArgs a) 
     const long end = (long)u.seq + u.w;  // positions the request has
     const int32_t* table = c.tables + (size_t)u.b * c.max_blocks;
 
-    // ---- keys of a tile: the block looked up two tiles ahead, its rows one
-    uint4 raw[2 * U];
-    float raw_scale = 0.f;
-    int blk = -1, raw_blk = -1;
+    // ---- keys of a tile: the block looked up two tiles ahead, its rows one (two:
+    // 79.5 us for the case above instead of 74)
+    struct Keys {
+      uint4 row[2 * U];
+      float scale;
+      int blk;
+    } keys;
+    int blk = -1;
     auto lookup = [&](int tile) {
       const unsigned x = (unsigned)tile * kWWarps + warp;  // group of 16 keys
       blk = tile < tile1 && (long)x * 16 < end ? table[col16(a, x)] : -1;
     };
     auto fetch = [&](int tile) {
-      raw_blk = blk < c.num_blocks ? blk : -1;
-      if (raw_blk >= 0) {
+      keys.blk = blk < c.num_blocks ? blk : -1;
+      keys.scale = 0.f;
+      if (keys.blk >= 0) {
         const unsigned x = (unsigned)tile * kWWarps + warp;
-        const uint8_t* kp = c.pool + c.row(raw_blk, 0, u.h, (int)(x - col16(a, x) * (c.tpb / 16)) * 16);
-        raw_scale = c.scales[c.scale_at(raw_blk, 0, u.h)];
+        const uint8_t* kp = c.pool + c.row(keys.blk, 0, u.h, (int)(x - col16(a, x) * (c.tpb / 16)) * 16);
+        keys.scale = c.scales[c.scale_at(keys.blk, 0, u.h)];
 #pragma unroll
         for (int y = 0; y < U; ++y) {
-          raw[2 * y] = reinterpret_cast<const uint4*>(kp + g * D)[cc + 4 * y];
-          raw[2 * y + 1] = reinterpret_cast<const uint4*>(kp + (g + 8) * D)[cc + 4 * y];
+          keys.row[2 * y] = reinterpret_cast<const uint4*>(kp + g * D)[cc + 4 * y];
+          keys.row[2 * y + 1] = reinterpret_cast<const uint4*>(kp + (g + 8) * D)[cc + 4 * y];
         }
       }
       lookup(tile + 1);
@@ -112,6 +116,27 @@ __global__ void __launch_bounds__(kWThreads, 4) weigh_kernel(const WeighArgs a) 
       if (r < rows) {
         const int i = (unsigned)r / (unsigned)a.G, head = u.h * a.G + r - i * a.G;
         q = reinterpret_cast<const uint4*>(a.q + 2 * (u.b * a.qb + i * a.qt + head * a.qh))[at];
+      }
+      if constexpr (kScaled) {  // V lanes hold a row
+        uint32_t* w = &q.x;
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = as_float2(w[e], (T*)nullptr);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+#pragma unroll
+        for (int d = 1; d < V; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        int e2;
+        frexpf(top, &e2);  // top < 2^e2
+        const int up = top > 0.f && top < INFINITY ? min(15 - e2, 126) : 0;
+        const float f = ldexpf(1.f, up);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = as_float2(w[e], (T*)nullptr);
+          w[e] = half2_of(y.x * f, y.y * f);
+        }
+        if (at == 0) sUnit[r] = ldexpf(1.f, -up);
       }
       *reinterpret_cast<uint4*>(sQ + r * kPitch + at * 16) = q;
     }
@@ -129,16 +154,16 @@ __global__ void __launch_bounds__(kWThreads, 4) weigh_kernel(const WeighArgs a) 
       const long t0 = (long)tile * kWKeys + warp * 16;
       // ---- the keys of this warp, as fragments
       uint32_t k[U * 4][4];
-      const bool real = raw_blk >= 0;
-      const float cs = a.scale * raw_scale;
+      const bool real = keys.blk >= 0;
+      const float cs = a.scale * keys.scale;
 #pragma unroll
       for (int y = 0; y < U; ++y) {
-        const uint4 p = real ? raw[2 * y] : make_uint4(0, 0, 0, 0), q = real ? raw[2 * y + 1] : make_uint4(0, 0, 0, 0);
+        const uint4 p = real ? keys.row[2 * y] : make_uint4(0, 0, 0, 0), q = real ? keys.row[2 * y + 1] : make_uint4(0, 0, 0, 0);
         const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          e4m3x4_to(pw[x], k[y * 4 + x][0], k[y * 4 + x][2], (T*)nullptr);
-          e4m3x4_to(qw[x], k[y * 4 + x][1], k[y * 4 + x][3], (T*)nullptr);
+          e4m3x4_to_half(pw[x], k[y * 4 + x][0], k[y * 4 + x][2]);
+          e4m3x4_to_half(qw[x], k[y * 4 + x][1], k[y * 4 + x][3]);
         }
       }
       fetch(tile + 1);
@@ -156,24 +181,26 @@ __global__ void __launch_bounds__(kWThreads, 4) weigh_kernel(const WeighArgs a) 
           const uint4 p = qp[0], q = qp[1];
           const uint32_t b[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mma_k16(s, k[y * 4 + x], b[2 * x], b[2 * x + 1], (T*)nullptr);
+          for (int x = 0; x < 4; ++x) mma_k16(s, k[y * 4 + x], b[2 * x], b[2 * x + 1]);
         }
         // element e: key g + 8 (e / 2), row 2 cc + e % 2
         const float2 l = *reinterpret_cast<const float2*>(sNeg + n * 8 + 2 * cc);
+        float2 scale = make_float2(cs, cs);
+        if constexpr (kScaled) scale = mul2(scale, *reinterpret_cast<const float2*>(sUnit + n * 8 + 2 * cc));
         if (plain && n * 8 + 8 <= rows) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float2 e = mul2(fma2(make_float2(s[2 * x], s[2 * x + 1]), make_float2(cs, cs), l),
+            const float2 e = mul2(fma2(make_float2(s[2 * x], s[2 * x + 1]), scale, l),
                                   make_float2(kLog2e, kLog2e));
             sum[x] = add2(sum[x], make_float2(ex2(e.x), ex2(e.y)));
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float ln = e & 1 ? l.y : l.x, p = ex2(fmaf(s[e], cs, ln) * kLog2e);
+            const float ln = e & 1 ? l.y : l.x, p = ex2(fmaf(s[e], e & 1 ? scale.y : scale.x, ln) * kLog2e);
             // place j of the window is seen from its own token on
-            const long from = max(0l, t0 + g + 8 * (e >> 1) - u.seq) * a.G;
-            if (n * 8 + 2 * cc + (e & 1) >= from && ln != -INFINITY) (e & 1 ? sum[e >> 1].y : sum[e >> 1].x) += p;
+            const long since = max(0l, t0 + g + 8 * (e >> 1) - u.seq) * a.G;
+            if (n * 8 + 2 * cc + (e & 1) >= since && ln != -INFINITY) (e & 1 ? sum[e >> 1].y : sum[e >> 1].x) += p;
           }
         }
       }

@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
   __shared__ __align__(16) float sNeg[kStages][kWRows];  // -lse, -inf: no weight
   __shared__ int sSome[kStages][2];                      // some row of this half has no weight
   __shared__ float sScale[2][kWKeys];
+  __shared__ long sRow[2][kWRows];  // where a step's rows lie, in elements of q; -1: no such row
   __shared__ Line sLine;
   __shared__ Shares sShares;
   __shared__ uint32_t sTmem;
@@ -362,19 +363,19 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
       for (int s = v.s0; s < v.s1; ++s, ++n) {
         const int st = n % kStages;
         bar_wait(&bars.q_empty[st], ((n / kStages) & 1) ^ 1, dead);
-#pragma unroll
-        for (int p = 0; p < kWRows / kPer; ++p) {
-          const int r = s * kWRows + p * kPer + row;
-          const bool real = r < v.rows;
-          const int i = real ? (unsigned)r / (unsigned)a.G : 0, g = real ? r - i * a.G : 0;
-          cp16(at + st * kStage + p * kPer * 128 + (((vec & 7) ^ ((p * kPer + row) & 7)) << 4),
-               a.q + 2 * (v.b * a.qb + i * a.qt + ((long)v.h * a.G + g) * a.qh + vec * 8), real);
-        }
-        if (t < kWRows) {
+        if (t < kWRows) {  // a division per row: one in every copy took as long as the rest of a step
           const int r = s * kWRows + t;
           const bool real = r < v.rows;
           const int i = real ? (unsigned)r / (unsigned)a.G : 0, g = real ? r - i * a.G : 0;
+          sRow[n & 1][t] = real ? v.b * a.qb + i * a.qt + ((long)v.h * a.G + g) * a.qh : -1;
           cp4(smem_u32(&sNeg[st][t]), a.row_lse + ((size_t)v.b * a.W + i) * a.Hq + (size_t)v.h * a.G + g, real);
+        }
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kRowWarps * 32) : "memory");
+#pragma unroll
+        for (int p = 0; p < kWRows / kPer; ++p) {
+          const long from = sRow[n & 1][p * kPer + row];
+          cp16(at + st * kStage + p * kPer * 128 + (((vec & 7) ^ ((p * kPer + row) & 7)) << 4),
+               a.q + (from == -1 ? 0 : 2 * (from + vec * 8)), from != -1);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
