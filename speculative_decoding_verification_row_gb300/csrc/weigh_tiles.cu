@@ -9,7 +9,9 @@
 //   8-11   keys: e4m3 rows of the pages as bf16 or fp16 (exact) into tensor
 //          memory, a unit ahead.
 //   12-15  queries: rows and their lse into shared memory (cp.async, 128-byte
-//          swizzle), two steps ahead of their use.
+//          swizzle), every warp each fourth step, two of its steps under way.
+//          (All four on one step: 88 us for 2 prompt chunks of 2049 tokens, 16/4
+//          heads of 64; a division in every copy there: 101.)
 //   16     one thread issues the products.
 // 256 keys share a read of the queries: a step takes 16 KB (D = 128) from L2
 // and 16384 exponentials.
@@ -33,7 +35,6 @@ constexpr int kSumWarps = 8, kKeyWarps = 4, kRowWarp = kSumWarps + kKeyWarps, kR
               kMmaWarp = kRowWarp + kRowWarps;
 constexpr int kWThreads = (kMmaWarp + 1) * 32;
 constexpr int kStages = 8;
-constexpr int kFly = 4;  // steps of rows under way from L2, besides the one being issued
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kColA = 0, kColD = 256, kCols = 512;  // keys: two buffers of two tiles; scores likewise
 
@@ -188,9 +189,9 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
   extern __shared__ unsigned char smem_raw[];
   __shared__ Bars bars;
   __shared__ __align__(16) float sNeg[kStages][kWRows];  // -lse, -inf: no weight
-  __shared__ int sSome[kStages][2];                      // some row of this half has no weight
+  __shared__ int sSome[kStages];                         // some row has no weight
   __shared__ float sScale[2][kWKeys];
-  __shared__ long sRow[2][kWRows];  // where a step's rows lie, in elements of q; -1: no such row
+  __shared__ long sRow[kRowWarps][kWRows];  // where a step's rows lie, in elements of q; -1: no such row
   __shared__ Line sLine;
   __shared__ Shares sShares;
   __shared__ uint32_t sTmem;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      bar_init(&bars.q_full[i], kRowWarps);
+      bar_init(&bars.q_full[i], 1);
       bar_init(&bars.q_empty[i], 1 + kSumWarps);
     }
     for (int i = 0; i < 2; ++i) {
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
         bar_wait(&bars.d_full[n & 1], (n >> 1) & 1, dead);
         bar_wait(&bars.q_full[st], (n / kStages) & 1, dead);
         fence_after();
-        const bool plain = r0 >= seen && !(sSome[st][0] | sSome[st][1]);
+        const bool plain = r0 >= seen && !sSome[st];
         float2 acc = make_float2(0.f, 0.f);  // a step's sum on its own: fewer roundings on the way
 #pragma unroll
         for (int half = 0; half < kWRows; half += 32) {
@@ -339,58 +340,61 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
       if (lane == 0) bar_arrive(&bars.a_full[seg & 1]);
     }
   } else if (warp < kMmaWarp) {
-    // ---- thread t: 16-byte vector t % V of every kPer-th row; and row t's lse
-    constexpr int V = D / 8, kPer = kRowWarps * 32 / V;
-    const int t = tid - kRowWarp * 32, vec = t % V, row = t / V;
-    const uint32_t base = smem_u32(rows_s), at = base + (vec >> 3) * (kWRows * 128) + row * 128;
-    uint32_t done = 0;  // steps handed over
-    int left[kFly + 1] = {};  // rows that the steps under way have, the oldest first
-    auto hand = [&](int rows) {  // step `done` has arrived
-      const int st = done % kStages;
-      if (t < kWRows) {
-        const float l = sNeg[st][t];
-        const float neg = t < rows && l != -INFINITY ? -l : -INFINITY;
-        sNeg[st][t] = neg;
-        const unsigned none = __ballot_sync(~0u, neg == -INFINITY);
-        if (lane == 0) sSome[st][warp - kRowWarp] = none != 0;
+    // ---- a lane: 16-byte vector lane % V of every kPer-th row, and two rows' place and lse
+    constexpr int V = D / 8, kPer = 32 / V;
+    const int mine = warp - kRowWarp, vec = lane % V, row = lane / V;
+    const uint32_t at = smem_u32(rows_s) + (vec >> 3) * (kWRows * 128) + row * 128;
+    uint32_t last = 0;  // the warp's step before, and its rows from its first on
+    int left = 0;
+    bool any = false;
+    auto hand = [&]() {  // that step has arrived
+      const int st = last % kStages;
+      bool none = false;
+#pragma unroll
+      for (int r = lane; r < kWRows; r += 32) {
+        const float l = sNeg[st][r], neg = r < left && l != -INFINITY ? -l : -INFINITY;
+        sNeg[st][r] = neg;
+        none = none || neg == -INFINITY;
       }
+      none = __any_sync(~0u, none);
+      if (lane == 0) sSome[st] = none;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive(&bars.q_full[st]);
-      ++done;
     };
     for (; v.next(a); ++seg) {
       for (int s = v.s0; s < v.s1; ++s, ++n) {
+        if (n % kRowWarps != mine) continue;
         const int st = n % kStages;
         bar_wait(&bars.q_empty[st], ((n / kStages) & 1) ^ 1, dead);
-        if (t < kWRows) {  // a division per row: one in every copy took as long as the rest of a step
-          const int r = s * kWRows + t;
+#pragma unroll
+        for (int x = lane; x < kWRows; x += 32) {
+          const int r = s * kWRows + x;
           const bool real = r < v.rows;
           const int i = real ? (unsigned)r / (unsigned)a.G : 0, g = real ? r - i * a.G : 0;
-          sRow[n & 1][t] = real ? v.b * a.qb + i * a.qt + ((long)v.h * a.G + g) * a.qh : -1;
-          cp4(smem_u32(&sNeg[st][t]), a.row_lse + ((size_t)v.b * a.W + i) * a.Hq + (size_t)v.h * a.G + g, real);
+          sRow[mine][x] = real ? v.b * a.qb + i * a.qt + ((long)v.h * a.G + g) * a.qh : -1;
+          cp4(smem_u32(&sNeg[st][x]), a.row_lse + ((size_t)v.b * a.W + i) * a.Hq + (size_t)v.h * a.G + g, real);
         }
-        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kRowWarps * 32) : "memory");
-#pragma unroll
+        __syncwarp();
+#pragma unroll 8
         for (int p = 0; p < kWRows / kPer; ++p) {
-          const long from = sRow[n & 1][p * kPer + row];
-          cp16(at + st * kStage + p * kPer * 128 + (((vec & 7) ^ ((p * kPer + row) & 7)) << 4),
+          const int r = p * kPer + row;
+          const long from = sRow[mine][r];
+          cp16(at + st * kStage + p * kPer * 128 + (((vec ^ r) & 7) << 4),
                a.q + (from == -1 ? 0 : 2 * (from + vec * 8)), from != -1);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-#pragma unroll
-        for (int k = 0; k < kFly; ++k) left[k] = left[k + 1];
-        left[kFly] = v.rows - s * kWRows;
-        if (n >= kFly) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kFly) : "memory");
-          hand(left[0]);
+        if (any) {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          hand();
         }
+        any = true;
+        last = n;
+        left = v.rows - s * kWRows;
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-    for (int k = 1; k <= kFly; ++k)
-      if (n + k > kFly) hand(left[k]);
+    if (any) hand();
   } else {
     const uint64_t q_desc = smem_desc(smem_u32(rows_s), 16);
     for (; v.next(a); ++seg) {
