@@ -768,7 +768,8 @@ size_t spec_weigh_scratch_size(int B, int W, int q_heads, int kv_heads, int head
  * seq_lens < 0, more than max_blocks blocks or T positions, or a block id
  * outside [0, num_blocks) among those it has is left untouched: new_lens =
  * seq_lens, its kept rows all -1, free_blocks 0.  Blocks must not be shared
- * between requests, nor stand twice in a request's row.
+ * between requests, nor stand twice in a request's row.  Layers that share
+ * block tables are evicted one by one, each with the same seq_lens.
  *   scratch: spec_evict_scratch_size(...) bytes, 256-byte aligned, with the
  *         rules of spec_attend_kv's. */
 typedef struct spec_evict_params {

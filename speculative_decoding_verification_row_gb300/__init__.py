@@ -35,6 +35,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -945,6 +946,15 @@ def adjust_logits(logits, *, tokens=None, token_lens=None, prompt_lens=None, rep
     return out
 
 
+@functools.lru_cache(maxsize=None)
+def _scratch_bytes(call: str, *sizes) -> int:
+    """spec_<call>_scratch_size of these sizes."""
+    need = getattr(lib(), f"spec_{call}_scratch_size")(*sizes)
+    if need == 0:
+        raise SpecError(f"spec_{call}_scratch_size", SPEC_EINVAL)
+    return need
+
+
 _NO_STRIDES = _Strides(0, 0, 0)
 
 
@@ -1034,8 +1044,9 @@ def rotate_store_kv(q, k, v, inv_freq, kv_pool, kv_scales, block_tables, seq_len
     _cuda(k, "k", ("B", "W", "Hkv", "D"))
     W, H, D = k.shape[1], cache.kv_heads, cache.head_dim
     _cuda(q, "q", ("B", "W", "Hq", "D"))
-    vp, vs = _rows(v, "v", dev, (B, W, H, D), k.dtype)
-    _rows(k, "k", dev, (B, W, H, D), k.dtype)
+    if k.shape != (B, W, H, D):
+        raise ValueError(f"k must have shape {(B, W, H, D)}, got {tuple(k.shape)}")
+    vp, vs = _rows(v, "v", dev, k.shape, k.dtype)
     seq = _at(seq_lens, "seq_lens", dev, _I32, (B,))
     sh, ctx = _on_stream(stream, dev)
     with ctx:
@@ -1045,8 +1056,8 @@ def rotate_store_kv(q, k, v, inv_freq, kv_pool, kv_scales, block_tables, seq_len
                         out_q, dev, B, W, D, k.dtype)
         _outside(q, out_q, "out_q")
         if scratch is None:
-            need = lib().spec_rotate_store_scratch_size(B, W, H, D, cache.tokens_per_block)
-            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+            scratch = torch.empty(_scratch_bytes("rotate_store", B, W, H, D, cache.tokens_per_block), dtype=torch.uint8,
+                                  device=dev)
         sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
         _apart(prm.out_q, prm.k, vp, cache.pool, sp)
         rc = lib().spec_rotate_store_kv(cache, prm, vp, vs, seq, sp, scratch.numel(), sh)
@@ -1084,9 +1095,7 @@ def weigh_kv(q, lse, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=
     win = None if window_lens is None else _at(window_lens, "window_lens", dev, _I32, (B,))
     lp = _at(lse, "lse", dev, _F32, (B, W, Hq))
     wp = None if weights is None else _at(weights, "weights", dev, _F32, (B, H, T))
-    need = lib().spec_weigh_scratch_size(B, W, Hq, H, D)
-    if need == 0:
-        raise SpecError("spec_weigh_scratch_size", SPEC_EINVAL)
+    need = _scratch_bytes("weigh", B, W, Hq, H, D)
     sh, ctx = _on_stream(stream, dev)
     with ctx:
         if out is None:
@@ -1130,9 +1139,7 @@ def evict_kv(weights, kv_pool, kv_scales, block_tables, seq_lens, keep: int, *, 
     held = None if blocks_held is None else _at(blocks_held, "blocks_held", dev, _I32, (B,))
     if held is None and out_free is not None:
         raise ValueError("out_free goes with blocks_held")
-    need = lib().spec_evict_scratch_size(B, H, keep, cache.tokens_per_block)
-    if need == 0:
-        raise SpecError("spec_evict_scratch_size", SPEC_EINVAL)
+    need = _scratch_bytes("evict", B, H, keep, cache.tokens_per_block)
     sh, ctx = _on_stream(stream, dev)
     with ctx:
         if out_lens is None:

@@ -38,9 +38,8 @@ struct EvictArgs {
   int B, T, T_out, keep, first, recent;
 };
 
-constexpr int kPickThreads = 512;
 constexpr int kBins = 2048;
-constexpr int kHeld = 4;   // tiles of kPickThreads kTake weights that stay in registers
+constexpr int kHeld = 4;   // tiles of THREADS x kTake weights that stay in registers
 constexpr int kTake = 4;   // runs of 32 positions that a warp takes at a time
 
 // Order key of a weight: NaN below all, -0 as 0.
@@ -48,11 +47,12 @@ __device__ __forceinline__ uint32_t weight_key(float x) { return x == x ? ord32(
 
 // Exclusive sum over the CTA of two small counts of a warp, packed in 16 bits
 // each; *total: their sum over all warps.
+template <int THREADS>
 __device__ __forceinline__ uint32_t before_warp(uint32_t mine, uint32_t* sWarp, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) sWarp[warp] = mine;
   __syncthreads();
-  uint32_t x = lane < kPickThreads / 32 ? sWarp[lane] : 0u;
+  uint32_t x = lane < THREADS / 32 ? sWarp[lane] : 0u;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t y = __shfl_up_sync(~0u, x, d);
@@ -64,9 +64,10 @@ __device__ __forceinline__ uint32_t before_warp(uint32_t mine, uint32_t* sWarp, 
   return upto - mine;
 }
 
-__global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) pick_kernel(const EvictArgs a) {
   __shared__ int sHist[kBins];
-  __shared__ uint32_t sWarp[kPickThreads / 32];
+  __shared__ uint32_t sWarp[THREADS / 32];
   __shared__ int sBin, sAbove;
   const KvCache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -80,11 +81,11 @@ __global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a
   int bad = n < 0 || n > a.T || (long)n > (long)c.max_blocks * c.tpb;
   if (!bad) {
     const int32_t* table = c.tables + (size_t)b * c.max_blocks;
-    for (int i = tid; (long)i * c.tpb < n; i += kPickThreads) bad |= table[i] < 0 || table[i] >= c.num_blocks;
+    for (int i = tid; (long)i * c.tpb < n; i += THREADS) bad |= table[i] < 0 || table[i] >= c.num_blocks;
   }
   bad = __syncthreads_or(bad);
   if (bad || n <= a.keep) {
-    for (int j = tid; j < a.keep; j += kPickThreads) {
+    for (int j = tid; j < a.keep; j += THREADS) {
       const bool real = !bad && j < n;
       kept[j] = real ? j : -1;
       if (real) out[j] = w[j];
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a
   const int lo = a.first, hi = n - a.recent;  // the positions that may go: [lo, hi)
   const int want = a.keep - a.first - a.recent;
   // The weights, a warp's 32 kTake in a row: those of short requests stay in registers.
-  constexpr int kTile = kPickThreads * kTake;
+  constexpr int kTile = THREADS * kTake;
   const int mine = warp * kTake * 32 + lane;
   float x[kHeld][kTake];
   auto load = [&](float (&v)[kTake], int t0) {
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? kBins : kBins / 2;
-      for (int i = tid; i < kBins; i += kPickThreads) sHist[i] = 0;
+      for (int i = tid; i < kBins; i += THREADS) sHist[i] = 0;
       __syncthreads();
       tiles([&](const float (&v)[kTake], int t0) {
 #pragma unroll
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a
       });
       __syncthreads();
       // the highest bin whose sum from the top reaches `left`: some bins a thread, from the top
-      constexpr int kMine = kBins / kPickThreads;
+      constexpr int kMine = kBins / THREADS;
       const int b0 = bins - 1 - kMine * tid;
       int count[kMine], incl = 0;
 #pragma unroll
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a
   }
   // ---- the kept positions in order
   int* now = a.now + (size_t)blockIdx.x * a.pages * 2;
-  for (int i = tid; i < 2 * a.pages; i += kPickThreads) now[i] = 0;
+  for (int i = tid; i < 2 * a.pages; i += THREADS) now[i] = 0;
   int before = 0, equal = 0;  // kept without the ties, and ties, of the tiles before
   tiles([&](const float (&v)[kTake], int t0) {
     unsigned am[kTake], tm[kTake];
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a
       count += (uint32_t)__popc(am[y]) << 16 | (uint32_t)__popc(tm[y]);
     }
     uint32_t total;  // at most kTile of each kind
-    const uint32_t pre = before_warp(count, sWarp, &total);
+    const uint32_t pre = before_warp<THREADS>(count, sWarp, &total);
     int at = before + (int)(pre >> 16), tied = equal + (int)(pre & 0xffffu);
     const unsigned mask = (1u << lane) - 1;
 #pragma unroll
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) pick_kernel(const EvictArgs a
   int2* from = a.from + (size_t)blockIdx.x * a.keep;
   float2* had = a.had + (size_t)blockIdx.x * a.keep;
 #pragma unroll 4
-  for (int j0 = warp * 32; j0 < a.keep; j0 += kPickThreads) {
+  for (int j0 = warp * 32; j0 < a.keep; j0 += THREADS) {
     const int j = min(j0 + lane, a.keep - 1), t = kept[j], col = a.col(t), blk = table[col];
     const float* s = c.scales + c.scale_at(blk, 0, h);
     const float2 had_j = make_float2(s[0], s[c.H]);
@@ -367,7 +368,10 @@ int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params* p, void* 
   a.first = p->first;
   a.recent = p->recent;
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = launch_first(pick_kernel, heads, kPickThreads, st, a);
+  // A CTA of 1024 holds 16384 weights in its registers, and there is one for each
+  // SM; with more heads two of 512.
+  cudaError_t e = heads <= 152 ? launch_first(pick_kernel<1024>, heads, 1024, st, a)
+                               : launch_first(pick_kernel<512>, heads, 512, st, a);
   if (e != cudaSuccess) return SPEC_ECUDA;
   // Whole rows where they give every SM several CTAs, else half of them, or 32
   // bytes (a sector) with larger CTAs.  64 requests, 2048 of up to 8192
