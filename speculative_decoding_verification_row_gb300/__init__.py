@@ -946,7 +946,7 @@ def adjust_logits(logits, *, tokens=None, token_lens=None, prompt_lens=None, rep
     return out
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _scratch_bytes(call: str, *sizes) -> int:
     """spec_<call>_scratch_size of these sizes."""
     need = getattr(lib(), f"spec_{call}_scratch_size")(*sizes)
@@ -1161,8 +1161,11 @@ def evict_kv(weights, kv_pool, kv_scales, block_tables, seq_lens, keep: int, *, 
             scratch = torch.empty(need, dtype=torch.uint8, device=dev)
         sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
         others = (kp, fp, held, sp, cache.pool, cache.scales, cache.block_tables)
-        for w, n in ((wp, seq), (op, seq), (wp, lp), (op, lp)):  # op may be wp, and lp seq
-            _apart(w, n, *others)
+        _apart(wp, seq, *others)
+        if op != wp or lp != seq:  # op may be wp, and lp seq
+            taken = {x for x in (wp, seq, *others) if x}
+            if op == lp or (op != wp and op in taken) or (lp != seq and lp in taken):
+                raise ValueError("two of the call's arrays are the same memory")
         prm = EvictParams(_EVICT_BYTES, wp, T, B, seq, keep, int(first), int(recent), lp, kp, op, T_out, held, fp)
         rc = lib().spec_evict_kv(cache, prm, sp, scratch.numel(), sh)
     if rc != SPEC_OK:

@@ -11,6 +11,10 @@
 // row never moves up, so a CTA gathers its slice batch by batch: all of a batch
 // is read before any of it is written, and what is written lies below every
 // row still to be read.
+//
+// In a graph: 64 requests of up to 8192 positions to 2048, 8 heads of 128, 147 us,
+// the selection some 40 (latency of its passes) and the move 105 (0.7 of the
+// measured copy rate); one request of 16000 to 4096 32 us.
 #include "kvcache.cuh"
 
 namespace sv {

@@ -10,6 +10,10 @@
 // of a tile's some 250 instructions: 78 us for 64 windows of 1 to 4 tokens over
 // 512 to 8192 positions, 32/8 heads of 128.)  A weight is exp of a score less
 // the row's lse, at most 1 but for rounding.
+//
+// Bound by the bytes under way: 16 warps an SM with a tile each.  In a graph that
+// case takes 75 us, 4.0 TB/s (0.60 of the measured copy rate); 100 requests of
+// one token over 8192 positions 180 us, 5.0 TB/s.
 #include "weigh.cuh"
 
 namespace sv {

@@ -8,11 +8,12 @@
 //          memory and adds exp(score - lse); writes the sum.
 //   8-11   keys: e4m3 rows of the pages as bf16 or fp16 (exact) into tensor
 //          memory, a unit ahead.
-//   12-15  queries: rows and their lse into shared memory (cp.async, 128-byte
-//          swizzle), every warp each fourth step, two of its steps under way.
-//          (All four on one step: 88 us for 2 prompt chunks of 2049 tokens, 16/4
+//   12-14  queries: rows and their lse into shared memory (cp.async, 128-byte
+//          swizzle), every warp each third step, two of its steps under way.
+//          (Four warps on one step: 88 us for 2 prompt chunks of 2049 tokens, 16/4
 //          heads of 64; a division in every copy there: 101.)
-//   16     one thread issues the products.
+//   15     one thread issues the products.  (16 warps in all leave 128 registers,
+//          room for a step's 64 scores at once; 17 with 32 at a time: 86.)
 // 256 keys share a read of the queries: a step takes 16 KB (D = 128) from L2
 // and 16384 exponentials.
 //
@@ -20,6 +21,11 @@
 // that see any of them.  The steps of all units form one line that is cut into
 // equal shares, one per CTA; a unit that falls to several CTAs is joined by a
 // second launch in a fixed order.
+//
+// In a graph: 2 prompt chunks of 2049 tokens over 0 and 4500, 16/4 heads of 64,
+// 80 us; 32/8 heads of 128, 163 us (675 TFLOP/s, 0.35 of the measured dense
+// rate); a prompt of 4096 109 us.  A step takes some 1600 clocks, its exponentials
+// 512 to 1024, its products 512: the hops scores -> sums -> next products.
 #include "tcgen05.cuh"
 #include "weigh.cuh"
 
@@ -31,7 +37,7 @@ constexpr int kWKeys = 256;   // keys of a unit: two tiles of 128 lanes
 constexpr int kWRows = 64;    // rows of a step
 constexpr int kUnitCost = 2;  // cells of a unit besides its steps
 constexpr int kLeast = 4;     // cells below which a share is not worth a CTA
-constexpr int kSumWarps = 8, kKeyWarps = 4, kRowWarp = kSumWarps + kKeyWarps, kRowWarps = 4,
+constexpr int kSumWarps = 8, kKeyWarps = 4, kRowWarp = kSumWarps + kKeyWarps, kRowWarps = 3,
               kMmaWarp = kRowWarp + kRowWarps;
 constexpr int kWThreads = (kMmaWarp + 1) * 32;
 constexpr int kStages = 8;
@@ -254,17 +260,19 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
         fence_after();
         const bool plain = r0 >= seen && !sSome[st];
         float2 acc = make_float2(0.f, 0.f);  // a step's sum on its own: fewer roundings on the way
-#pragma unroll
-        for (int half = 0; half < kWRows; half += 32) {
-          if (t0 >= end) break;
-          float x[32];
-          tmem_ld32(x, lanes + (n & 1) * 128 + half);
+        if (t0 < end) {
+          float x[kWRows];
+          tmem_ld32(x, lanes + (n & 1) * 128);
+          tmem_ld32(x + 32, lanes + (n & 1) * 128 + 32);
           tmem_wait_ld();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bars.d_empty[n & 1]);
           if (plain) {
             const float2 scale = make_float2(cs, cs), log2e = make_float2(kLog2e, kLog2e);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 neg = *reinterpret_cast<const float4*>(&sNeg[st][half + k]);
+            for (int k = 0; k < kWRows; k += 4) {
+              const float4 neg = *reinterpret_cast<const float4*>(&sNeg[st][k]);
               const float2 y = mul2(fma2(make_float2(x[k], x[k + 1]), scale, make_float2(neg.x, neg.y)), log2e);
               const float2 z = mul2(fma2(make_float2(x[k + 2], x[k + 3]), scale, make_float2(neg.z, neg.w)), log2e);
               acc = add2(acc, make_float2(ex2(y.x), ex2(y.y)));
@@ -272,17 +280,19 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float neg = sNeg[st][half + k];
+            for (int k = 0; k < kWRows; ++k) {
+              const float neg = sNeg[st][k];
               const float e = ex2(fmaf(x[k], cs, neg) * kLog2e);
-              if (r0 + half + k >= from && neg != -INFINITY) acc.x += e;
+              if (r0 + k >= from && neg != -INFINITY) acc.x += e;
             }
           }
+        } else {
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bars.d_empty[n & 1]);
         }
         sum += acc.x + acc.y;
-        fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars.d_empty[n & 1]), bar_arrive(&bars.q_empty[st]);
+        if (lane == 0) bar_arrive(&bars.q_empty[st]);
       }
       if (cs != cs || *dead) sum = NAN;  // no such block
       if (v.whole()) {

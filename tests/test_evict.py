@@ -172,7 +172,9 @@ def _check_weigh(q, lse, pool, scales, tables, lens, wins, dtype, T, weights=Non
                                                ([100, 0, 257], 5, 8, 2, 64, 32), ([15, 400], 16, 10, 2, 128, 48),
                                                ([70], 60, 16, 2, 128, 64), ([0, 33], 130, 4, 1, 64, 16),
                                                ([300], 33, 40, 8, 128, 128), ([5], 300, 5, 5, 128, 1024),
-                                               ([1000, 3], 64, 1, 1, 64, 80), ([130], 257, 12, 2, 128, 32)])
+                                               ([1000, 3], 64, 1, 1, 64, 80), ([130], 257, 12, 2, 128, 32),
+                                               ([40, 700], 8, 8, 2, 64, 16), ([40, 700], 11, 6, 2, 128, 32),
+                                               ([3000], 20, 8, 2, 64, 64), ([1000], 400, 8, 2, 64, 32)])
 def test_weigh_matches_oracle(dtype, lens, W, Hq, H, D, tpb):
     rng = np.random.default_rng(W + D)
     lens = np.asarray(lens)
@@ -423,6 +425,7 @@ def test_binding_refusals():
     for bad in (dict(keep=0), dict(first=15, recent=6), dict(first=-1), dict(recent=-1), dict(w=w[:, :1]), dict(w=w.half()),
                 dict(out_weights=w[:, :, :19].contiguous()), dict(out_kept=torch.zeros((2, 2, 19), dtype=torch.int32, device="cuda")),
                 dict(out_lens=seq.long()), dict(out_free=held), dict(blocks_held=held, out_free=held),
-                dict(blocks_held=seq, out_lens=seq), dict(out_weights=scales)):
+                dict(blocks_held=seq, out_lens=seq), dict(out_weights=scales),
+                dict(out_lens=held, blocks_held=held)):
         with pytest.raises(ValueError):
             evict(**bad)
