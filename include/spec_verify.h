@@ -604,7 +604,8 @@ int spec_relocate_quantised_kv(const spec_kv_cache *cache, const int32_t *base_l
  *   tokens  [B, T] int32 or NULL: the request's tokens so far, the first
  *           prompt_lens[b] of them its prompt, the others its output;
  *           token_lens [B] (NULL: T) of them are real.  Lengths are taken into
- *           [0, T] and [0, token_lens[b]]; prompt_lens NULL: no prompt.
+ *           [0, T] and [0, token_lens[b]]; prompt_lens NULL: no prompt.  T is
+ *           below 2^29.
  *   draft_tokens: the window's tokens, which count as output for the rows
  *           behind them.  Without masks [B, R - 1], a chain: row i follows
  *           drafts 0..i-1.  With masks [B, R] and masks [B, R, ceil(R / 32)]
@@ -625,7 +626,8 @@ int spec_relocate_quantised_kv(const spec_kv_cache *cache, const int32_t *base_l
  *           where bit t % 32 of word t / 32 of the row's mask is clear,
  *           whatever x is (NaN included).  allowed_rows [B, R] is each row's
  *           mask, below 0 for none (num_allowed or more: all of the row
- *           becomes -inf); NULL: mask b * R + i, and num_allowed is B * R.
+ *           becomes -inf, which the verify calls do not take); NULL: mask
+ *           b * R + i, and num_allowed is B * R.
  * Arithmetic in fp32, rounded once. */
 typedef struct spec_adjust_params {
     size_t size;

@@ -988,8 +988,12 @@ def _rotation(q, k, starts, inv_freq, interleaved, gain, window_lens, masks, out
 
 def _outside(t, out, name):
     """An output is its input (of the same strides) or lies apart from it."""
-    if out is not None and out is not t and t.data_ptr() == out.data_ptr() and t.stride() != out.stride():
+    if out is t:
+        return
+    if t.data_ptr() == out.data_ptr() and t.stride() != out.stride():
         raise ValueError(f"{name} is its input's memory with other strides")
+    if 0 in out.stride() and any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
+        raise ValueError(f"{name} has several elements in one place")
 
 
 def rotate_qk(q, k, starts, inv_freq, *, interleaved=False, gain: float = 1.0, window_lens=None, masks=None,

@@ -250,6 +250,42 @@ def test_weights_of_an_attention_sum_to_its_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("W", [3, 90])
+def test_weigh_beside_an_attention_on_another_stream_and_captured(W):
+    rng = np.random.default_rng(12)
+    lens = np.array([900, 30])
+    q, lse, pool, scales, tables, wins = _weigh_case(rng, lens, W, 8, 2, 64, 16, "bf16")
+    qd = torch.from_numpy(q).cuda().bfloat16()
+    p, s, tb, ld = _gpu(pool, scales, tables, lse)
+    seq = _i32(lens)
+    one = sv.weigh_kv(qd, ld, p, s, tb, seq)
+    att = sv.attend_kv(qd, p, s, tb, seq)[0]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):  # both kinds take tensor memory
+        w = sv.weigh_kv(qd, ld, p, s, tb, seq, stream=a)
+        x = sv.attend_kv(qd, p, s, tb, seq, stream=b)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(w, one) and torch.equal(x, att)
+    # accumulated three times, eagerly and in two graphs of one call each
+    def call(w):
+        return sv.weigh_kv(qd, ld, p, s, tb, seq, weights=w, decay=0.5, out=w)
+    want = torch.zeros_like(one)
+    for _ in range(3):
+        call(want)
+    got = torch.zeros_like(one)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            call(got)
+    got.zero_()
+    for g in (graphs[0], graphs[1], graphs[0]):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
 def test_weigh_in_a_pool_over_4_gb():
     H, D, tpb, N = 8, 128, 64, 36000  # 4.7 GB
     pool = torch.zeros((N, 2, H, tpb, D), dtype=torch.uint8, device="cuda")

@@ -303,6 +303,7 @@ def test_binding_refusals():
     for bad in (dict(f=f.float()), dict(f=f[:12]), dict(f=torch.cat([f, f])), dict(f=f.cpu()), dict(s=s.long()),
                 dict(s=s[:1]), dict(q=q.float()), dict(k=k.half()), dict(k=k[:, :2]), dict(q=q[..., 1:49]),
                 dict(q=None, k=None), dict(q=None, out_q=q), dict(out_q=k), dict(out_q=q.half()),
+                dict(out_q=torch.zeros_like(q[:, :1]).expand(2, 3, 4, 64)),
                 dict(out_k=q[:, :, :2], out_q=q), dict(window_lens=s.float()),
                 dict(masks=torch.zeros((2, 3, 2), dtype=torch.int32, device="cuda")), dict(q=q.cpu())):
         with pytest.raises(ValueError):
