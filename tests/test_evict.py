@@ -353,6 +353,17 @@ def test_evict_matches_oracle(lens, H, D, tpb, keep, first, recent):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,H,D,keep", [(20, 8, 64, 40), (39, 8, 128, 33), (77, 8, 64, 20), (77, 8, 128, 24)])
+def test_evict_of_many_heads(B, H, D, keep):
+    """More heads than SMs: other sizes of CTAs and of the moved slices."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 90, B)
+    pool, scales, tables = cache(rng, lens, H, D, 16)
+    w = np.exp(rng.normal(0, 2, (B, H, 90))).astype(np.float32)
+    _check_evict(w, pool, scales, tables, lens, keep, 2, 5, -(-lens // 16))
+
+
+@pytest.mark.gpu
 def test_untouched_requests():
     rng = np.random.default_rng(7)
     lens = np.array([90, 90, -3, 90, 200, 90, 0, 95])
