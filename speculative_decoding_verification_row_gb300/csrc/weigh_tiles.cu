@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weigh_tiles_kernel(const WeighAr
           cp16(at + st * kStage + p * kPer * 128 + (((vec ^ r) & 7) << 4),
                a.q + (from == -1 ? 0 : 2 * (from + vec * 8)), from != -1);
         }
+        __syncwarp();  // the places have been read by every lane: the next step writes them
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (any) {
           asm volatile("cp.async.wait_group 1;" ::: "memory");

@@ -188,6 +188,35 @@ def test_weigh_matches_oracle(dtype, lens, W, Hq, H, D, tpb):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64)])
+def test_shares_of_many_steps(dtype, D):
+    """88 steps of 64 rows over 15 units a head: each CTA stages some 14 steps, four or five by each of its staging warps.
+    Neighbouring steps' rows differ in size and direction, so a row of another step shows; and equal calls give
+    equal bits.  The lse are no attention's: in fp16 some weights pass fp32's largest value (e^89; scores reach 150),
+    and read inf."""
+    rng = np.random.default_rng(15)
+    H, G, W, tpb, s = 2, 4, 1400, 32, 2300
+    pool, scales, tables = cache(rng, [s + W], H, D, tpb)
+    q = rng.normal(0, 1, (1, W, H * G, D)) * np.where(np.arange(W) // 16 % 2, 1.0, 0.25)[None, :, None, None]
+    q = to_bf16(q) if dtype == "bf16" else to_f16(q)
+    lse = (5.0 + rng.normal(0, 1, (1, W, H * G))).astype(np.float32)
+    p, sc, tb, ld = _gpu(pool, scales, tables, lse)
+    qd = torch.from_numpy(q).to(TYPES[dtype]).cuda()
+    one = sv.weigh_kv(qd, ld, p, sc, tb, _i32([s]))
+    for _ in range(30):
+        assert torch.equal(sv.weigh_kv(qd, ld, p, sc, tb, _i32([s])), one)
+    want, spread = window.weigh(q, lse.astype(np.float64), pool, scales, tables, [s], np.zeros((1, H, s + W)))
+    got = one.double().cpu().numpy()[:, :, :s + W]
+    # the bound of the file's head
+    rel = math.expm1(spread.max() * (D * 2.0 ** -23 + 6 * 2.0 ** -24) + 16 * 2.0 ** -24) + 2.0 ** -21 + (W * G / 64 + 64) * 2.0 ** -24
+    top = float(np.finfo(np.float32).max)
+    beyond = want > top
+    assert not ((want > top * (1 - rel)) & (want < top * (1 + rel))).any()  # none that may be either
+    assert np.isinf(got[beyond]).all()
+    assert (np.abs(got - want)[~beyond] <= rel * want[~beyond]).all()
+
+
+@pytest.mark.gpu
 def test_an_empty_window_decays():
     rng = np.random.default_rng(1)
     q, lse, pool, scales, tables, wins = _weigh_case(rng, np.array([50, 70]), 3, 4, 2, 64, 16, "bf16", [0, 2])
