@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 6) adjust_kernel(const AdjustArgs a)
   constexpr int E = Vec::EPV, ES = Vec::ES;
   constexpr int U = 4;  // vectors in flight per thread
   constexpr uint32_t kAll = (1u << E) - 1;
-  extern __shared__ uint32_t smem[];
+  extern __shared__ __align__(16) uint32_t smem[];  // cleared as 16-byte vectors
   __shared__ int sListed, sDrafts, sBiased, sNext;
   int* masked = reinterpret_cast<int*>(smem);                   // rows' grammars
   uint32_t* count = smem + (BAN ? (a.rows + 3) & ~3 : 0);       // [kSeg] tokens' words
