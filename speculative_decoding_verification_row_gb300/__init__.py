@@ -1063,7 +1063,8 @@ def rotate_store_kv(q, k, v, inv_freq, kv_pool, kv_scales, block_tables, seq_len
             scratch = torch.empty(_scratch_bytes("rotate_store", B, W, H, D, cache.tokens_per_block), dtype=torch.uint8,
                                   device=dev)
         sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
-        _apart(prm.out_q, prm.k, vp, cache.pool, sp)
+        _apart(prm.out_q, prm.k, cache.pool, sp)  # k and v are only read: they may be one array
+        _apart(prm.out_q, vp, cache.pool, sp)
         rc = lib().spec_rotate_store_kv(cache, prm, vp, vs, seq, sp, scratch.numel(), sh)
     if rc != SPEC_OK:
         raise SpecError("spec_rotate_store_kv", rc)

@@ -280,6 +280,22 @@ def test_rotating_store_starts_at_the_cursor():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("W", [3, 40])
+def test_keys_and_values_of_one_array(W):
+    """k and v are only read, so they may be one array, as for store_kv; in one launch and in two."""
+    rng = np.random.default_rng(9)
+    lens = np.array([20, 5])
+    pool, scales, tables = (torch.from_numpy(x).cuda() for x in cache(rng, lens + W, 2, 64, 16))
+    q, k, _ = _qkv(rng, 2, W, 4, 2, 64, "bf16")
+    f, _ = sv.rotary_frequencies(64, device="cuda")
+    p2, s2 = pool.clone(), scales.clone()
+    q2, k2 = sv.rotate_qk(q, k, _i32(lens), f)
+    sv.store_kv(k2, k, p2, s2, tables, _i32(lens))
+    q1 = sv.rotate_store_kv(q, k, k, f, pool, scales, tables, _i32(lens))
+    assert torch.equal(q1, q2) and torch.equal(pool, p2) and torch.equal(scales, s2)
+
+
+@pytest.mark.gpu
 def test_largest_windows():
     rng = np.random.default_rng(5)
     W = sv.SPEC_MAX_WINDOW
