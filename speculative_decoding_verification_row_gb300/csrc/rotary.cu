@@ -45,9 +45,10 @@ int rotate_setup(const spec_rotate_params* p, RotateArgs* a) {
     if (heads[x] < 0 || heads[x] > 16384 || (heads[x] > 0) != (in[x] != nullptr)) return SPEC_EINVAL;
     if (in[x] && !kv_strides_ok(in[x], is[x])) return SPEC_EINVAL;
     if (out[x] && !kv_strides_ok(out[x], os[x])) return SPEC_EINVAL;
+    const int n[3] = {p->B, p->W, heads[x]};
     if (in[x] == out[x] && in[x])
       for (int d = 0; d < 3; ++d)
-        if (is[x][d] != os[x][d]) return SPEC_EINVAL;
+        if (n[d] > 1 && is[x][d] != os[x][d]) return SPEC_EINVAL;  // the stride of an axis of one element is never used
     a->x[x] = RotateRows{static_cast<const char*>(in[x]), static_cast<char*>(out[x]), is[x][0], is[x][1],
                          is[x][2], os[x][0], os[x][1], os[x][2], heads[x]};
   }

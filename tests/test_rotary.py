@@ -131,6 +131,15 @@ def test_refusals_of_each_call():
     assert lib.spec_rotate_store_kv(None, _fake(out_k=None), f, s3, f, f, 1 << 30, None) == sv.SPEC_EINVAL
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would read the addresses made up here")
+def test_the_stride_of_an_axis_of_one_element_does_not_count():
+    f = 1 << 20
+    other = (ctypes.c_int64 * 3)(512, 128, 64)
+    one = dict(q=f, out_q=f, k=None, k_heads=0, out_k=None, starts=2 * f, inv_freq=3 * f, out_q_strides=other)
+    assert sv.lib().spec_rotate_qk(_fake(**one, B=1), None) == sv.SPEC_ECUDA  # not refused: there is no GPU
+    assert sv.lib().spec_rotate_qk(_fake(**one, B=2), None) == sv.SPEC_EINVAL
+
+
 # ------------------------------------------------------------------ GPU
 def _i32(a):
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
@@ -293,6 +302,19 @@ def test_keys_and_values_of_one_array(W):
     sv.store_kv(k2, k, p2, s2, tables, _i32(lens))
     q1 = sv.rotate_store_kv(q, k, k, f, pool, scales, tables, _i32(lens))
     assert torch.equal(q1, q2) and torch.equal(pool, p2) and torch.equal(scales, s2)
+
+
+@pytest.mark.gpu
+def test_in_place_through_a_view_with_another_stride_on_an_axis_of_one_element():
+    rng = np.random.default_rng(10)
+    f, _ = sv.rotary_frequencies(64, device="cuda")
+    for shape, stride in (((1, 3, 4, 64), (8, 256, 64, 1)), ((2, 1, 4, 64), (256, 24, 64, 1)), ((2, 3, 1, 64), (192, 64, 640, 1))):
+        x = torch.from_numpy(rng.normal(0, 1, shape)).cuda().bfloat16()
+        s = _i32(rng.integers(0, 100, shape[0]))
+        want = sv.rotate_qk(x, None, s, f)[0]
+        view = x.as_strided(shape, stride)
+        assert torch.equal(view, x) and view.stride() != x.stride()
+        assert sv.rotate_qk(x, None, s, f, out_q=view)[0] is view and torch.equal(x, want)
 
 
 @pytest.mark.gpu
