@@ -72,7 +72,8 @@ typedef struct CUstream_st *spec_stream_t;
 
 typedef enum {
     SPEC_OK = 0,
-    SPEC_EINVAL = -1,      /* bad size, dtype, temperature or null pointer */
+    SPEC_EINVAL = -1,      /* bad size, dtype, temperature or null pointer; arrays that
+                              overlap where a call checks them */
     SPEC_EBADINDEX = -2,   /* a token or node id was out of range (device status) */
     SPEC_ECUDA = -3,       /* a CUDA launch or copy failed */
     SPEC_EWORKSPACE = -4,  /* workspace missing or smaller than spec_workspace_size() */
@@ -658,8 +659,9 @@ int spec_adjust_logits(const spec_adjust_params *params, spec_stream_t stream);
  *   q [B, W, q_heads, head_dim], k [B, W, k_heads, head_dim] of `dtype`
  *         (SPEC_BF16 or SPEC_F16), strided as in spec_store_kv, and out_q,
  *         out_k likewise; head_dim a multiple of 16 up to 512.  q or k is NULL
- *         with no heads.  An output may be its input (same strides) and must
- *         overlap no other array, nor itself.
+ *         with no heads.  An output may be its input (same strides).  One that
+ *         shares a byte with another array, or has two elements in one place,
+ *         is refused (rows between the other's rows are apart).
  *   starts [B] int32: the position of window token 0.  It may differ from the
  *         cache's cursor (spec_evict_kv drops positions of the cache, not of
  *         the text).  Token i has position starts[b] + i, or with masks
@@ -698,7 +700,8 @@ int spec_rotate_qk(const spec_rotate_params *params, spec_stream_t stream);
  * into the cache at seq_lens, with the results of the two calls, bit for bit.
  * out_k must be NULL, k_heads and head_dim are the cache's; v is strided like
  * k.  The rows of q are rotated for every request whose window length is in
- * [0, W], those that store nothing included.
+ * [0, W], those that store nothing included.  Arrays that overlap are refused as
+ * there; the pool, its scales and the scratch are written too.
  *   scratch: spec_rotate_store_scratch_size(...) bytes (room for the rotated
  *         keys of long windows), 256-byte aligned, with the rules of
  *         spec_attend_kv's. */

@@ -987,9 +987,9 @@ def _rotation(q, k, starts, inv_freq, interleaved, gain, window_lens, masks, out
 
 
 def _outside(t, out, name):
-    """An output is its input (of the same strides) or lies apart from it."""
-    if out is t:
-        return
+    """An output is its input (of the same strides) or another array, and has a
+    place for each element.  (That it shares no part with another is the C call's
+    check.)"""
     if t.data_ptr() == out.data_ptr() and any(n > 1 and x != y for n, x, y in zip(t.shape, t.stride(), out.stride())):
         raise ValueError(f"{name} is its input's memory with other strides")
     if 0 in out.stride() and any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "apart.cuh"
 #include "kernels.cuh"
 
 namespace sv {
@@ -49,6 +50,14 @@ inline int kv_setup(const spec_kv_cache* s, KvCache* c) {
 inline bool kv_strides_ok(const void* p, const int64_t* st) {
   return p && st && reinterpret_cast<uintptr_t>(p) % 16 == 0 && st[0] % 8 == 0 &&
          st[1] % 8 == 0 && st[2] % 8 == 0;
+}
+
+// The cache among a call's arrays; `written`: its pool and scales.
+inline void cache_arrays(const KvCache& c, int B, bool written, Arrays* a) {
+  const Span x[2] = {dense(c.pool, (Wide)c.num_blocks * 2 * c.H * c.tpb * c.D),
+                     dense(c.scales, (Wide)c.num_blocks * 2 * c.H * sizeof(float))};
+  a->read(dense(c.tables, (Wide)B * c.max_blocks * sizeof(int32_t)));
+  for (const Span& s : x) written ? a->write(s) : a->read(s);
 }
 
 // The least power of two s >= 2^-126 with amax <= 448 s (448 = 1.75 * 2^8 is

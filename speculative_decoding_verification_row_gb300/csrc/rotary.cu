@@ -65,6 +65,18 @@ int rotate_setup(const spec_rotate_params* p, RotateArgs* a) {
   return SPEC_OK;
 }
 
+void rotate_arrays(const spec_rotate_params* p, Arrays* x) {
+  const int B = p->B, W = p->W, D = p->head_dim;
+  const int q = x->read(strided(p->q, p->q_strides, B, W, p->q_heads, D, 2));
+  const int k = x->read(strided(p->k, p->k_strides, B, W, p->k_heads, D, 2));
+  x->read(dense(p->starts, (Wide)B * sizeof(int32_t)));
+  x->read(dense(p->window_lens, (Wide)B * sizeof(int32_t)));
+  x->read(dense(p->masks, (Wide)B * W * ceil_div(W, 32) * sizeof(int32_t)));
+  x->read(dense(p->inv_freq, (Wide)p->pairs * sizeof(double)));
+  x->write(strided(p->out_q, p->out_q_strides, B, W, p->q_heads, D, 2), q);
+  x->write(strided(p->out_k, p->out_k_strides, B, W, p->k_heads, D, 2), k);
+}
+
 cudaError_t launch_rotate(const RotateArgs& a, int dtype, cudaStream_t st) {
   return dtype == SPEC_BF16 ? launch<__nv_bfloat16>(a, st) : launch<__half>(a, st);
 }
@@ -78,6 +90,9 @@ extern "C" int spec_rotate_qk(const spec_rotate_params* p, spec_stream_t stream)
   const int rc = rotate_setup(p, &a);
   if (rc != SPEC_OK) return rc;
   if ((!a.x[0].in && !a.x[1].in) || !a.x[0].in != !a.x[0].out || !a.x[1].in != !a.x[1].out) return SPEC_EINVAL;
+  Arrays x;
+  rotate_arrays(p, &x);
+  if (!x.apart()) return SPEC_EINVAL;
   const cudaError_t e = launch_rotate(a, p->dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }

@@ -183,6 +183,8 @@ __device__ __forceinline__ void rotate_token(const RotateArgs& a, int b, int i, 
 
 // Host check of a rotation's arguments; fills `a`.
 int rotate_setup(const spec_rotate_params* p, RotateArgs* a);
+// Its arrays, eight of them.
+void rotate_arrays(const spec_rotate_params* p, Arrays* x);
 // Enqueues the rotation of all rows (rotary.cu).
 cudaError_t launch_rotate(const RotateArgs& a, int dtype, cudaStream_t st);
 

@@ -135,9 +135,102 @@ def test_refusals_of_each_call():
 def test_the_stride_of_an_axis_of_one_element_does_not_count():
     f = 1 << 20
     other = (ctypes.c_int64 * 3)(512, 128, 64)
-    one = dict(q=f, out_q=f, k=None, k_heads=0, out_k=None, starts=2 * f, inv_freq=3 * f, out_q_strides=other)
+    one = dict(q=f, out_q=f, k=None, k_heads=0, out_k=None, starts=2 * f, inv_freq=3 * f, out_q_strides=other, W=2, q_heads=2)
     assert sv.lib().spec_rotate_qk(_fake(**one, B=1), None) == sv.SPEC_ECUDA  # not refused: there is no GPU
     assert sv.lib().spec_rotate_qk(_fake(**one, B=2), None) == sv.SPEC_EINVAL
+
+
+_NO_GPU = pytest.mark.skipif(torch.cuda.is_available(),
+                             reason="a call that is not refused would read the addresses made up here")
+
+
+def _s3(*s):
+    return (ctypes.c_int64 * 3)(*s)
+
+
+def _placed(**o):
+    """Arguments that lie apart: B 2, W 3, q of 4 heads and k of 2, slices of one row of 8 heads per token."""
+    f, row = 1 << 20, 8 * 64
+    s = _s3(3 * row, row, 64)
+    a = dict(q=f, k=f + 4 * 128, out_q=2 * f, out_k=2 * f + 4 * 128, q_strides=s, k_strides=s, out_q_strides=s, out_k_strides=s,
+             starts=3 * f, inv_freq=4 * f)
+    a.update(o)
+    return _fake(**a)
+
+
+_F, _ROW = 1 << 20, 8 * 64 * 2  # bytes of a token's row
+OVERLAPS = [dict(out_q=_F + 128), dict(out_q=_F + 16), dict(out_q=_F - _ROW), dict(out_k=_F), dict(out_k=2 * _F + 3 * 128),
+            dict(out_k=2 * _F + 3 * 128 + _ROW, out_k_strides=_s3(_ROW // 2, 3 * _ROW // 2, 64)),
+            dict(out_q_strides=_s3(3 * 512, 248, 64)), dict(out_q_strides=_s3(3 * 512, 512, 56)), dict(out_q_strides=_s3(0, 512, 64)),
+            dict(out_q_strides=_s3(1024, 512, 64)), dict(q=2 * _F, out_q=2 * _F, q_strides=_s3(0, 512, 64), out_q_strides=_s3(0, 512, 64)),
+            dict(starts=2 * _F + 4 * 128 + 60), dict(inv_freq=2 * _F + 5 * _ROW), dict(out_q_strides=_s3(-3 * 512, 512, 64), k=2 * _F - 3 * _ROW)]
+APART = [dict(), dict(out_q=_F, out_k=_F + 4 * 128), dict(out_q=_F + 6 * 3 * _ROW), dict(q=2 * _F + 6 * 128, k=_F, q_heads=2),
+         dict(starts=2 * _F + 6 * 128), dict(out_k=2 * _F + 5 * 128 + _ROW, out_k_strides=_s3(_ROW // 2, 3 * _ROW // 2, 64)),
+         dict(out_q_strides=_s3(-3 * 512, 512, 64)), dict(k=_F), dict(q_strides=_s3(0, 0, 0)),
+         dict(inv_freq=2 * _F + 6 * _ROW), dict(out_q_strides=_s3(64, 512, 128), out_q=2 * _F, k=None, k_heads=0, out_k=None)]
+
+
+@_NO_GPU
+def test_arrays_that_overlap_are_refused():
+    from test_kv_store import _fake_cache
+    lib, f = sv.lib(), _F
+    for o in APART:  # not refused: there is no GPU
+        assert lib.spec_rotate_qk(_placed(**o), None) == sv.SPEC_ECUDA, o
+    for o in OVERLAPS:
+        assert lib.spec_rotate_qk(_placed(**o), None) == sv.SPEC_EINVAL, o
+
+    def store(v=6 * f, seq=7 * f, scratch=8 * f, cache=(), **o):
+        c = _fake_cache(**{**dict(pool=9 * f, scales=10 * f, block_tables=11 * f), **dict(cache)})
+        return lib.spec_rotate_store_kv(c, _placed(out_k=None, **o), v, _s3(3 * 512, 512, 64), seq, scratch, 1 << 20, None)
+    assert store() == store(out_q=_F) == store(v=_F + 4 * 128) == store(starts=7 * f) == sv.SPEC_ECUDA
+    for o in (dict(out_q=6 * f - _ROW), dict(out_q=_F + 128), dict(seq=2 * f), dict(scratch=2 * f), dict(scratch=_F + 4 * 128, W=40),
+              dict(v=9 * f + 4096), dict(cache=dict(scales=9 * f + 4)), dict(cache=dict(block_tables=9 * f)),
+              dict(out_q=9 * f), dict(scratch=10 * f), dict(seq=10 * f + 28), dict(out_q_strides=_s3(3 * 512, 8, 64))):
+        assert store(**o) == sv.SPEC_EINVAL, o
+
+
+def test_meeting_of_strided_arrays_by_enumeration(tmp_path):
+    """csrc/apart.cuh against the sets of bytes, for small arrays of any strides."""
+    import os
+    import shutil
+    import subprocess
+    if shutil.which("g++") is None:
+        pytest.skip("no C++ compiler")
+    csrc = os.path.join(os.path.dirname(os.path.abspath(sv.__file__)), "csrc")
+    src = tmp_path / "meet.cpp"
+    src.write_text(f"""#include <cstdio>
+#include "{csrc}/apart.cuh"
+int main() {{
+  long p[2], st[2][3], n[2][3], run[2];
+  while (true) {{
+    sv::Span s[2];
+    for (int k = 0; k < 2; ++k) {{
+      if (scanf("%ld %ld %ld %ld %ld %ld %ld %ld", &p[k], &st[k][0], &st[k][1], &st[k][2], &n[k][0], &n[k][1], &n[k][2], &run[k]) != 8) return 0;
+      const int64_t x[3] = {{st[k][0], st[k][1], st[k][2]}};
+      s[k] = sv::strided((const void*)p[k], x, n[k][0], n[k][1], n[k][2], run[k], 2);
+    }}
+    printf("%d %d\\n", sv::meet(s[0], s[1]), sv::folds(s[0]));
+  }}
+}}
+""")
+    exe = tmp_path / "meet"
+    subprocess.run(["g++", "-std=c++17", "-x", "c++", str(src), "-o", str(exe)], check=True)
+    rng = np.random.default_rng(0)
+    lines, want = [], []
+    for _ in range(3000):
+        sets = []
+        for _ in range(2):
+            n, run = rng.integers(1, 5, 3), int(rng.integers(1, 6))
+            st = rng.integers(-3, 4, 3) * rng.choice([1, 3, 7, 20], 3)
+            p = int(rng.integers(1000, 1150))
+            lines.append(" ".join(str(x) for x in (p, *st, *n, run)))
+            at = [p + 2 * int(i * st[0] + j * st[1] + k * st[2]) + e for i in range(n[0]) for j in range(n[1]) for k in range(n[2])
+                  for e in range(2 * run)]
+            sets.append(at)
+        want.append((int(bool(set(sets[0]) & set(sets[1]))), int(len(set(sets[0])) != len(sets[0]))))
+    out = subprocess.run([str(exe)], input="\n".join(lines), capture_output=True, text=True, check=True).stdout.split()
+    got = list(zip(map(int, out[0::2]), map(int, out[1::2])))
+    assert got == want and 300 < sum(w[0] for w in want) < 2700 and 300 < sum(w[1] for w in want) < 2700
 
 
 # ------------------------------------------------------------------ GPU
@@ -315,6 +408,34 @@ def test_in_place_through_a_view_with_another_stride_on_an_axis_of_one_element()
         view = x.as_strided(shape, stride)
         assert torch.equal(view, x) and view.stride() != x.stride()
         assert sv.rotate_qk(x, None, s, f, out_q=view)[0] is view and torch.equal(x, want)
+
+
+@pytest.mark.gpu
+def test_outputs_that_overlap_are_refused():
+    rng = np.random.default_rng(11)
+    q, k, v = _qkv(rng, 2, 5, 4, 2, 64, "bf16")
+    f, _ = sv.rotary_frequencies(64, device="cuda")
+    s = _i32([3, 4])
+    buf = torch.zeros(2 * 5 * 8 * 64 + 1024, dtype=torch.bfloat16, device="cuda")
+    x, y = buf[:5120].view(2, 5, 8, 64)[:, :, :4], buf[64:5184].view(2, 5, 8, 64)[:, :, :4]
+    rows = buf.as_strided((2, 5, 4, 64), (1280, 248, 64, 1))  # a row's end is the next one's beginning
+    for kw in (dict(q=x, out_q=y), dict(q=q, out_q=rows), dict(q=q, k=k, out_q=x, out_k=buf[192:5312].view(2, 5, 8, 64)[:, :, :2])):
+        with pytest.raises(sv.SpecError):
+            sv.rotate_qk(kw["q"], kw.get("k"), s, f, out_q=kw["out_q"], out_k=kw.get("out_k"))
+    one = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16, device="cuda").expand(2, 5, 4, 64)
+    with pytest.raises(ValueError):
+        sv.rotate_qk(one, None, s, f, out_q=one)
+    pool, scales, tables = (torch.from_numpy(z).cuda() for z in cache(rng, [30, 61], 2, 64, 16))
+    for out in (rows, buf):
+        with pytest.raises((ValueError, sv.SpecError)):
+            sv.rotate_store_kv(x, k, v, f, pool, scales, tables, s, out_q=y if out is buf else out)
+    assert not buf.any()
+    # rows between each other's rows are apart: q, k and both outputs in one array
+    all4 = torch.zeros((2, 5, 12, 64), dtype=torch.bfloat16, device="cuda")
+    all4[:, :, :4], all4[:, :, 8:10] = q, k
+    got = sv.rotate_qk(all4[:, :, :4], all4[:, :, 8:10], s, f, out_q=all4[:, :, 4:8], out_k=all4[:, :, 10:])
+    want = sv.rotate_qk(q, k, s, f)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 @pytest.mark.gpu
