@@ -723,7 +723,8 @@ size_t spec_rotate_store_scratch_size(int B, int W, int kv_heads, int head_dim, 
  *                        + sum of exp(scale * q . k_t - lse)
  *         over the window's tokens that see t and the query heads of KV head
  *         h.  weights NULL: 0.  `out` may be `weights`, and is left as it is
- *         at every other position.  A row whose lse is -inf adds nothing.
+ *         at every other position; that it or the scratch overlaps another array
+ *         is refused.  A row whose lse is -inf adds nothing.
  * Positions in a block whose id lies outside [0, num_blocks) read NaN; for a
  * request with seq_lens < 0, w_b outside [0, W] or a window past max_blocks
  * blocks nothing is written.  Scores and sums are held in fp32; q's elements

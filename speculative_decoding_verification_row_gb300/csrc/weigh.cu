@@ -275,6 +275,17 @@ int spec_weigh_kv(const spec_kv_cache* cache, const spec_weigh_params* p, void* 
   const size_t need = spec_weigh_scratch_size(p->B, p->W, p->q_heads, a.c.H, a.c.D);
   if (need == 0) return SPEC_EINVAL;
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256 != 0 || scratch_bytes < need) return SPEC_EWORKSPACE;
+  const Wide B = p->B, weights = B * a.c.H * p->T * sizeof(float);
+  Arrays x;
+  const int old = x.read(dense(p->weights, weights));
+  x.read(strided(p->q, p->q_strides, p->B, p->W, p->q_heads, a.c.D, 2));
+  x.read(dense(p->lse, B * p->W * p->q_heads * sizeof(float)));
+  x.read(dense(p->seq_lens, B * sizeof(int32_t)));
+  x.read(dense(p->window_lens, B * sizeof(int32_t)));
+  cache_arrays(a.c, p->B, false, &x);
+  x.write(dense(p->out, weights), old);
+  x.write(dense(scratch, need));
+  if (!x.apart()) return SPEC_EINVAL;
   a.q = static_cast<const char*>(p->q);
   a.qb = p->q_strides[0];
   a.qt = p->q_strides[1];

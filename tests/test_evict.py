@@ -122,6 +122,32 @@ def test_refusals_before_any_launch():
     assert weigh(None, _fake_weigh()) == evict(None, _fake_evict()) == sv.SPEC_EINVAL
 
 
+_NO_GPU = pytest.mark.skipif(torch.cuda.is_available(),
+                             reason="a call that is not refused would read the addresses made up here")
+_F = 1 << 20
+_CACHE = dict(pool=9 * _F, scales=10 * _F, block_tables=11 * _F)
+
+
+@_NO_GPU
+@pytest.mark.parametrize("W", [3, 300])
+def test_weigh_refuses_arrays_that_overlap(W):
+    lib, f, B, H, T = sv.lib(), _F, 2, 2, 100
+    row = (ctypes.c_int64 * 3)(W * 512, 512, 64)
+
+    def call(scratch=12 * f, cache=(), **o):
+        a = dict(q=f, q_strides=row, W=W, seq_lens=4 * f, window_lens=5 * f, lse=6 * f, weights=7 * f, out=8 * f, B=B, T=T)
+        return lib.spec_weigh_kv(_fake_cache(**{**_CACHE, **dict(cache)}), _fake_weigh(**{**a, **o}), scratch, 1 << 24, None)
+    n = B * H * T * 4
+    for o in (dict(), dict(out=7 * f), dict(weights=None), dict(out=7 * f + n), dict(weights=8 * f + n), dict(window_lens=None),
+              dict(out=f + 4 * 128, T=2, q_strides=(ctypes.c_int64 * 3)(W * 512, 512, 64), B=1), dict(lse=7 * f),
+              dict(q_strides=(ctypes.c_int64 * 3)(0, 512, 64))):  # not refused: there is no GPU
+        assert call(**o) == sv.SPEC_ECUDA, o
+    for o in (dict(out=7 * f + 4), dict(out=7 * f - n + 4), dict(out=6 * f + 8), dict(out=f), dict(out=4 * f), dict(out=5 * f + 4),
+              dict(out=9 * f), dict(out=10 * f), dict(out=11 * f), dict(scratch=f), dict(scratch=7 * f), dict(scratch=8 * f),
+              dict(scratch=6 * f), dict(scratch=11 * f)):
+        assert call(**o) == sv.SPEC_EINVAL, o
+
+
 # ------------------------------------------------------------------ GPU: weights
 def _i32(a):
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
@@ -326,6 +352,19 @@ def test_weigh_in_a_pool_over_4_gb():
     out = sv.weigh_kv(q, torch.zeros((1, 1, H), device="cuda"), pool, scales, tables, _i32([150]), scale=1.0)
     want = torch.exp(torch.where(torch.arange(151, device="cuda") < 64, 0.0, 2.0))
     assert (out[0, :, :151] / want - 1).abs().max() < 1e-6 and not out[0, :, 151:].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("W", [2, 50])
+def test_weights_shifted_against_the_output_are_refused(W):
+    rng = np.random.default_rng(16)
+    pool, scales, tables = _gpu(*cache(rng, [30, 61], 2, 64, 16))
+    q = torch.zeros((2, W, 4, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((2, W, 4), device="cuda")
+    buf = torch.zeros(2 * 2 * 64 + 4, device="cuda")
+    with pytest.raises(sv.SpecError):
+        sv.weigh_kv(q, lse, pool, scales, tables, _i32([20, 9]), weights=buf[:256].view(2, 2, 64), out=buf[4:].view(2, 2, 64))
+    assert not buf.any()
 
 
 # ------------------------------------------------------------------ GPU: eviction
