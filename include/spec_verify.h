@@ -768,7 +768,8 @@ size_t spec_weigh_scratch_size(int B, int W, int q_heads, int kv_heads, int head
  *   kept [B, kv_heads, keep] int32: the positions that the rows came from, -1
  *         behind new_lens[b]; out_weights [B, kv_heads, T_out] float32, T_out
  *         >= keep: their weights, left as it is from new_lens[b] on (may be
- *         `weights` itself, with T_out = T);
+ *         `weights` itself, with T_out = T).  Arrays that overlap in any other
+ *         way are refused;
  *   free_blocks [B] or NULL = max(0, blocks_held[b] - ceil(new_len /
  *         tokens_per_block)), for spec_release_blocks.
  * A request of at most `keep` positions keeps all and moves nothing.  One with

@@ -349,6 +349,17 @@ int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params* p, void* 
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256 != 0 ||
       scratch_bytes < scratch_bytes_of(p->B, a.c.H, p->keep, a.c.tpb))
     return SPEC_EWORKSPACE;
+  const Wide lens = (Wide)p->B * sizeof(int32_t), per_row = (Wide)p->B * a.c.H * sizeof(float);
+  Arrays x;
+  const int old = x.read(dense(p->weights, per_row * p->T)), seq = x.read(dense(p->seq_lens, lens));
+  x.read(dense(p->blocks_held, lens));
+  cache_arrays(a.c, p->B, true, &x);
+  x.write(dense(p->new_lens, lens), seq);
+  x.write(dense(p->kept, per_row * p->keep));
+  x.write(dense(p->out_weights, per_row * p->T_out), old);
+  x.write(dense(p->free_blocks, lens));
+  x.write(dense(scratch, scratch_bytes_of(p->B, a.c.H, p->keep, a.c.tpb)));
+  if (!x.apart()) return SPEC_EINVAL;
   const long heads = (long)p->B * a.c.H;
   char* s = static_cast<char*>(scratch);
   a.from = reinterpret_cast<int2*>(s);

@@ -148,6 +148,25 @@ def test_weigh_refuses_arrays_that_overlap(W):
         assert call(**o) == sv.SPEC_EINVAL, o
 
 
+@_NO_GPU
+def test_evict_refuses_arrays_that_overlap():
+    lib, f = sv.lib(), _F
+    row = 2 * 2 * 4  # bytes a position: 2 requests, 2 heads
+
+    def call(scratch=12 * f, cache=(), **o):
+        a = dict(weights=f, seq_lens=2 * f, new_lens=3 * f, kept=4 * f, out_weights=5 * f, blocks_held=6 * f, free_blocks=7 * f)
+        return lib.spec_evict_kv(_fake_cache(**{**_CACHE, **dict(cache)}), _fake_evict(**{**a, **o}), scratch, 1 << 20, None)
+    for o in (dict(), dict(new_lens=2 * f), dict(out_weights=f, T_out=100), dict(new_lens=2 * f, out_weights=f, T_out=100),
+              dict(blocks_held=None, free_blocks=None), dict(out_weights=f + 100 * row), dict(kept=5 * f + 20 * row),
+              dict(free_blocks=3 * f + 8)):  # not refused: there is no GPU
+        assert call(**o) == sv.SPEC_ECUDA, o
+    for o in (dict(new_lens=2 * f + 4), dict(out_weights=f + 4), dict(out_weights=f + 4, T_out=100), dict(out_weights=f + 100 * row - 4),
+              dict(kept=f), dict(kept=5 * f + 20 * row - 4), dict(free_blocks=3 * f + 4), dict(free_blocks=6 * f), dict(new_lens=6 * f + 4),
+              dict(kept=9 * f), dict(out_weights=10 * f), dict(out_weights=11 * f), dict(scratch=f), dict(scratch=4 * f), dict(scratch=11 * f),
+              dict(cache=dict(scales=9 * f + 64)), dict(cache=dict(pool=f)), dict(cache=dict(block_tables=9 * f + 4))):
+        assert call(**o) == sv.SPEC_EINVAL, o
+
+
 # ------------------------------------------------------------------ GPU: weights
 def _i32(a):
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
@@ -483,6 +502,17 @@ def test_long_requests_and_repeated_eviction():
     lens2, kept2, _, _ = sv.evict_kv(out, pool, scales, tables, seq, keep, first=100, recent=1000)
     assert lens2.item() == keep and torch.equal(kept2[0, 0].long(), torch.arange(keep, device="cuda"))
     assert torch.equal(pool, before)
+
+
+@pytest.mark.gpu
+def test_kept_weights_shifted_against_the_weights_are_refused():
+    rng = np.random.default_rng(17)
+    pool, scales, tables = _gpu(*cache(rng, [30, 61], 2, 64, 16))
+    old = pool.clone()
+    buf = torch.zeros(2 * 2 * 64 + 4, device="cuda")
+    with pytest.raises(sv.SpecError):
+        sv.evict_kv(buf[4:].view(2, 2, 64), pool, scales, tables, _i32([30, 60]), 20, out_weights=buf[:256].view(2, 2, 64))
+    assert torch.equal(pool, old) and not buf.any()
 
 
 @pytest.mark.gpu
