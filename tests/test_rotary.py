@@ -367,6 +367,67 @@ def test_rotating_store_is_the_two_calls(dtype, B, W, Hq, H, D, tpb, inter, rot)
         assert torch.equal(q1, q2) and torch.equal(p1, p2) and torch.equal(s1, s2)
 
 
+# (B, W, Hq, H, D, tpb) of one launch: min(W, tpb) * D / 8 at most 64
+ONE_LAUNCH = [(3, 1, 32, 8, 128, 16), (4, 3, 8, 2, 128, 16), (4, 4, 4, 4, 128, 32), (2, 2, 2, 1, 128, 1024), (5, 4, 10, 5, 128, 48),
+              (4, 8, 4, 2, 64, 16), (3, 7, 6, 3, 64, 16), (2, 5, 2, 1, 64, 48), (3, 6, 7, 7, 64, 32)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,W,Hq,H,D,tpb", ONE_LAUNCH)
+@pytest.mark.parametrize("inter,rot", [(False, 1.0), (True, 1.0), (False, 0.25), (True, 0.75)])
+def test_one_launch_is_the_two_calls(dtype, B, W, Hq, H, D, tpb, inter, rot):
+    """Windows of a decode step, across a block's end and inside it, as chains and as trees."""
+    assert sv.lib().spec_rotate_store_scratch_size(B, W, H, D, tpb) == 256  # no scratch for rotated keys
+    rng = np.random.default_rng(W * D + tpb)
+    lens = 2 * tpb - 1 - np.arange(B) * (W // 2)  # the first window crosses the end of its block, the last ones end there
+    lens[-1] = 0
+    pool, scales, tables = cache(rng, lens + W, H, D, tpb)
+    pool, scales, tables = torch.from_numpy(pool).cuda(), torch.from_numpy(scales).cuda(), _i32(tables)
+    q, k, v = _qkv(rng, B, W, Hq, H, D, dtype)
+    k *= torch.from_numpy(np.exp(rng.normal(0, 1, (B, W, 1, 1)))).to(k.dtype).cuda()  # some grow their block's scale
+    f, gain = sv.rotary_frequencies(int(rot * D), scaling="ramp", factor=4, original_len=2048, device="cuda")
+    starts = _i32(rng.integers(0, 200000, B))
+    masks = _i32(kv.tree_masks(np.stack([random_paths(rng, W, W, 4) for _ in range(B)]), W))
+    wins = rng.integers(0, W + 1, B)
+    wins[0] = W
+    for win, m in ((None, None), (_i32(wins), None), (None, masks), (_i32(wins), masks)):
+        args = dict(interleaved=inter, gain=gain, window_lens=win, masks=m)
+        p2, s2 = pool.clone(), scales.clone()
+        q2, k2 = sv.rotate_qk(q, k, starts, f, **args)
+        sv.store_kv(k2, v, p2, s2, tables, _i32(lens), window_lens=win)
+        p1, s1 = pool.clone(), scales.clone()
+        q1 = sv.rotate_store_kv(q, k, v, f, p1, s1, tables, _i32(lens), starts=starts, **args)
+        assert torch.equal(q1, q2) and torch.equal(p1, p2) and torch.equal(s1, s2)
+        assert not torch.equal(p1, pool)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,W,Hq,H,D,inter", [(1300, 4, 8, 8, 128, False), (2600, 4, 6, 3, 128, True), (1300, 8, 8, 8, 64, False)])
+def test_one_launch_of_a_large_batch(B, W, Hq, H, D, inter):
+    """So many blocks that a CTA takes all (kind, head) pairs of one, which share its angles."""
+    tpb = 16
+    assert sv.lib().spec_rotate_store_scratch_size(B, W, H, D, tpb) == 256
+    assert B * 2 * -(-2 * H // 4) > 8 * 152 * 8  # where the CTAs change
+    rng = np.random.default_rng(B)
+    tables = _i32(rng.permutation(2 * B).reshape(B, 2))
+    pool = torch.from_numpy(rng.integers(0, 256, (2 * B, 2, H, tpb, D)).astype(np.uint8)).cuda()
+    scales = torch.from_numpy(np.exp2(rng.integers(-9, -4, (2 * B, 2, H))).astype(np.float32)).cuda()
+    lens = rng.integers(0, 2 * tpb - W + 1, B)
+    q, k, v = _qkv(rng, B, W, Hq, H, D, "bf16")
+    f, _ = sv.rotary_frequencies(D, device="cuda")
+    starts = _i32(rng.integers(0, 5000, B))
+    win = _i32(rng.integers(0, W + 1, B))
+    masks = _i32(np.broadcast_to(kv.tree_masks(random_paths(rng, W, W, 4)[None], W), (B, W, 1)))
+    for args in (dict(window_lens=win), dict(masks=masks)):
+        p2, s2 = pool.clone(), scales.clone()
+        q2, k2 = sv.rotate_qk(q, k, starts, f, interleaved=inter, **args)
+        sv.store_kv(k2, v, p2, s2, tables, _i32(lens), window_lens=args.get("window_lens"))
+        p1, s1 = pool.clone(), scales.clone()
+        q1 = sv.rotate_store_kv(q, k, v, f, p1, s1, tables, _i32(lens), starts=starts, interleaved=inter, **args)
+        assert torch.equal(q1, q2) and torch.equal(p1, p2) and torch.equal(s1, s2)
+
+
 @pytest.mark.gpu
 def test_rotating_store_starts_at_the_cursor():
     rng = np.random.default_rng(4)
