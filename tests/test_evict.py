@@ -298,6 +298,47 @@ def test_bad_requests_and_blocks():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,W,D", [("bf16", 4, 128), ("f16", 4, 64), ("bf16", 64, 64), ("f16", 64, 128), ("bf16", 400, 128),
+                                       ("f16", 400, 64)])
+def test_weights_of_exact_scores(dtype, W, D):
+    """Rows and keys of whole numbers, as many bits as their types hold, whose scores are exact in fp32 in any order
+    (below 2^24), less an lse that is a multiple of the same unit.  What is left to round: the product of y = score - lse
+    with log2(e), 2^-24 |y|, and that constant, 2^-25 |y|; exp2, 2^-22; and the sums, one 2^-24 an addition on a
+    weight's way (rows in a lane or a step of 64, then steps, shuffles and parts).  A bf16 row's first element is 2^28,
+    where the keys are 0: the others are 2^-28 of it."""
+    rng = np.random.default_rng(W + D)
+    H, G, tpb, s = 2, 4, 16, 700
+    bits = 8 if dtype == "bf16" else 11
+    unit = 2.0 ** (-13 if dtype == "bf16" else -16)
+    q = rng.integers(-2 ** bits + 1, 2 ** bits, (W, H, G, D)).astype(np.float64)
+    n = s + W
+    k = rng.integers(-15, 16, (n, H, D)).astype(np.float64)
+    if dtype == "bf16":
+        q[..., 0], k[..., 0] = 2.0 ** 28, 0
+    S = np.einsum("ihgd,thd->ihgt", q, k) * unit
+    S[np.broadcast_to((np.arange(n)[None] > s + np.arange(W)[:, None])[:, None, None], S.shape)] = -np.inf
+    top = S.max(-1, keepdims=True)
+    lse = np.round((top + np.log(np.exp(S - top).sum(-1, keepdims=True))) / unit) * unit
+    y = S - lse
+    p = np.exp(y)
+    want = p.sum((0, 2))
+    adds = 33 + W * G // 64 + 16
+    bound = (p * (1.5 * 2.0 ** -24 * np.abs(np.where(p > 0, y, 0)) + 2.0 ** -22)).sum((0, 2)) + adds * 2.0 ** -24 * want
+    cols = -(-n // tpb)
+    tables = rng.permutation(cols).astype(np.int32)[None]
+    pool = np.zeros((cols, 2, H, tpb, D), np.uint8)
+    for t in range(n):
+        pool[tables[0, t // tpb], 0, :, t % tpb] = kv.encode(k[t])
+    pd, tb = _gpu(pool, tables)
+    qd = torch.from_numpy(q.reshape(1, W, H * G, D)).to(TYPES[dtype]).cuda()
+    assert np.array_equal(qd.double().cpu().numpy().reshape(q.shape), q)
+    ld = torch.from_numpy(lse.astype(np.float32).reshape(1, W, H * G)).cuda()
+    got = sv.weigh_kv(qd, ld, pd, torch.ones((cols, 2, H), device="cuda"), tb, _i32([s]), scale=unit)
+    err = np.abs(got[0, :, :n].double().cpu().numpy() - want)
+    assert (err <= bound + 1e-37).all(), (err / bound).max()
+
+
+@pytest.mark.gpu
 def test_weights_of_an_attention_sum_to_its_rows():
     rng = np.random.default_rng(4)
     for W, lens in ((3, [5000, 1, 700]), (700, [1300, 0, 5])):
@@ -448,6 +489,18 @@ def test_evict_of_many_heads(B, H, D, keep):
     pool, scales, tables = cache(rng, lens, H, D, 16)
     w = np.exp(rng.normal(0, 2, (B, H, 90))).astype(np.float32)
     _check_evict(w, pool, scales, tables, lens, keep, 2, 5, -(-lens // 16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,H,keep", [([40001], 1, 15000), ([13001, 8300, 2500] + [60] * 17, 8, 3000)])
+def test_weights_in_place_beyond_the_registers(lens, H, keep):
+    """A CTA's registers hold 16384 weights of few heads and 8192 with more heads than SMs; what is behind is read as the
+    kept weights are written below it.  Many weights are equal."""
+    rng = np.random.default_rng(18)
+    pool, scales, tables = cache(rng, lens, H, 64, 64)
+    w = np.round(np.exp(rng.normal(0, 1, (len(lens), H, max(lens)))), 1).astype(np.float32)
+    _check_evict(w, pool, scales, tables, lens, keep, 4, 500, [-(-n // 64) for n in lens], inplace=True)
+    _check_evict(w, pool, scales, tables, lens, keep, 4, 500, extra=3)
 
 
 @pytest.mark.gpu
