@@ -303,6 +303,37 @@ def test_verify_of_penalised_rows_is_the_oracles_choice():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sampling_verifies_of_penalised_and_masked_rows(dtype):
+    """Rows whose adjusted distribution is one token but for e^-20: chain and tree verify by sampling choose it."""
+    V, k = 700, 3
+    x = torch.full((2, k + 1, V), -1000.0, dtype=TYPES[dtype], device="cuda")
+    for t, v in ((10, 0.0), (20, -20.0), (30, -40.0), (40, -60.0)):  # each is next once those before it stand in the output
+        x[:, :, t] = v
+    draft = torch.tensor([[10, 20, 30]] * 2, dtype=torch.int32, device="cuda")
+    q = torch.full((2, k, V), -1000.0, dtype=TYPES[dtype], device="cuda")
+    q.scatter_(2, draft.long()[..., None], 0.0)
+    u = torch.full((2, k + 1), 0.5, device="cuda")
+    allowed = torch.zeros((1, -(-V // 32)), dtype=torch.int32, device="cuda")
+    allowed[0, 0] = 1 << 5
+    rows = torch.full((2, k + 1), -1, dtype=torch.int32, device="cuda")
+    rows[1, 1] = 0  # behind 10 the second request's grammar has token 5 alone
+    adj = sv.adjust_logits(x, draft_tokens=draft, frequency=torch.full((2,), 100.0, device="cuda"), allowed=allowed, allowed_rows=rows)
+    tok, n, _ = sv.verify_chain(adj, q, draft, u, 1.0)
+    assert n.tolist() == [3, 1] and tok[0].tolist() == [10, 20, 30, 40] and tok[1].tolist() == [10, 5, -1, -1]
+    assert sv.verify_chain(x, q, draft, u, 1.0)[1].tolist() == [1, 1]
+    # 0 -> 1 (10) -> 2 (20) -> 4 (30), and 1 -> 3 (10 again)
+    paths = torch.tensor([[[0, 1, 2, 4], [0, 1, 3, -1]]], dtype=torch.int32, device="cuda")
+    tree = torch.tensor([[0, 10, 20, 10, 30]], dtype=torch.int32, device="cuda")
+    y = x[:1, :1].expand(1, 5, V).contiguous()
+    u = torch.full((1, 5), 0.5, device="cuda")
+    adj = sv.adjust_logits(y, draft_tokens=tree, masks=sv.tree_masks(paths, 5), frequency=torch.full((1,), 100.0, device="cuda"))
+    tok, n, _, nodes = sv.verify_tree_sampled(adj, tree, paths, u, 1.0)
+    assert n.tolist() == [3] and nodes[0].tolist() == [0, 1, 2, 4] and tok[0].tolist() == [10, 20, 30, 40]
+    assert sv.verify_tree_sampled(y, tree, paths, u, 1.0)[3][0, :3].tolist() == [0, 1, 3]
+
+
+@pytest.mark.gpu
 def test_two_streams_and_a_captured_call():
     rng = np.random.default_rng(13)
     a, b = _case(rng, 4, 4, 20000), _case(rng, 4, 4, 20000)
