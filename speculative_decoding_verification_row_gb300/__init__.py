@@ -987,9 +987,8 @@ def _rotation(q, k, starts, inv_freq, interleaved, gain, window_lens, masks, out
 
 
 def _outside(t, out, name):
-    """An output is its input (of the same strides) or another array, and has a
-    place for each element.  (That it shares no part with another is the C call's
-    check.)"""
+    """Names what the C call refused: an output that is its input's memory in
+    another order, or has no place for each element."""
     if t.data_ptr() == out.data_ptr() and any(n > 1 and x != y for n, x, y in zip(t.shape, t.stride(), out.stride())):
         raise ValueError(f"{name} is its input's memory with other strides")
     if 0 in out.stride() and any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
@@ -1023,14 +1022,16 @@ def rotate_qk(q, k, starts, inv_freq, *, interleaved=False, gain: float = 1.0, w
         prm = _rotation(q, k, starts, inv_freq, interleaved, gain, window_lens, masks, out_q, dev, B, W, D, x.dtype)
         if k is not None:
             prm.out_k, prm.out_k_strides = _rows(out_k, "out_k", dev, k.shape, x.dtype)
-            _outside(k, out_k, "out_k")
-        if q is not None:
-            _outside(q, out_q, "out_q")
-        _apart(prm.out_q, prm.out_k)
-        _apart(prm.q, prm.out_k)
-        _apart(prm.out_q, prm.k)
         rc = lib().spec_rotate_qk(prm, sh)
     if rc != SPEC_OK:
+        if rc == SPEC_EINVAL:  # say why, where it is one of these
+            if k is not None:
+                _outside(k, out_k, "out_k")
+            if q is not None:
+                _outside(q, out_q, "out_q")
+            _apart(prm.out_q, prm.out_k)
+            _apart(prm.q, prm.out_k)
+            _apart(prm.out_q, prm.k)
         raise SpecError("spec_rotate_qk", rc)
     return out_q, out_k
 
@@ -1058,15 +1059,15 @@ def rotate_store_kv(q, k, v, inv_freq, kv_pool, kv_scales, block_tables, seq_len
             out_q = (torch.empty if window_lens is None else torch.zeros)(q.shape, dtype=k.dtype, device=dev)
         prm = _rotation(q, k, seq_lens if starts is None else starts, inv_freq, interleaved, gain, window_lens, masks,
                         out_q, dev, B, W, D, k.dtype)
-        _outside(q, out_q, "out_q")
         if scratch is None:
             scratch = torch.empty(_scratch_bytes("rotate_store", B, W, H, D, cache.tokens_per_block), dtype=torch.uint8,
                                   device=dev)
         sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
-        _apart(prm.out_q, prm.k, cache.pool, sp)  # k and v are only read: they may be one array
-        _apart(prm.out_q, vp, cache.pool, sp)
         rc = lib().spec_rotate_store_kv(cache, prm, vp, vs, seq, sp, scratch.numel(), sh)
     if rc != SPEC_OK:
+        if rc == SPEC_EINVAL:  # say why, where it is one of these (k and v may be one array: both are only read)
+            _outside(q, out_q, "out_q")
+            _apart(prm.out_q, prm.k, cache.pool, sp, vp if vp != prm.k else 0)
         raise SpecError("spec_rotate_store_kv", rc)
     return out_q
 
@@ -1109,11 +1110,12 @@ def weigh_kv(q, lse, kv_pool, kv_scales, block_tables, seq_lens, *, window_lens=
             scratch = torch.empty(need, dtype=torch.uint8, device=dev)
         op = _at(out, "out", dev, _F32, (B, H, T))
         sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
-        _apart(op, lp, qp, cache.pool, sp)
         prm = WeighParams(_WEIGH_BYTES, qp, qs, SPEC_BF16 if q.dtype is torch.bfloat16 else SPEC_F16, B, W, Hq, seq, win,
                           lp, D ** -0.5 if scale is None else scale, wp, decay, op, T)
         rc = lib().spec_weigh_kv(cache, prm, sp, scratch.numel(), sh)
     if rc != SPEC_OK:
+        if rc == SPEC_EINVAL:  # say why, where it is this
+            _apart(op, lp, qp, cache.pool, sp)
         raise SpecError("spec_weigh_kv", rc)
     return out
 
@@ -1165,15 +1167,11 @@ def evict_kv(weights, kv_pool, kv_scales, block_tables, seq_lens, keep: int, *, 
         if scratch is None:
             scratch = torch.empty(need, dtype=torch.uint8, device=dev)
         sp = _at(scratch, "scratch", dev, torch.uint8, (scratch.numel(),))
-        others = (kp, fp, held, sp, cache.pool, cache.scales, cache.block_tables)
-        _apart(wp, seq, *others)
-        if op != wp or lp != seq:  # op may be wp, and lp seq
-            taken = {x for x in (wp, seq, *others) if x}
-            if op == lp or (op != wp and op in taken) or (lp != seq and lp in taken):
-                raise ValueError("two of the call's arrays are the same memory")
         prm = EvictParams(_EVICT_BYTES, wp, T, B, seq, keep, int(first), int(recent), lp, kp, op, T_out, held, fp)
         rc = lib().spec_evict_kv(cache, prm, sp, scratch.numel(), sh)
     if rc != SPEC_OK:
+        if rc == SPEC_EINVAL:  # say why, where it is this: op may be wp, and lp seq
+            _apart(kp, fp, held, sp, cache.pool, cache.scales, cache.block_tables, *{wp, op}, *{seq, lp})
         raise SpecError("spec_evict_kv", rc)
     return out_lens, out_kept, out_weights, out_free
 

@@ -8,20 +8,21 @@
 
 namespace sv {
 
-using Wide = __int128;  // strides are the caller's: no sum of them overflows
-
 // Runs of `run` bytes, st[d] bytes apart along each of up to three axes.
 struct Span {
-  Wide at = 0, size = 0, run = 0;  // first byte; from there to the last one's end; run 0: no array
+  long at = 0, size = 0, run = 0;  // first byte; from there to the last one's end; run 0: no array
   int dims = 0;
-  Wide n[3], st[3];                // strides above 0, the largest first
+  long n[3], st[3];                // strides above 0, the largest first
   bool repeats = false;            // an axis whose elements are all one
 };
 
-inline Span dense(const void* p, Wide bytes) {
+// No memory is as long as this: a larger stride counts as it, so that no sum overflows.
+constexpr long kFar = 1l << 42;
+
+inline Span dense(const void* p, long bytes) {
   Span s;
   if (p) {
-    s.at = reinterpret_cast<uintptr_t>(p);
+    s.at = (long)reinterpret_cast<uintptr_t>(p);
     s.size = s.run = bytes;
   }
   return s;
@@ -29,11 +30,11 @@ inline Span dense(const void* p, Wide bytes) {
 
 // [n0, n1, n2, run] of `elem` bytes each, strides in elements.
 inline Span strided(const void* p, const int64_t* st, long n0, long n1, long n2, long run, int elem) {
-  Span s = dense(p, (Wide)run * elem);
+  Span s = dense(p, run * elem);
   const long n[3] = {n0, n1, n2};
   for (int d = 0; p && d < 3; ++d) {
     if (n[d] <= 1) continue;
-    const Wide step = (Wide)(st[d] < 0 ? -(Wide)st[d] : (Wide)st[d]) * elem;
+    const long far = kFar / elem, step = (st[d] < 0 ? st[d] < -far ? far : -st[d] : st[d] > far ? far : st[d]) * elem;
     if (step == 0) {
       s.repeats = true;
       continue;
@@ -50,25 +51,25 @@ inline Span strided(const void* p, const int64_t* st, long n0, long n1, long n2,
 
 // A stride and how often it may be taken.
 struct Steps {
-  Wide st, lo, hi;
+  long st, lo, hi;
 };
 
-inline Wide floor_div(Wide a, Wide b) { return a / b - (a % b < 0); }
+inline long floor_div(long a, long b) { return a / b - (a % b < 0); }
 
 // Whether gap + sum of c_i st_i comes into [lo, hi] for whole c_i of their
 // ranges.  The strides fall, so where axes nest (a row's bytes lie inside the
 // stride of the axis above) one or two c_i of each are tried.  `left` bounds the
 // search: what it does not settle counts as reached.
-inline bool reaches(const Steps* t, int n, Wide gap, Wide lo, Wide hi, int* left) {
+inline bool reaches(const Steps* t, int n, long gap, long lo, long hi, int* left) {
   if (--*left < 0) return true;
   if (n == 0) return lo <= gap && gap <= hi;
-  Wide least = 0, most = 0;  // of the smaller strides
+  long least = 0, most = 0;  // of the smaller strides
   for (int i = 1; i < n; ++i) least += t[i].lo * t[i].st, most += t[i].hi * t[i].st;
-  Wide c0 = -floor_div(gap + most - lo, t->st), c1 = floor_div(hi - gap - least, t->st);
+  long c0 = -floor_div(gap + most - lo, t->st), c1 = floor_div(hi - gap - least, t->st);
   if (c0 < t->lo) c0 = t->lo;
   if (c1 > t->hi) c1 = t->hi;
   if (n == 1) return c0 <= c1;
-  for (Wide c = c0; c <= c1; ++c)
+  for (long c = c0; c <= c1; ++c)
     if (reaches(t + 1, n - 1, gap + c * t->st, lo, hi, left)) return true;
   return false;
 }
@@ -81,7 +82,7 @@ inline bool meet(const Span& a, const Span& b) {
   int n = 0;
   // b's runs less a's, equal strides as one
   for (int i = 0, j = 0; i < a.dims || j < b.dims; ++n) {
-    const Wide x = i < a.dims ? a.st[i] : 0, y = j < b.dims ? b.st[j] : 0;
+    const long x = i < a.dims ? a.st[i] : 0, y = j < b.dims ? b.st[j] : 0;
     t[n] = Steps{x > y ? x : y, 0, 0};
     for (; i < a.dims && a.st[i] == t[n].st; ++i) t[n].lo -= a.n[i] - 1;
     for (; j < b.dims && b.st[j] == t[n].st; ++j) t[n].hi += b.n[j] - 1;
@@ -94,9 +95,13 @@ inline bool meet(const Span& a, const Span& b) {
 inline bool folds(const Span& a) {
   if (!a.run) return false;
   if (a.repeats) return true;
+  long inner = a.run;  // bytes that a step along the next axis has to pass
+  int d = a.dims;
+  for (; d > 0 && a.st[d - 1] >= inner; --d) inner += (a.n[d - 1] - 1) * a.st[d - 1];
+  if (d == 0) return false;
   for (int top = 0; top < a.dims; ++top) {  // the first axis along which they differ
     Steps t[3];
-    for (int i = top; i < a.dims; ++i) t[i] = Steps{a.st[i], i == top ? (Wide)1 : 1 - a.n[i], a.n[i] - 1};
+    for (int i = top; i < a.dims; ++i) t[i] = Steps{a.st[i], i == top ? 1l : 1 - a.n[i], a.n[i] - 1};
     int left = kSearch;
     if (reaches(t + top, a.dims - top, 0, 1 - a.run, a.run - 1, &left)) return true;
   }

@@ -349,7 +349,7 @@ int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params* p, void* 
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256 != 0 ||
       scratch_bytes < scratch_bytes_of(p->B, a.c.H, p->keep, a.c.tpb))
     return SPEC_EWORKSPACE;
-  const Wide lens = (Wide)p->B * sizeof(int32_t), per_row = (Wide)p->B * a.c.H * sizeof(float);
+  const long lens = (long)p->B * sizeof(int32_t), per_row = (long)p->B * a.c.H * sizeof(float);
   Arrays x;
   const int old = x.read(dense(p->weights, per_row * p->T)), seq = x.read(dense(p->seq_lens, lens));
   x.read(dense(p->blocks_held, lens));

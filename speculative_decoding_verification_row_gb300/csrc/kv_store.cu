@@ -437,7 +437,7 @@ int spec_rotate_store_kv(const spec_kv_cache* cache, const spec_rotate_params* p
   Arrays x;
   rotate_arrays(p, &x);
   x.read(strided(v, v_strides, a.B, a.W, a.c.H, a.c.D, 2));
-  x.read(dense(seq_lens, (Wide)a.B * sizeof(int32_t)));
+  x.read(dense(seq_lens, (long)a.B * sizeof(int32_t)));
   cache_arrays(a.c, a.B, true, &x);
   x.write(dense(scratch, spec_rotate_store_scratch_size(a.B, a.W, a.c.H, a.c.D, a.c.tpb)));
   if (!x.apart()) return SPEC_EINVAL;

@@ -54,9 +54,9 @@ inline bool kv_strides_ok(const void* p, const int64_t* st) {
 
 // The cache among a call's arrays; `written`: its pool and scales.
 inline void cache_arrays(const KvCache& c, int B, bool written, Arrays* a) {
-  const Span x[2] = {dense(c.pool, (Wide)c.num_blocks * 2 * c.H * c.tpb * c.D),
-                     dense(c.scales, (Wide)c.num_blocks * 2 * c.H * sizeof(float))};
-  a->read(dense(c.tables, (Wide)B * c.max_blocks * sizeof(int32_t)));
+  const Span x[2] = {dense(c.pool, (long)c.num_blocks * 2 * c.H * c.tpb * c.D),
+                     dense(c.scales, (long)c.num_blocks * 2 * c.H * sizeof(float))};
+  a->read(dense(c.tables, (long)B * c.max_blocks * sizeof(int32_t)));
   for (const Span& s : x) written ? a->write(s) : a->read(s);
 }
 

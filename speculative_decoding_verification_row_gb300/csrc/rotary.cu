@@ -69,10 +69,10 @@ void rotate_arrays(const spec_rotate_params* p, Arrays* x) {
   const int B = p->B, W = p->W, D = p->head_dim;
   const int q = x->read(strided(p->q, p->q_strides, B, W, p->q_heads, D, 2));
   const int k = x->read(strided(p->k, p->k_strides, B, W, p->k_heads, D, 2));
-  x->read(dense(p->starts, (Wide)B * sizeof(int32_t)));
-  x->read(dense(p->window_lens, (Wide)B * sizeof(int32_t)));
-  x->read(dense(p->masks, (Wide)B * W * ceil_div(W, 32) * sizeof(int32_t)));
-  x->read(dense(p->inv_freq, (Wide)p->pairs * sizeof(double)));
+  x->read(dense(p->starts, (long)B * sizeof(int32_t)));
+  x->read(dense(p->window_lens, (long)B * sizeof(int32_t)));
+  x->read(dense(p->masks, (long)B * W * ceil_div(W, 32) * sizeof(int32_t)));
+  x->read(dense(p->inv_freq, (long)p->pairs * sizeof(double)));
   x->write(strided(p->out_q, p->out_q_strides, B, W, p->q_heads, D, 2), q);
   x->write(strided(p->out_k, p->out_k_strides, B, W, p->k_heads, D, 2), k);
 }

@@ -275,7 +275,7 @@ int spec_weigh_kv(const spec_kv_cache* cache, const spec_weigh_params* p, void* 
   const size_t need = spec_weigh_scratch_size(p->B, p->W, p->q_heads, a.c.H, a.c.D);
   if (need == 0) return SPEC_EINVAL;
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256 != 0 || scratch_bytes < need) return SPEC_EWORKSPACE;
-  const Wide B = p->B, weights = B * a.c.H * p->T * sizeof(float);
+  const long B = p->B, weights = B * a.c.H * p->T * sizeof(float);
   Arrays x;
   const int old = x.read(dense(p->weights, weights));
   x.read(strided(p->q, p->q_strides, p->B, p->W, p->q_heads, a.c.D, 2));
