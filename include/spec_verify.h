@@ -667,7 +667,7 @@ int spec_adjust_logits(const spec_adjust_params *params, spec_stream_t stream);
  *         the text).  Token i has position starts[b] + i, or with masks
  *         [B, W, ceil(W / 32)] (spec_tree_masks; W <= SPEC_MAX_TREE_NODES)
  *         starts[b] + its depth, one less than the bits of its row (at least 0).
- *   inv_freq [pairs] float64: radians per position; pairs a multiple of 8,
+ *   inv_freq [pairs] float64, finite: radians per position; pairs a multiple of 8,
  *         2 * pairs at most head_dim.  Pair i is
  *         elements (i, i + pairs), or (2 i, 2 i + 1) where interleaved != 0;
  *         elements from 2 * pairs on are copied.

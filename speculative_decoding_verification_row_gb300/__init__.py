@@ -1003,7 +1003,7 @@ def rotate_qk(q, k, starts, inv_freq, *, interleaved=False, gain: float = 1.0, w
 
     starts [B] int32: the position of token 0.  Token i of a chain has
     position starts + i, a tree's node (masks [B, W, ceil(W / 32)], tree_masks)
-    starts + its depth.  inv_freq [pairs] float64 and gain: rotary_frequencies.
+    starts + its depth.  inv_freq [pairs] float64 (finite) and gain: rotary_frequencies.
     The first 2 * pairs elements turn, as pairs (i, i + pairs) or, interleaved,
     (2 i, 2 i + 1).  Rows behind a window's end are left as they are in the
     outputs (zeros in tensors made here)."""
