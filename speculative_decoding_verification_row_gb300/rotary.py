@@ -18,8 +18,12 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str | No
                 is divided by factor, the fastest kept
       "ramp"    pairs that turn at least `fast` times within original_len kept,
                 those that turn at most `slow` times divided by factor, a linear
-                blend over the number of turns between; gain 0.1 ln(factor) + 1
-      "smooth"  the same ends, with gain 1
+                blend over the number of turns between; gain 0.1 ln(factor) + 1.
+                (Model code often blends over the pair's index instead, between the
+                pairs of `fast` and `slow` turns: the ends are the same, the blended
+                pairs' frequencies differ, and a model trained so needs its own.)
+      "smooth"  the same blend with gain 1; models that use it are published with
+                fast=4 and slow=1, which have to be given: `fast` is 32 by default
     """
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError(f"rot_dim must be even and positive, got {rot_dim}")
