@@ -391,7 +391,12 @@ int spec_evict_kv(const spec_kv_cache* cache, const spec_evict_params* p, void* 
   // Whole rows where they give every SM several CTAs, else half of them, or 32
   // bytes (a sector) with larger CTAs.  64 requests, 2048 of up to 8192
   // positions kept: 149 us with 4 CTAs of 256 per SM, 158 with 2 of 512; one
-  // request, 4096 of 16000: 42 with CTAs of 256, 36 with 512.
+  // request, 4096 of 16000: 42 with CTAs of 256, 36 with 512.  The rule's ends, 8 KV
+  // heads, 2048 of 8192 kept, the three forms in this order (heads of 64 have no
+  // second): 1 request 30, -, 20 with heads of 64 and 44, 30, 20 with 128; 16
+  // requests 45, -, 35 and 73, 46, 53; 38 requests 62, -, 69 and 90, 91, 108; 100
+  // requests 167, -, 178 and 245, 244, 281.  Between 16 and 38 requests the best form
+  // is some 10 percent ahead of the rule's.
   const bool wide = a.c.D == 128;
   if (2 * heads >= 8 * 152)
     e = wide ? launch_gather<8, 256>(a, 2 * heads, st) : launch_gather<4, 256>(a, 2 * heads, st);

@@ -356,8 +356,10 @@ int launch_store(StoreArgs& a, cudaStream_t st) {
 // Whether the rotating store is one launch, its units few rows each.  Longer
 // windows are rotated into scratch and stored from there: every KV head's unit
 // makes its rows' angles anew.  64 windows of 1 token, 8 heads of 128: 3.9 us in
-// one launch, 5.9 in two; 256 of 4: 10.4 and 11.4; 64 of 8: 7.9 and 7.8; 16
-// trees of 60: 18.5 and 11.0; 16 prompts of 4096: 621 and 273.
+// one launch, 5.9 in two; 256 of 4: 10.4 and 11.4; 1024 of 4: 34.5 and 34.3; 64 of
+// 8: 7.9 and 7.8; 16 trees of 60: 18.5 and 11.0; 16 prompts of 4096: 621 and 273.
+// With heads of 64: 64 windows of 4 tokens 5.2 and 6.5, of 8 (the last in one launch)
+// 7.2 and 7.1, 256 of 8 10.2 and 11.8, 1024 of 8 35.2 and 33.9.
 bool turn_in_store(int tpb, int W, int D) { return store_vecs(tpb, W, D) <= 32 * kTurnVecs; }
 
 template <class T, int TURN>

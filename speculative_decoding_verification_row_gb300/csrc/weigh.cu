@@ -9,7 +9,9 @@
 // fp16: exact down to 2^-28 of the row's largest.  (Keys as bf16 instead took 128
 // of a tile's some 250 instructions: 78 us for 64 windows of 1 to 4 tokens over
 // 512 to 8192 positions, 32/8 heads of 128.)  A weight is exp of a score less
-// the row's lse, at most 1 but for rounding.
+// the row's lse, at most 1 but for rounding; the tensor cores cut a score's partial
+// sums off, and exp2 is ex2.approx: 8 rows of 4 heads of 128 in fp16 over 700
+// positions are 2.4e-7 off (of the weights' norm), fp32 products and exp 2.0e-7.
 //
 // Bound by the bytes under way: 16 warps an SM with a tile each.  In a graph that
 // case takes 75 us, 4.0 TB/s (0.60 of the measured copy rate); 100 requests of
@@ -240,10 +242,12 @@ cudaError_t launch_weigh_rows(const WeighArgs& a, int dtype, cudaStream_t st) {
 
 namespace {
 
-// Whether this file's kernel serves this many rows per KV head; else
-// weigh_tiles.cu.  16 requests of 8192 positions, 8 KV heads of 128: 50 us here and
-// 90 there with 32 rows; with 64 rows 77 here, if twice the rows are staged (which
-// slows the case above to 80), and 79 there.
+// Whether this file's kernel serves this many rows per KV head, as many as it
+// stages; else weigh_tiles.cu.  8192 positions, 8 KV heads of 64 and of 128, 32 rows:
+// 1 request 10 us here and 11 there, 12 and 12; 16 requests 43 and 70, 49 and 90; 64
+// requests 126 and 251, 165 and 336; with fewer rows, and over 1000 positions, it is
+// ahead by more.  With 64 rows 16 requests (heads of 128) took 77 here, if twice the
+// rows are staged (which slows the case above to 80), and 79 there.
 bool few_rows(int W, int G) { return (long)W * G <= kWRows; }
 
 }  // namespace

@@ -22,8 +22,17 @@
 // equal shares, one per CTA; a unit that falls to several CTAs is joined by a
 // second launch in a fixed order.
 //
+// What is rounded: a score is one chain of D / 16 products, whose partial sums the
+// tensor cores cut off instead of rounding; score - lse and its product with
+// log2(e) round to fp32, exp2 is ex2.approx, and a key's rows are summed in fp32,
+// 64 of a step on their own and then the steps.  A prompt of 1500 tokens, 8/2 heads
+// of 128 in fp16 is 2.2e-7 off (of the weights' norm) and 0.7e-7 with scores that
+// are exact, where products, exp and sums in fp32 give 0.6e-7 and 0.5e-7: the chain
+// is what is left.  Two chains, as in weigh.cu, would take four buffers of scores;
+// tensor memory has two beside the keys.  Weights only rank positions.
+//
 // In a graph: 2 prompt chunks of 2049 tokens over 0 and 4500, 16/4 heads of 64,
-// 80 us; 32/8 heads of 128, 163 us (675 TFLOP/s, 0.35 of the measured dense
+// 80 us; 32/8 heads of 128, 163 us (675 TFLOP/s, 0.36 of the measured dense
 // rate); a prompt of 4096 109 us.  A step takes some 1600 clocks, its exponentials
 // 512 to 1024, its products 512: the hops scores -> sums -> next products.
 #include "tcgen05.cuh"
