@@ -728,8 +728,8 @@ size_t spec_rotate_store_scratch_size(int B, int W, int kv_heads, int head_dim, 
  * Positions in a block whose id lies outside [0, num_blocks) read NaN; for a
  * request with seq_lens < 0, w_b outside [0, W] or a window past max_blocks
  * blocks nothing is written.  Scores and sums are held in fp32 (a score is off by
- * at most D * 2^-23 of the sum of its products' magnitudes), exp is good to 2^-21;
- * q's elements count to at least 2^-28 of their row's largest.
+ * at most D * 2^-23 of the sum of its products' magnitudes; exp(x) by 2^-22 +
+ * |x| 2^-23 of itself); q's elements count to at least 2^-28 of their row's largest.
  *   scratch: spec_weigh_scratch_size(...) bytes, 256-byte aligned, with the
  *         rules of spec_attend_kv's (which may serve where it is large enough).
  * Limits: as spec_attend_kv's. */
