@@ -12,7 +12,8 @@
 // for 64 x 8 rows of 128256; counting before copying took 90.)
 //
 // In a graph: 64 x 8 rows of 128256 (bf16) with 4096 tokens and 16 biases each
-// 58 us, 4.5 TB/s (0.66 of the measured copy rate); 16 trees of 60 rows of
+// 58 us, 4.5 TB/s (0.66 of the measured copy rate), with 60000 tokens each, which
+// every segment reads, 197; 16 trees of 60 rows of
 // 151936 under 40 grammars 122 us; a grammar in place on 256 x 4 rows of 129280
 // 60 us; one row of 32000 (fp32) 5.6 us, latency.
 #include <cuda_bf16.h>
